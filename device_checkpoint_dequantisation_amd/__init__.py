@@ -603,3 +603,16 @@ from .shards import (ShardedStateDict, ShardError, index_shards, load_checkpoint
 __all__ += ["StreamStateDict", "PrefixViewStateDict", "FilterViewStateDict", "RenameViewStateDict", "RamCache",
             "LazyModuleLoader", "DiskRef", "OutputMeta", "ShardedStateDict", "ShardError", "index_shards",
             "load_checkpoint", "shard_files"]
+
+# Operators on quantised weights (ops.py), imported on first use: they need torch, which the rest of the package imports
+# only where it allocates.
+_OPS = ("QuantizedActivation", "linear", "quantize_activation", "rms_norm")
+__all__ += list(_OPS)
+
+
+def __getattr__(name):
+    if name in _OPS:
+        from . import ops
+        value = globals()[name] = getattr(ops, name)
+        return value
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

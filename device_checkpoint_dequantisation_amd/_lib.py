@@ -89,6 +89,27 @@ class StreamStats(C.Structure):
 assert C.sizeof(StreamRange) == 32 and C.sizeof(StreamStep) == 40 and C.sizeof(StreamStats) == 40
 
 
+class LinearArgs(C.Structure):
+    _fields_ = ([(f, C.c_void_p) for f in ("x", "x_scale", "w", "w_scale", "w_scale2", "bias", "residual", "out",
+                                           "workspace")] +
+                [(f, C.c_uint64) for f in ("workspace_bytes", "m", "n", "k", "x_pitch", "residual_pitch", "out_pitch")] +
+                [(f, C.c_uint32) for f in ("x_type", "w_kind", "activation", "bias_type", "residual_type", "out_type")])
+
+
+class EncodeArgs(C.Structure):
+    _fields_ = ([(f, C.c_void_p) for f in ("x", "gate", "data", "scale")] +
+                [(f, C.c_uint64) for f in ("m", "d", "x_pitch", "gate_pitch")] +
+                [(f, C.c_uint32) for f in ("x_type", "kind")])
+
+
+class RmsNormArgs(C.Structure):
+    _fields_ = ([(f, C.c_void_p) for f in ("x", "residual", "weight", "h_out", "out", "scale")] +
+                [(f, C.c_uint64) for f in ("m", "d", "x_pitch", "residual_pitch")] + [("eps", C.c_double)] +
+                [(f, C.c_uint32) for f in ("x_type", "weight_type", "out_type", "kind")])
+
+
+assert C.sizeof(LinearArgs) == 152 and C.sizeof(EncodeArgs) == 72 and C.sizeof(RmsNormArgs) == 104
+
 # name -> (restype, argtypes); the full list of exported symbols the header declares.
 SIGNATURES = {
     "st_last_error": (C.c_char_p, []),
@@ -124,6 +145,10 @@ SIGNATURES = {
                                     C.c_void_p]),
     "st_materialize_noalloc": (C.c_int, [C.c_void_p, C.c_void_p, C.c_size_t, C.c_size_t, C.c_void_p, C.c_size_t,
                                          C.c_uint32, C.c_uint32, C.c_void_p]),
+    "st_linear_workspace_bytes": (C.c_int, [C.c_void_p, C.POINTER(C.c_uint64)]),
+    "st_linear": (C.c_int, [C.c_void_p, C.c_void_p]),
+    "st_encode": (C.c_int, [C.c_void_p, C.c_void_p]),
+    "st_rms_norm": (C.c_int, [C.c_void_p, C.c_void_p]),
     "st_index_out_dtype": (C.c_uint32, [C.c_void_p]),
     "st_stream_plan_build": (C.c_int, [C.c_void_p, C.c_uint64, C.POINTER(C.c_void_p)]),
     "st_stream_plan_select": (C.c_int, [C.c_void_p, C.POINTER(C.c_uint32), C.c_size_t, C.c_uint64, C.c_uint32,

@@ -5,6 +5,7 @@ import os
 import shutil
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -13,6 +14,10 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libstmat.so")
 ARCH = "gfx950"
+# sources that call the HIP runtime or hold kernels, and host-only sources
+HIP_SOURCES = ("linear_bf16.hip", "linear_f16.hip", "linear_fp8.hip", "materialize.hip", "encode.hip", "linear.cpp",
+               "stage.cpp")
+HOST_SOURCES = ("index.cpp", "stream_plan.cpp")
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 COMMON = ["-std=c++17", "-fPIC", "-Wall", "-Wno-unused-function", f"-I{INCLUDE}", f"-I{CSRC}"]
@@ -38,18 +43,20 @@ def build(verbose: bool = False, extra_device_flags=(), out: str = LIB, defines=
     "STK_WORDS_FP8=4") override the compile-time work-unit geometry in every source."""
     os.makedirs(build_dir, exist_ok=True)
     dflags = [f"-D{d}" for d in defines]
-    objs = []
-    # host-only sources
-    for src in ("index.cpp", "stream_plan.cpp"):
+
+    def compile_one(src):
         o = os.path.join(build_dir, src + ".o")
-        _run(["g++", "-O2", *COMMON, *dflags, "-c", os.path.join(CSRC, src), "-o", o], verbose)
-        objs.append(o)
-    # sources that call the HIP runtime or hold kernels
-    for src in ("stage.cpp", "materialize.hip"):
-        o = os.path.join(build_dir, src + ".o")
-        lang = ["-x", "hip"] if src.endswith(".hip") else []
-        _run([HIPCC, *lang, *COMMON, *DEVICE, *dflags, *extra_device_flags, "-c", os.path.join(CSRC, src), "-o", o], verbose)
-        objs.append(o)
+        if src in HOST_SOURCES:
+            _run(["g++", "-O2", *COMMON, *dflags, "-c", os.path.join(CSRC, src), "-o", o], verbose)
+        else:
+            lang = ["-x", "hip"] if src.endswith(".hip") else []
+            _run([HIPCC, *lang, *COMMON, *DEVICE, *dflags, *extra_device_flags, "-c", os.path.join(CSRC, src), "-o", o],
+                 verbose)
+        return o
+
+    # the longest compilations first, a few at a time
+    with ThreadPoolExecutor(max_workers=min(6, os.cpu_count() or 1)) as pool:
+        objs = list(pool.map(compile_one, HIP_SOURCES + HOST_SOURCES))
     tmp = out + ".tmp"
     _run([HIPCC, "-shared", "-fPIC", f"--offload-arch={ARCH}", *objs, "-o", tmp], verbose)
     os.replace(tmp, out)

@@ -1,0 +1,129 @@
+// Host side of st_linear: argument checks, the cut into workgroups, the launch.
+#include "linear.h"
+
+#include <cstring>
+
+namespace {
+
+using namespace st_linear_impl;
+
+Plan plan_of(const st_linear_args& g) {
+    Plan p;
+    const bool q = is_q(g.x_type), fp4 = is_fp4(g.w_kind);
+    const uint64_t xb = g.x_pitch * (q ? 1 : 2), wb = fp4 ? g.k / 2 : g.k;
+    auto al = [](const void* v, uint64_t n) { return reinterpret_cast<uintptr_t>(v) % n == 0; };
+    p.direct = al(g.x, 16) && al(g.w, 16) && (g.m <= 1 || xb % 16 == 0) && wb % 16 == 0;
+    const uint64_t ks = q ? 128 : 64;
+    if (g.w_kind == ST_KIND_NVFP4) p.direct = p.direct && al(g.w_scale, 4) && g.k % 64 == 0;
+    if (is_mx(g.w_kind)) p.direct = p.direct && al(g.w_scale, ks / 32) && g.k % ks == 0;
+    if (g.x_type == ST_X_MXFP8) p.direct = p.direct && al(g.x_scale, 4);
+    p.bm = g.m <= 64 ? 64 : 128;
+    p.bn = p.bm;
+    p.f8 = q && p.bm > 64 && g.out_type != ST_OUT_F32;
+    const uint64_t tiles = ((g.m + p.bm - 1) / p.bm) * ((g.n + p.bn - 1) / p.bn), all = (g.k + ks - 1) / ks;
+    // Too few tiles to fill 256 CUs: split K, in whole groups of 128, while each part keeps 8 steps
+    uint64_t s = 1;
+    while (tiles * s < 512 && all / (2 * s) >= 8) s *= 2;
+    const uint64_t gran = 128 / ks;
+    p.steps = uint32_t((all + s - 1) / s);
+    p.steps = uint32_t((p.steps + gran - 1) / gran * gran);
+    if (p.steps == 0) p.steps = 1;
+    p.splits = uint32_t((all + p.steps - 1) / p.steps);
+    if (p.splits < 1) p.splits = 1;
+    p.part_bytes = p.splits > 1 ? uint64_t(p.splits) * g.m * g.n * 4 : 0;
+    return p;
+}
+
+static_assert(sizeof(st_linear_args) == 152, "the ctypes declaration has this size");
+
+const char* kWho = "st_linear";
+
+st_status check_args(const st_linear_args* g) {
+    if (!g) return st_fail(ST_E_ARG, "%s: null arguments", kWho);
+    if (g->x_type > ST_X_MXFP8) return st_fail(ST_E_ARG, "%s: unknown x type %u", kWho, g->x_type);
+    if (g->w_kind < ST_KIND_FP8_TENSOR || g->w_kind > ST_KIND_MXFP4)
+        return st_fail(ST_E_ARG, "%s: weight kind %u is not a quantised kind", kWho, g->w_kind);
+    if (g->activation > ST_ACT_GELU_TANH) return st_fail(ST_E_ARG, "%s: unknown activation %u", kWho, g->activation);
+    if (g->bias_type > ST_OUT_F32 || g->residual_type > ST_OUT_F32 || g->out_type > ST_OUT_F32)
+        return st_fail(ST_E_ARG, "%s: unknown bias, residual or output type", kWho);
+    const bool pair = !is_q(g->x_type) || (g->x_type == ST_X_FP8_ROW && g->w_kind == ST_KIND_FP8_TENSOR) ||
+                      (g->x_type == ST_X_FP8_GROUP128 && g->w_kind == ST_KIND_FP8_BLOCK128) ||
+                      (g->x_type == ST_X_MXFP8 && is_mx(g->w_kind));
+    if (!pair) return st_fail(ST_E_ARG, "%s: x type %u does not go with weight kind %u", kWho, g->x_type, g->w_kind);
+    const uint64_t lim = uint64_t(1) << 31;
+    if (g->m >= lim || g->n >= lim || g->k >= lim)
+        return st_fail(ST_E_SHAPE, "%s: m %llu, n %llu, k %llu: each must be below 2^31", kWho, (unsigned long long)g->m,
+                       (unsigned long long)g->n, (unsigned long long)g->k);
+    if (g->w_kind == ST_KIND_NVFP4 && g->k % 16)
+        return st_fail(ST_E_SHAPE, "%s: NVFP4 k %llu is not a multiple of 16", kWho, (unsigned long long)g->k);
+    if (is_mx(g->w_kind) && g->k % 32)
+        return st_fail(ST_E_SHAPE, "%s: MX k %llu is not a multiple of 32", kWho, (unsigned long long)g->k);
+    if (g->m == 0 || g->n == 0) return ST_OK;
+    if (!g->out) return st_fail(ST_E_ARG, "%s: null out", kWho);
+    if ((g->m > 1 && g->out_pitch < g->n) || (g->m > 1 && g->x_pitch < g->k && g->x_pitch != 0) ||
+        (g->residual && g->m > 1 && g->residual_pitch < g->n && g->residual_pitch != 0))
+        return st_fail(ST_E_SHAPE, "%s: a row pitch is shorter than its row", kWho);
+    if (g->k && (!g->x || !g->w)) return st_fail(ST_E_ARG, "%s: null x or weight", kWho);
+    // (the tensor-wide and per-row scales are read in the epilogue, whatever k is)
+    if (!g->x_scale && (g->x_type == ST_X_FP8_ROW || (g->k && is_q(g->x_type)))) return st_fail(ST_E_ARG, "%s: null x scale", kWho);
+    if (!g->w_scale && (g->w_kind == ST_KIND_FP8_TENSOR || g->k)) return st_fail(ST_E_ARG, "%s: null weight scale", kWho);
+    if (!g->w_scale2 && g->w_kind == ST_KIND_NVFP4) return st_fail(ST_E_ARG, "%s: null global scale", kWho);
+    auto off = [](const void* v, uint64_t n) { return v && reinterpret_cast<uintptr_t>(v) % n != 0; };
+    auto size = [](uint32_t t) { return t == ST_OUT_F32 ? 4u : 2u; };
+    if (off(g->out, size(g->out_type)) || off(g->bias, size(g->bias_type)) || off(g->residual, size(g->residual_type)) ||
+        (!is_q(g->x_type) && off(g->x, 2)))
+        return st_fail(ST_E_ARG, "%s: a pointer is not aligned to its element type", kWho);
+    if ((g->w_kind <= ST_KIND_FP8_BLOCK128 && off(g->w_scale, 4)) || off(g->w_scale2, 4) ||
+        ((g->x_type == ST_X_FP8_ROW || g->x_type == ST_X_FP8_GROUP128) && off(g->x_scale, 4)))
+        return st_fail(ST_E_ARG, "%s: an fp32 scale is not 4-byte aligned", kWho);
+    return ST_OK;
+}
+
+}  // namespace
+
+extern "C" st_status st_linear_workspace_bytes(const st_linear_args* args, uint64_t* bytes) {
+    if (!bytes) return st_fail(ST_E_ARG, "st_linear_workspace_bytes: null bytes");
+    *bytes = 0;
+    const st_status r = check_args(args);
+    if (r != ST_OK) return r;
+    if (args->m && args->n) *bytes = plan_of(*args).part_bytes;
+    return ST_OK;
+}
+
+extern "C" st_status st_linear(const st_linear_args* args, void* stream) {
+    const st_status r = check_args(args);
+    if (r != ST_OK) return r;
+    const st_linear_args& g = *args;
+    if (g.m == 0 || g.n == 0) return ST_OK;
+    const Plan p = plan_of(g);
+    if (p.part_bytes) {
+        if (!g.workspace || g.workspace_bytes < p.part_bytes)
+            return st_fail(ST_E_ARG, "%s: %llu bytes of workspace, %llu are needed", kWho,
+                           (unsigned long long)(g.workspace ? g.workspace_bytes : 0), (unsigned long long)p.part_bytes);
+        if (reinterpret_cast<uintptr_t>(g.workspace) % 16) return st_fail(ST_E_ARG, "%s: workspace is not 16-byte aligned", kWho);
+    }
+    Args a;
+    memset(&a, 0, sizeof a);
+    auto b = [](const void* v) { return static_cast<const uint8_t*>(v); };
+    a.x = b(g.x); a.xs = b(g.x_scale); a.w = b(g.w); a.ws = b(g.w_scale); a.ws2 = b(g.w_scale2);
+    a.bias = b(g.bias); a.res = b(g.residual);
+    a.out = static_cast<uint8_t*>(g.out);
+    a.part = p.part_bytes ? static_cast<float*>(g.workspace) : nullptr;
+    a.x_pitch = g.x_pitch; a.res_pitch = g.residual_pitch; a.out_pitch = g.out_pitch;
+    a.m = uint32_t(g.m); a.n = uint32_t(g.n); a.k = uint32_t(g.k);
+    a.act = g.activation; a.bias_type = g.bias_type; a.res_type = g.residual_type; a.out_type = g.out_type;
+    a.splits = p.splits; a.steps = p.steps;
+    a.tiles_m = uint32_t((g.m + p.bm - 1) / p.bm); a.tiles_n = uint32_t((g.n + p.bn - 1) / p.bn);
+    if (uint64_t(a.tiles_m) * a.tiles_n > 0x7FFFFFFFull) return st_fail(ST_E_SHAPE, "%s: too many tiles", kWho);
+    auto quad = [](const void* v, uint32_t type, uint64_t pitch, uint64_t rows) {
+        const uint64_t e = type == ST_OUT_F32 ? 4 : 2;
+        return reinterpret_cast<uintptr_t>(v) % (4 * e) == 0 && (rows <= 1 || pitch % 4 == 0);
+    };
+    a.vec = quad(g.out, g.out_type, g.out_pitch, g.m) &&
+            (!g.residual || quad(g.residual, g.residual_type, g.residual_pitch, g.m));
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    (is_q(g.x_type) ? launch_fp8 : g.x_type == ST_X_F16 ? launch_f16 : launch_bf16)(a, p, g.w_kind, s);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return st_fail(ST_E_HIP, "%s: launch failed: %s", kWho, hipGetErrorString(e));
+    return ST_OK;
+}

@@ -1,0 +1,538 @@
+// Matrix product over a quantised weight, with bias, activation and residual in its epilogue:
+//   y[m, n] = act(sum_k x[m, k] w[n, k] + b[n]) + r[m, n]
+// for a weight as the checkpoint stores it (FP8_TENSOR, FP8_BLOCK128, NVFP4, MXFP8, MXFP4) and rows x in
+// bf16 or fp16, or in e4m3 with scales (FP8_ROW, FP8_GROUP128, MXFP8).
+//
+// Arithmetic.  w[n, k] is the code's value times its scales, not rounded to bf16 as a decoded weight is.
+// Every product is exact and every sum is kept in fp32:
+//  * dense x: e4m3 and e2m1 codes, an e2m1 code times its e4m3 block scale (at most 6 significant
+//    bits) and a code times a power of two are exact in bf16; the first three are exact in fp16 too, so the
+//    weight enters the bf16 or fp16 matrix instructions without rounding.  fp16 rows against an MX
+//    weight, whose scales reach beyond fp16, are split into two bf16 terms (x = hi + lo, exact).
+//  * e4m3 x: widened to bf16 (times its E8M0 scale, exact) like the weight; or, for large products with 16-bit outputs,
+//    the f8f6f4 matrix instructions, which run at twice the rate and apply the E8M0 scales of both sides
+//    themselves.  Of 16 products that lie in one lane these cut what is below 2^-13 of the largest (measured: such
+//    a product next to a larger one is lost; across lanes the sum is whole): at most 15 * 2^-13 of that largest product
+//    per 16, in practice 7e-6 of y, far below the 2^-9 and 2^-12 of a 16-bit result's own rounding.  fp32 outputs keep the exact form.
+//  * fp32 scales (per tensor, per row, per 128 x 128 block, NVFP4's global one) multiply fp32 sums.
+// The result is rounded once, to the output type.
+//
+// The weight is the A operand of the matrix instructions (its rows are the D rows), so a lane holds four
+// consecutive output columns of one row of y and stores them together.
+//
+// Three kernels:
+//  * linear_few: m <= 16.  Bound by the weight's bytes: each wavefront streams its part of K for a few
+//    16-row groups of the weight straight into registers, the wavefronts of a workgroup join in LDS.
+//  * linear_tile: tiles of y staged through LDS, double-buffered, one barrier per step of K.  x and the weight are
+//    staged as stored and the weight is decoded on its way from LDS to the matrix instructions.
+//  * linear_join: adds the fp32 partial results where K was split over workgroups, in a fixed order.
+#pragma once
+
+#include "linear.h"
+#include "st_device.h"
+
+namespace st_linear_impl {
+namespace {
+
+using namespace st_dev;
+
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef u32x4 u32x4_any __attribute__((aligned(1)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+
+
+// ------------------------------------------------------------------------- epilogue
+
+__device__ __forceinline__ float activate(float v, uint32_t act) {
+    switch (act) {
+        case ST_ACT_RELU: return v != v ? v : fmaxf(v, 0.0f);
+        case ST_ACT_SILU: return silu(v);
+        case ST_ACT_GELU: return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
+        // (1 + tanh u) / 2 is the logistic function of 2u
+        case ST_ACT_GELU_TANH: {
+            const float u = 1.5957691216057308f * v * (1.0f + 0.044715f * v * v);
+            return v / (1.0f + expf(-u));
+        }
+        default: return v;
+    }
+}
+
+// Columns n..n+3 of row m from their sums (the kind's tensor-wide scales not yet applied).
+template <int X, int WK>
+__device__ __forceinline__ void finish(const Args& a, uint32_t m, uint32_t n, f32x4 v) {
+    if (m >= a.m || n >= a.n) return;
+    float s = 1.0f;
+    if constexpr (WK == ST_KIND_FP8_TENSOR) s = *reinterpret_cast<const float*>(a.ws);
+    if constexpr (WK == ST_KIND_NVFP4) s = *reinterpret_cast<const float*>(a.ws2);
+    const uint32_t cnt = a.n - n < 4 ? a.n - n : 4;
+    float y[4];
+#pragma unroll
+    for (uint32_t i = 0; i < 4; ++i) {
+        y[i] = v[i];
+        if constexpr (WK == ST_KIND_FP8_TENSOR || WK == ST_KIND_NVFP4) y[i] *= s;
+        if constexpr (X == ST_X_FP8_ROW) y[i] *= reinterpret_cast<const float*>(a.xs)[m];
+    }
+    if (a.bias) {
+#pragma unroll
+        for (uint32_t i = 0; i < 4; ++i)
+            if (i < cnt) y[i] += load_as_f32(a.bias, a.bias_type, n + i);
+    }
+#pragma unroll
+    for (uint32_t i = 0; i < 4; ++i) y[i] = activate(y[i], a.act);
+    const uint64_t o = uint64_t(m) * a.out_pitch + n;
+    if (a.res) {
+        const uint64_t r = uint64_t(m) * a.res_pitch + n;
+        if (a.vec && cnt == 4) {
+            float t[4];
+            load4_as_f32(a.res, a.res_type, r, t);
+#pragma unroll
+            for (uint32_t i = 0; i < 4; ++i) y[i] += t[i];
+        } else {
+            for (uint32_t i = 0; i < cnt; ++i) y[i] += load_as_f32(a.res, a.res_type, r + i);
+        }
+    }
+    if (a.vec && cnt == 4) store4(a.out, a.out_type, o, y);
+    else
+        for (uint32_t i = 0; i < cnt; ++i) store_as(a.out, a.out_type, o + i, y[i]);
+}
+
+// A workgroup's result for columns n..n+3 of row m: the output, or this split's partial sums.
+template <int X, int WK>
+__device__ __forceinline__ void emit(const Args& a, uint32_t split, uint32_t m, uint32_t n, f32x4 v) {
+    if (!a.part) return finish<X, WK>(a, m, n, v);
+    if (m >= a.m || n >= a.n) return;
+    float* p = a.part + (uint64_t(split) * a.m + m) * a.n + n;
+    if ((a.n & 3) == 0) *reinterpret_cast<f32x4*>(p) = v;
+    else
+        for (uint32_t i = 0; i < 4 && n + i < a.n; ++i) p[i] = v[i];
+}
+
+template <int X, int WK>
+__global__ __launch_bounds__(256) void linear_join(Args a) {
+    const uint32_t q = (a.n + 3) / 4;
+    const uint64_t i = uint64_t(blockIdx.x) * 256 + threadIdx.x;
+    if (i >= uint64_t(q) * a.m) return;
+    const uint32_t m = uint32_t(i / q), n = uint32_t(i % q) * 4;
+    f32x4 v = {0, 0, 0, 0};
+    for (uint32_t s = 0; s < a.splits; ++s) {
+        const float* p = a.part + (uint64_t(s) * a.m + m) * a.n + n;
+        if ((a.n & 3) == 0) v += *reinterpret_cast<const f32x4*>(p);
+        else
+            for (uint32_t j = 0; j < 4 && n + j < a.n; ++j) v[j] += p[j];
+    }
+    finish<X, WK>(a, m, n, v);
+}
+
+// ------------------------------------------------------------------------- weight codes to matrix operands
+
+// Eight codes to eight bf16 or fp16 values times 2^e (s = 2^e; NVFP4: times the e4m3 block scale's value s).
+// Exact in every case (see the top of the file).  lo and hi: the eight e4m3 codes; fp4: lo alone.
+template <bool F16, int WK>
+__device__ __forceinline__ u32x4 codes8(uint32_t lo, uint32_t hi, float s) {
+    u32x4 r;
+    if constexpr (!is_fp4(WK)) {
+        if constexpr (F16) {
+            r[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, s, false));
+            r[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, s, true));
+            r[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, s, false));
+            r[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, s, true));
+        } else {
+            r[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, s, false));
+            r[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, s, true));
+            r[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, s, false));
+            r[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, s, true));
+        }
+    } else if constexpr (WK == ST_KIND_MXFP4) {
+        r[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(lo, s, 0));
+        r[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(lo, s, 1));
+        r[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(lo, s, 2));
+        r[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(lo, s, 3));
+    } else if constexpr (F16) {
+        // 2^-10 <= |e2m1 * scale| <= 2688 with at most 6 bits: exact in fp16
+        const f16x2 b = {_Float16(s), _Float16(s)};
+        r[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(lo, 1.0f, 0) * b);
+        r[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(lo, 1.0f, 1) * b);
+        r[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(lo, 1.0f, 2) * b);
+        r[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(lo, 1.0f, 3) * b);
+    } else {
+        f32x2 p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(lo, 1.0f, 0);
+        r[0] = cvt_bf16x2(p.x * s, p.y * s);
+        p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(lo, 1.0f, 1);
+        r[1] = cvt_bf16x2(p.x * s, p.y * s);
+        p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(lo, 1.0f, 2);
+        r[2] = cvt_bf16x2(p.x * s, p.y * s);
+        p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(lo, 1.0f, 3);
+        r[3] = cvt_bf16x2(p.x * s, p.y * s);
+    }
+    return r;
+}
+
+// The fp32 a scale code stands for: e4m3 (NVFP4), or E8M0 as the conversions above take it (the exponent
+// field c: 2^(c - 127), 0 read as 2^-127 and 255 as NaN, checked on the device for every code).
+template <int WK>
+__device__ __forceinline__ float scale_of(uint32_t code) {
+    if constexpr (WK == ST_KIND_NVFP4) return __builtin_amdgcn_cvt_pk_f32_fp8(code, false)[0];
+    else if constexpr (is_mx(WK)) return as_f32(code << 23);
+    else return 1.0f;
+}
+
+// 16x16x32 product of eight values per lane of each side.
+template <bool F16>
+__device__ __forceinline__ f32x4 mfma32(u32x4 a, u32x4 b, f32x4 c) {
+    if constexpr (F16)
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+// fp16 pairs as two bf16 terms, x = hi + lo: hi has the upper 8 of x's 11 significant bits, lo the rest.
+__device__ __forceinline__ void split_f16(u32x4 x, u32x4& hi, u32x4& lo) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const f16x2 h = __builtin_bit_cast(f16x2, uint32_t(x[i]));
+        const float a = float(h.x), b = float(h.y);
+        const uint32_t t = cvt_bf16x2(a, b);
+        hi[i] = t;
+        // infinities and NaN stay whole in hi
+        const float la = a - as_f32(t << 16), lb = b - as_f32(t & 0xFFFF0000u);
+        lo[i] = cvt_bf16x2(la == la ? la : 0.0f, lb == lb ? lb : 0.0f);
+    }
+}
+
+// How dense x meets the weight: fp16 operands, or bf16 with fp16 x split in two terms.
+template <int X, int WK>
+struct Dense {
+    static constexpr bool F16 = X == ST_X_F16 && !is_mx(WK), SPLIT = X == ST_X_F16 && is_mx(WK);
+};
+
+// ------------------------------------------------------------------------- tiles
+
+// A tile of BM x BN outputs by WAVES_M x WAVES_N wavefronts; a step of K is 128 bytes of x: 64 elements, or 128
+// of e4m3.  LDS holds rows of 16-byte chunks; chunk c of row r sits at c ^ swizzle(r), so that eight lanes
+// reading the same chunk of eight consecutive rows touch all 32 banks once.
+// F8 (8-bit x): the f8f6f4 matrix instructions, at twice the bf16 rate; otherwise both sides are widened to bf16.
+template <int X_, int WK_, int BM_, int BN_, int WAVES_M_, int WAVES_N_, bool F8_>
+struct Tile {
+    static constexpr int X = X_, WK = WK_, BM = BM_, BN = BN_, WAVES_M = WAVES_M_, WAVES_N = WAVES_N_;
+    static constexpr bool Q = is_q(X), FP4 = is_fp4(WK), F8 = F8_;
+    static constexpr int THREADS = 64 * WAVES_M * WAVES_N;
+    static constexpr int KS = Q ? 128 : 64;
+    static constexpr int XB = 128, WB = KS / (FP4 ? 2 : 1);       // bytes of a row per step
+    static constexpr int XC = XB / 16, WC = WB / 16;               // chunks of a row
+    static constexpr int MT = BM / WAVES_M / 16, NT = BN / WAVES_N / 16;
+    // scale bytes of a row per step (0: none) and elements per scale
+    static constexpr int WSB = WK == ST_KIND_NVFP4 ? KS / 16 : is_mx(WK) ? KS / 32 : 0;
+    static constexpr int XSB = X == ST_X_MXFP8 || X == ST_X_FP8_GROUP128 ? 4 : 0;
+    static constexpr bool GROUPED = WK == ST_KIND_FP8_BLOCK128;    // sums scaled per 128 of K
+    static constexpr int STAGE = BM * XB + BN * WB + (XSB ? BM * 4 : 0) + (WSB ? BN * 4 : 0);
+    static constexpr int X_PER = BM * XC / THREADS, W_PER = (BN * WC + THREADS - 1) / THREADS;
+    static_assert(BM * XC % THREADS == 0 && BM <= THREADS && BN <= THREADS, "tile");
+    static_assert(!GROUPED || BN / WAVES_N <= 64, "a wavefront's columns lie in one scale block");
+    static __device__ __forceinline__ int x_at(int r, int c) { return r * XB + ((c ^ (r & 7)) << 4); }
+    static __device__ __forceinline__ int w_at(int r, int c) {
+        return r * WB + ((c ^ ((r / (8 / WC)) & (WC - 1))) << 4);
+    }
+};
+
+// 16 bytes at p of which `avail` lie in the row, the others 0.
+__device__ __forceinline__ u32x4 load_chunk(const uint8_t* p, int64_t avail) {
+    if (avail >= 16) return *reinterpret_cast<const u32x4_any*>(p);
+    u32x4 v = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        if (i < avail) v[i >> 2] |= uint32_t(p[i]) << (8 * (i & 3));
+    return v;
+}
+__device__ __forceinline__ uint32_t load_codes(const uint8_t* p, int64_t avail, int want) {
+    uint32_t v = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (i < want && i < avail) v |= uint32_t(p[i]) << (8 * i);
+    return v;
+}
+
+// DIRECT: every row starts on 16 bytes (scale codes on a step's bytes), so whole steps go from global memory
+// straight into LDS; otherwise, and for the last step of a K that is no whole number of steps, chunks pass
+// through registers, with zeros behind the row's end.
+template <class T, bool DIRECT>
+__global__ __launch_bounds__(T::THREADS) void linear_tile(Args a) {
+    constexpr int X = T::X, WK = T::WK, MT = T::MT, NT = T::NT;
+    __shared__ __align__(128) uint8_t lds[2][T::STAGE];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int row = lane & 15, q = lane >> 4;
+    const int wm = wave / T::WAVES_N, wn = wave % T::WAVES_N;
+
+    // Workgroup b runs on XCD b mod 8: renumber so that each XCD takes consecutive tiles, and order tiles in
+    // bands of 8 row tiles so that neighbours share rows of both sides in that XCD's L2.
+    const uint32_t total = a.tiles_m * a.tiles_n;
+    uint32_t b = blockIdx.x;
+    {
+        const uint32_t per = total / 8, extra = total % 8, xcd = b % 8, at = b / 8;
+        b = xcd * per + (xcd < extra ? xcd : extra) + at;
+    }
+    const uint32_t band = b / (8 * a.tiles_n), in = b - band * 8 * a.tiles_n;
+    const uint32_t rows = a.tiles_m - band * 8 < 8 ? a.tiles_m - band * 8 : 8;
+    const uint32_t m0 = (band * 8 + in % rows) * T::BM, n0 = in / rows * T::BN;
+    const uint32_t split = blockIdx.y;
+    const uint32_t all = (a.k + T::KS - 1) / T::KS;
+    const uint32_t first = split * a.steps, last = first + a.steps < all ? first + a.steps : all;
+
+    const uint64_t x_row = a.x_pitch * (T::Q ? 1 : 2), w_row = T::FP4 ? a.k / 2 : a.k;
+    const uint64_t x_len = uint64_t(a.k) * (T::Q ? 1 : 2);
+    const uint64_t ws_row = a.k / (WK == ST_KIND_NVFP4 ? 16 : 32);
+    const uint32_t groups = (a.k + 127) / 128;
+    // rows past the last are read as the last one; nothing of them is stored
+    auto xr = [&](uint32_t r) { return m0 + r < a.m ? m0 + r : a.m - 1; };
+    auto wr = [&](uint32_t r) { return n0 + r < a.n ? n0 + r : a.n - 1; };
+
+    u32x4 rx[T::X_PER], rw[T::W_PER];      // chunks on their way through registers
+    uint32_t rxs = 0, rws = 0;
+    bool in_regs = false;
+
+    auto issue = [&](uint32_t step, int buf) {
+        const uint64_t kb = uint64_t(step) * T::XB, wb = uint64_t(step) * T::WB;
+        uint8_t* sx = lds[buf];
+        uint8_t* sw = lds[buf] + T::BM * T::XB;
+        in_regs = !DIRECT || uint64_t(step + 1) * T::KS > a.k;
+        if (!in_regs) {
+#pragma unroll
+            for (int i = 0; i < T::X_PER; ++i) {
+                const int s = i * T::THREADS + tid, r = s / T::XC, c = (s % T::XC) ^ (r & 7);
+                __builtin_amdgcn_global_load_lds(
+                    (const __attribute__((address_space(1))) void*)(a.x + xr(r) * x_row + kb + c * 16),
+                    (__attribute__((address_space(3))) void*)(sx + (i * T::THREADS + wave * 64) * 16), 16, 0, 0);
+            }
+#pragma unroll
+            for (int i = 0; i < T::W_PER; ++i) {
+                const int s = i * T::THREADS + tid, r = s / T::WC, c = (s % T::WC) ^ ((r / (8 / T::WC)) & (T::WC - 1));
+                if (T::BN * T::WC % T::THREADS == 0 || i * T::THREADS + wave * 64 < T::BN * T::WC)
+                    __builtin_amdgcn_global_load_lds(
+                        (const __attribute__((address_space(1))) void*)(a.w + wr(r) * w_row + wb + c * 16),
+                        (__attribute__((address_space(3))) void*)(sw + (i * T::THREADS + wave * 64) * 16), 16, 0, 0);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < T::X_PER; ++i) {
+                const int s = i * T::THREADS + tid, r = s / T::XC, c = s % T::XC;
+                rx[i] = load_chunk(a.x + xr(r) * x_row + kb + c * 16, int64_t(x_len) - int64_t(kb + c * 16));
+            }
+#pragma unroll
+            for (int i = 0; i < T::W_PER; ++i) {
+                const int s = i * T::THREADS + tid, r = s / T::WC, c = s % T::WC;
+                if (s < T::BN * T::WC)
+                    rw[i] = load_chunk(a.w + wr(r) * w_row + wb + c * 16, int64_t(w_row) - int64_t(wb + c * 16));
+            }
+        }
+        if constexpr (T::XSB != 0) {
+            if (tid < T::BM) {
+                if constexpr (X == ST_X_FP8_GROUP128)
+                    rxs = *reinterpret_cast<const uint32_t*>(a.xs + 4 * (uint64_t(xr(tid)) * groups + step));
+                else {
+                    const uint8_t* p = a.xs + uint64_t(xr(tid)) * (a.k / 32) + step * 4ull;
+                    rxs = !in_regs ? *reinterpret_cast<const uint32_t*>(p) : load_codes(p, int64_t(a.k / 32) - step * 4ll, 4);
+                }
+            }
+        }
+        if constexpr (T::WSB != 0) {
+            if (tid < T::BN) {
+                const uint8_t* p = a.ws + wr(tid) * ws_row + uint64_t(step) * T::WSB;
+                if (in_regs) rws = load_codes(p, int64_t(ws_row) - int64_t(step) * T::WSB, T::WSB);
+                else if constexpr (T::WSB == 4) rws = *reinterpret_cast<const uint32_t*>(p);
+                else rws = *reinterpret_cast<const uint16_t*>(p);
+            }
+        }
+    };
+    // What issue() left in registers goes to LDS.
+    auto commit = [&](int buf) {
+        uint8_t* sx = lds[buf];
+        uint8_t* sw = lds[buf] + T::BM * T::XB;
+        if (in_regs) {
+#pragma unroll
+            for (int i = 0; i < T::X_PER; ++i) {
+                const int s = i * T::THREADS + tid;
+                *reinterpret_cast<u32x4*>(sx + T::x_at(s / T::XC, s % T::XC)) = rx[i];
+            }
+#pragma unroll
+            for (int i = 0; i < T::W_PER; ++i) {
+                const int s = i * T::THREADS + tid;
+                if (s < T::BN * T::WC) *reinterpret_cast<u32x4*>(sw + T::w_at(s / T::WC, s % T::WC)) = rw[i];
+            }
+        }
+        uint32_t* ss = reinterpret_cast<uint32_t*>(sw + T::BN * T::WB);
+        if constexpr (T::XSB != 0) {
+            if (tid < T::BM) ss[tid] = rxs;
+            ss += T::BM;
+        }
+        if constexpr (T::WSB != 0) {
+            if (tid < T::BN) ss[tid] = rws;
+        }
+    };
+
+    f32x4 acc[NT][MT], part[T::GROUPED && !T::F8 ? NT : 1][T::GROUPED && !T::F8 ? MT : 1];
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int j = 0; j < MT; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+
+    if (first < last) {
+        issue(first, 0);
+        commit(0);
+    }
+    for (uint32_t step = first; step < last; ++step) {
+        const int buf = (step - first) & 1;
+        __syncthreads();       // this step's bytes are in LDS, and no wavefront reads the other buffer any more
+        if (step + 1 < last) issue(step + 1, buf ^ 1);
+        const uint8_t* sx = lds[buf];
+        const uint8_t* sw = sx + T::BM * T::XB;
+        const uint8_t* sxs = sw + T::BN * T::WB;
+        const uint8_t* sws = sxs + (T::XSB ? T::BM * 4 : 0);
+        float gs = 0.0f;       // the weight's scale of this wavefront's columns and this group of K
+        if constexpr (T::GROUPED) {
+            const uint32_t nb = (n0 + wn * (NT * 16)) / 128, lastb = (a.n - 1) / 128;
+            gs = reinterpret_cast<const float*>(a.ws)[uint64_t(nb < lastb ? nb : lastb) * groups + uint64_t(step) * T::KS / 128];
+        }
+        if constexpr (!T::F8) {
+            using D = Dense<X, WK>;
+            // 64 of K at a time: lane group q holds 16q..16q+15 of them, 8 for each of two instructions
+#pragma unroll
+            for (int h = 0; h < T::KS / 64; ++h) {
+                u32x4 xv[MT][2], xl[D::SPLIT ? MT : 1][2];
+#pragma unroll
+                for (int j = 0; j < MT; ++j) {
+                    const int r = (wm * MT + j) * 16 + row;
+                    if constexpr (T::Q) {
+                        const u32x4 c = *reinterpret_cast<const u32x4*>(sx + T::x_at(r, q + 4 * h));
+                        const float s = X == ST_X_MXFP8 ? scale_of<ST_KIND_MXFP8>(sxs[r * 4 + 2 * h + (q >> 1)]) : 1.0f;
+                        xv[j][0] = codes8<false, ST_KIND_MXFP8>(c.x, c.y, s);
+                        xv[j][1] = codes8<false, ST_KIND_MXFP8>(c.z, c.w, s);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const u32x4 v = *reinterpret_cast<const u32x4*>(sx + T::x_at(r, 2 * q + i));
+                            if constexpr (D::SPLIT) split_f16(v, xv[j][i], xl[j][i]);
+                            else xv[j][i] = v;
+                        }
+                    }
+                }
+                // GROUPED: sums of 128 of K start at zero and are scaled into acc at the end
+                const bool begin = T::GROUPED && (T::Q ? h == 0 : (step & 1) == 0 || step == first);
+                const bool end = T::GROUPED && (T::Q ? h == 1 : (step & 1) == 1 || step + 1 == last);
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                    const int r = (wn * NT + i) * 16 + row;
+                    u32x4 w0, w1;
+                    const float s = T::WSB ? scale_of<WK>(sws[r * 4 + (WK == ST_KIND_NVFP4 ? q : 2 * h + (q >> 1))]) : 1.0f;
+                    if constexpr (T::FP4) {
+                        const u32x2 c = *reinterpret_cast<const u32x2*>(sw + T::w_at(r, 2 * h + (q >> 1)) + (q & 1) * 8);
+                        w0 = codes8<D::F16, WK>(c.x, 0, s);
+                        w1 = codes8<D::F16, WK>(c.y, 0, s);
+                    } else {
+                        const u32x4 c = *reinterpret_cast<const u32x4*>(sw + T::w_at(r, q + 4 * h));
+                        w0 = codes8<D::F16, WK>(c.x, c.y, s);
+                        w1 = codes8<D::F16, WK>(c.z, c.w, s);
+                    }
+#pragma unroll
+                    for (int j = 0; j < MT; ++j) {
+                        f32x4 c = T::GROUPED ? (begin ? f32x4{0, 0, 0, 0} : part[T::GROUPED ? i : 0][T::GROUPED ? j : 0]) : acc[i][j];
+                        c = mfma32<D::F16>(w0, xv[j][0], c);
+                        c = mfma32<D::F16>(w1, xv[j][1], c);
+                        if constexpr (D::SPLIT) {
+                            c = mfma32<false>(w0, xl[j][0], c);
+                            c = mfma32<false>(w1, xl[j][1], c);
+                        }
+                        if constexpr (T::GROUPED) part[i][j] = c;
+                        else acc[i][j] = c;
+                    }
+                }
+                if constexpr (T::GROUPED) {
+                    if (end) {
+#pragma unroll
+                        for (int j = 0; j < MT; ++j) {
+                            float f = gs;
+                            if constexpr (X == ST_X_FP8_GROUP128)
+                                f *= reinterpret_cast<const float*>(sxs)[(wm * MT + j) * 16 + row];
+#pragma unroll
+                            for (int i = 0; i < NT; ++i)
+#pragma unroll
+                                for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(part[i][j][r], f, acc[i][j][r]);
+                        }
+                    }
+                }
+            }
+        } else {
+            // k of lane group q in a 16x16x128 operand: e4m3 16q..16q+15 and 64+16q..64+16q+15, e2m1 32q..32q+31;
+            // the scale of lane group q belongs to 32q..32q+31
+            i32x8 xv[MT];
+            int xe[MT];
+            float xf[MT];
+#pragma unroll
+            for (int j = 0; j < MT; ++j) {
+                const int r = (wm * MT + j) * 16 + row;
+                const u32x4 lo = *reinterpret_cast<const u32x4*>(sx + T::x_at(r, q));
+                const u32x4 hi = *reinterpret_cast<const u32x4*>(sx + T::x_at(r, q + 4));
+                xv[j] = i32x8{int(lo.x), int(lo.y), int(lo.z), int(lo.w), int(hi.x), int(hi.y), int(hi.z), int(hi.w)};
+                xe[j] = X == ST_X_MXFP8 ? sxs[r * 4 + q] : 127;
+                if constexpr (T::GROUPED) xf[j] = reinterpret_cast<const float*>(sxs)[r] * gs;
+            }
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+                const int r = (wn * NT + i) * 16 + row;
+                i32x8 wv;
+                const u32x4 lo = *reinterpret_cast<const u32x4*>(sw + T::w_at(r, q));
+                if constexpr (T::FP4) {
+                    wv = i32x8{int(lo.x), int(lo.y), int(lo.z), int(lo.w), 0, 0, 0, 0};
+                } else {
+                    const u32x4 hi = *reinterpret_cast<const u32x4*>(sw + T::w_at(r, q + 4));
+                    wv = i32x8{int(lo.x), int(lo.y), int(lo.z), int(lo.w), int(hi.x), int(hi.y), int(hi.z), int(hi.w)};
+                }
+                const int we = T::WSB ? sws[r * 4 + q] : 127;
+#pragma unroll
+                for (int j = 0; j < MT; ++j) {
+                    if constexpr (T::GROUPED) {
+                        const f32x4 p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wv, xv[j], f32x4{0, 0, 0, 0}, 0, 0, 0,
+                                                                                         127, 0, 127);
+#pragma unroll
+                        for (int t = 0; t < 4; ++t) acc[i][j][t] = __builtin_fmaf(p[t], xf[j], acc[i][j][t]);
+                    } else {
+                        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wv, xv[j], acc[i][j], T::FP4 ? 4 : 0, 0, 0,
+                                                                                     we, 0, xe[j]);
+                    }
+                }
+            }
+        }
+        if (step + 1 < last) commit(buf ^ 1);
+    }
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int j = 0; j < MT; ++j)
+            emit<X, WK>(a, split, m0 + (wm * MT + j) * 16 + row, n0 + (wn * NT + i) * 16 + 4 * q, acc[i][j]);
+}
+
+// ------------------------------------------------------------------------- launches
+
+template <int X, int WK, int BM, int BN, bool F8>
+void launch_tile(const Args& a, bool direct, hipStream_t s) {
+    using T = Tile<X, WK, BM, BN, 2, 2, F8>;
+    const dim3 grid(a.tiles_m * a.tiles_n, a.splits);
+    if (direct) hipLaunchKernelGGL((linear_tile<T, true>), grid, dim3(T::THREADS), 0, s, a);
+    else hipLaunchKernelGGL((linear_tile<T, false>), grid, dim3(T::THREADS), 0, s, a);
+}
+
+template <int X, int WK>
+void launch(const Args& a, const Plan& p, hipStream_t s) {
+    if (p.bm == 64) launch_tile<X, WK, 64, 64, false>(a, p.direct, s);
+    else if (!is_q(X) || !p.f8) launch_tile<X, WK, 128, 128, false>(a, p.direct, s);
+    else if constexpr (is_q(X)) launch_tile<X, WK, 128, 128, true>(a, p.direct, s);
+    if (a.part) {
+        const uint64_t items = uint64_t((a.n + 3) / 4) * a.m;
+        hipLaunchKernelGGL((linear_join<X, WK>), dim3(uint32_t((items + 255) / 256)), dim3(256), 0, s, a);
+    }
+}
+
+}  // namespace
+}  // namespace st_linear_impl

@@ -522,6 +522,105 @@ st_status st_materialize_noalloc(const void* blob, const void* table_host, size_
                                  void* const* outs_host, size_t n_outs, uint32_t out_dtype, uint32_t flags,
                                  void* stream);
 
+/* ---- Computing on quantised weights ---------------------------------------------------------------
+ * Operators for callers that keep a checkpoint's quantised weights as stored (the FP8 and ModelOpt FP4
+ * execution that "Resident Modal LLM Architecture", "Current Backend Boundary" and "Live GPU
+ * Validation" leave to the serving backend): a matrix product that decodes the weight on its way to the matrix
+ * instructions, the 8-bit encoding of its input, and the norm ahead of it.  All three only enqueue kernels on
+ * `stream`: they allocate, copy and synchronise nothing and may be captured into a HIP graph.  The stream's
+ * device must be the current one.  Element types are st_out_dtype codes (bf16, fp16, fp32). */
+
+/* Rows x of a product, or the encoding an 8-bit activation has:
+ *   ST_X_BF16, ST_X_F16   dense
+ *   ST_X_FP8_ROW          e4m3 [m, k], fp32 scale [m]                    goes with FP8_TENSOR weights
+ *   ST_X_FP8_GROUP128     e4m3 [m, k], fp32 scale [m, ceil(k / 128)]      goes with FP8_BLOCK128 weights
+ *   ST_X_MXFP8            e4m3 [m, k], E8M0 scale [m, k / 32]             goes with MXFP8 and MXFP4 weights
+ * A value is code * scale. */
+typedef enum st_x_type {
+    ST_X_BF16 = 0, ST_X_F16 = 1, ST_X_FP8_ROW = 2, ST_X_FP8_GROUP128 = 3, ST_X_MXFP8 = 4
+} st_x_type;
+
+typedef enum st_activation {
+    ST_ACT_NONE = 0, ST_ACT_RELU = 1, ST_ACT_SILU = 2, ST_ACT_GELU = 3 /* erf */, ST_ACT_GELU_TANH = 4
+} st_activation;
+
+/* out[m, n] = act(sum_k x[m, k] w[n, k] + bias[n]) + residual[m, n].
+ * w is a quantised weight as stored (contiguous [n, k], the kinds from ST_KIND_FP8_TENSOR on); its value is
+ * code * scale(s) in exact arithmetic, not the bf16 value st_materialize rounds it to.  Sums are kept in fp32
+ * and the result is rounded once.  Pitches are in elements between rows of x, residual and out (the elements of a
+ * row are adjacent; a residual pitch of 0 adds one row to every row; ignored for m <= 1).  out may be the
+ * residual itself; otherwise out must not overlap an input. */
+typedef struct st_linear_args {
+    const void* x;
+    const void* x_scale;     /* 8-bit x: its scales */
+    const void* w;
+    const void* w_scale;     /* as the weight's scale tensor (FP8_TENSOR: fp32 []) */
+    const void* w_scale2;    /* NVFP4: fp32 [] */
+    const void* bias;        /* [n] or NULL */
+    const void* residual;    /* [m, n] or NULL */
+    void* out;               /* [m, n] */
+    void* workspace;         /* st_linear_workspace_bytes bytes, 16-byte aligned, this call's own until it is done */
+    uint64_t workspace_bytes;
+    uint64_t m, n, k;        /* each below 2^31 */
+    uint64_t x_pitch, residual_pitch, out_pitch;
+    uint32_t x_type;         /* st_x_type */
+    uint32_t w_kind;         /* st_kind, ST_KIND_FP8_TENSOR .. ST_KIND_MXFP4 */
+    uint32_t activation;     /* st_activation */
+    uint32_t bias_type, residual_type, out_type;   /* st_out_dtype */
+} st_linear_args;
+
+/* Bytes of workspace st_linear needs for these arguments (0 for most; K is split over workgroups where the
+ * output alone is too small to fill the GPU).  Everything but the workspace fields must be set. */
+st_status st_linear_workspace_bytes(const st_linear_args* args, uint64_t* bytes);
+/* Errors: ST_E_ARG (null or misaligned pointers, unknown types, an x type that does not go with the weight kind,
+ * too little workspace), ST_E_SHAPE (NVFP4 k % 16, MX k % 32, pitches, size limits), ST_E_HIP (the launch). */
+st_status st_linear(const st_linear_args* args, void* stream);
+
+/* Rows x [m, d] (bf16, fp16 or fp32, rows `x_pitch` elements apart) to e4m3 codes [m, d] and scales:
+ *   v = x, or silu(gate) * x with gate [m, d] of x's type
+ *   ST_X_FP8_ROW       s = amax / 448 in fp32 over the row, scale [m]
+ *   ST_X_FP8_GROUP128  the same over 128 columns, scale [m, ceil(d / 128)]
+ *   ST_X_MXFP8         s = the smallest power of two >= amax / 448 over 32 columns, scale [m, d / 32] (d % 32 == 0)
+ *   code = v / s rounded to nearest even (saturated at +-448)
+ * amax is taken over the finite values; where it is 0, s is 1.  A value that is not finite becomes the NaN
+ * code and leaves the others as they are.  s is at least 2^-126 (MX: 2^-127).
+ * Source: the inverse of the formats at the top of this header, for the same checkpoint families. */
+typedef struct st_encode_args {
+    const void* x;
+    const void* gate;        /* or NULL */
+    void* data;              /* e4m3 [m, d], contiguous */
+    void* scale;
+    uint64_t m, d;           /* d below 2^31 */
+    uint64_t x_pitch, gate_pitch;
+    uint32_t x_type;         /* st_out_dtype: the element type of x and gate */
+    uint32_t kind;           /* ST_X_FP8_ROW, ST_X_FP8_GROUP128 or ST_X_MXFP8 */
+} st_encode_args;
+st_status st_encode(const st_encode_args* args, void* stream);
+
+/* Root-mean-square norm of rows, with the residual's addition ahead of it and an optional 8-bit output:
+ *   h = x + residual (x without one);  y = h / sqrt(mean(h^2) + eps) * weight
+ * h is written rounded to x's type (h_out, may be NULL; it may be x or residual itself), y from the unrounded h
+ * to `out` (type out_type, contiguous [m, d]) or, with kind != 0, as codes and scales as st_encode defines them
+ * (amax, scale and code from the unrounded y).  weight may be NULL (ones). */
+typedef struct st_rms_norm_args {
+    const void* x;
+    const void* residual;    /* of x's type, or NULL */
+    const void* weight;      /* [d] or NULL */
+    void* h_out;             /* [m, d] of x's type, contiguous, or NULL */
+    void* out;               /* y, or its e4m3 codes [m, d] */
+    void* scale;             /* kind != 0 */
+    uint64_t m, d;
+    uint64_t x_pitch, residual_pitch;
+    double eps;              /* >= 0 */
+    uint32_t x_type;         /* st_out_dtype */
+    uint32_t weight_type;    /* st_out_dtype */
+    uint32_t out_type;       /* st_out_dtype, kind == 0 */
+    uint32_t kind;           /* 0, ST_X_FP8_ROW, ST_X_FP8_GROUP128 or ST_X_MXFP8 */
+} st_rms_norm_args;
+st_status st_rms_norm(const st_rms_norm_args* args, void* stream);
+/* Errors of both: ST_E_ARG (null or misaligned pointers, unknown types or kind, eps), ST_E_SHAPE (MX d % 32,
+ * pitches, size limits), ST_E_HIP (the launch). */
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,170 @@
+"""CPU: what the operators on quantised weights refuse, before anything reaches a GPU, and the 64-bit reference
+forms of their tests against torch's own conversions."""
+import ctypes as C
+
+import pytest
+import torch
+
+import device_checkpoint_dequantisation_amd as st
+from device_checkpoint_dequantisation_amd import _lib
+from tests import ops_reference as ref
+
+KINDS = ("FP8_TENSOR", "FP8_BLOCK128", "NVFP4", "MXFP8", "MXFP4")
+P = 0x10000     # a well-aligned address that is never followed
+
+
+def _weight(kind="FP8_TENSOR", n=64, k=128):
+    return ref.random_weight(st, kind, n, k, 1)
+
+
+def _x(m=4, k=128, dtype=torch.bfloat16):
+    return torch.zeros(m, k, dtype=dtype)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_linear_needs_a_gpu(kind):
+    with pytest.raises(ValueError, match="GPU"):
+        st.linear(_x(), _weight(kind))
+    with pytest.raises(ValueError, match="GPU"):
+        st.rms_norm(_x())
+    with pytest.raises(ValueError, match="GPU"):
+        st.quantize_activation(_x(), "MXFP8")
+
+
+def test_linear_refuses_weights_that_are_not_what_they_say():
+    for kind in KINDS:
+        w = _weight(kind)
+        for field in ("data", "scale"):
+            good = getattr(w, field)
+            if good.numel() > 1:
+                setattr(w, field, good[:1])
+                with pytest.raises(ValueError, match="holds|scale"):
+                    st.linear(_x(), w)
+            setattr(w, field, torch.zeros(good.shape, dtype=torch.int8))
+            with pytest.raises(ValueError, match="holds|scale"):
+                st.linear(_x(), w)
+            setattr(w, field, good)
+    w = _weight("NVFP4")
+    w.scale2 = None
+    with pytest.raises(ValueError, match="global scale"):
+        st.linear(_x(), w)
+    w = _weight()
+    w.data = w.data.t().contiguous().t()
+    with pytest.raises(ValueError, match="strides"):
+        st.linear(_x(), w)
+    w = _weight()
+    w.shape, w.data = (64, 8, 16), w.data.view(64, 8, 16)
+    with pytest.raises(ValueError, match="matrix"):
+        st.linear(_x(), w)
+    w = _weight()
+    w.kind = "PASS_BF16"
+    with pytest.raises(ValueError, match="not a quantised kind"):
+        st.linear(_x(), w)
+
+
+def test_linear_refuses_rows_that_do_not_fit():
+    with pytest.raises(ValueError, match="against a weight"):
+        st.linear(_x(k=127), _weight())
+    with pytest.raises(ValueError, match="bf16, fp16"):
+        st.linear(_x(dtype=torch.float32), _weight())
+    for xk, wk in (("FP8_ROW", "NVFP4"), ("FP8_ROW", "FP8_BLOCK128"), ("MXFP8", "FP8_TENSOR"), ("FP8_GROUP128", "MXFP8"), ("MXFP8", "NVFP4")):
+        with pytest.raises(ValueError, match="do not go with"):
+            st.linear(ref.random_rows(st, xk, 4, 128, 2), _weight(wk))
+    q = ref.random_rows(st, "FP8_GROUP128", 4, 128, 2)
+    q.scale = q.scale[:3]
+    with pytest.raises(ValueError, match="scales"):
+        st.linear(q, _weight("FP8_BLOCK128"))
+
+
+def test_linear_and_norm_refuse_grad():
+    from device_checkpoint_dequantisation_amd import ops
+    dev = type("Device", (), {"type": "cuda"})()      # stands in for a GPU: the check comes with the device check
+    x2 = type("T", (), {"device": dev, "requires_grad": True})()
+    with pytest.raises(RuntimeError, match="no backward"):
+        ops._on_device(dev, (None, x2), "linear")
+    with torch.no_grad():
+        ops._on_device(dev, (None, x2), "linear")
+
+
+def test_encode_and_norm_refusals():
+    with pytest.raises(ValueError, match="unknown encoding"):
+        st.quantize_activation(_x(), "FP8")
+    with pytest.raises(ValueError, match="multiple of 32"):
+        st.quantize_activation(_x(k=100), "MXFP8")
+    with pytest.raises(ValueError, match="rows are needed"):
+        st.quantize_activation(torch.zeros(4, 4, dtype=torch.int32), "FP8_ROW")
+    with pytest.raises(ValueError):
+        st.rms_norm(torch.tensor(1.0))
+
+
+def _linear_args(**kw):
+    base = dict(x=P, x_scale=None, w=P, w_scale=P, w_scale2=None, bias=None, residual=None, out=P, workspace=None,
+                workspace_bytes=0, m=4, n=64, k=128, x_pitch=128, residual_pitch=0, out_pitch=64, x_type=0, w_kind=3,
+                activation=0, bias_type=0, residual_type=0, out_type=0)
+    base.update(kw)
+    return _lib.LinearArgs(**base)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(x_type=5), -1), (dict(w_kind=2), -1), (dict(w_kind=8), -1), (dict(activation=5), -1), (dict(out_type=3), -1),
+    (dict(bias_type=3), -1), (dict(x_type=2, w_kind=5), -1), (dict(x_type=4, w_kind=3), -1), (dict(m=1 << 31), -6),
+    (dict(n=1 << 31), -6), (dict(k=1 << 31), -6), (dict(w_kind=5, k=24), -6), (dict(w_kind=6, k=48), -6), (dict(out=None), -1),
+    (dict(out_pitch=63), -6), (dict(x_pitch=127), -6), (dict(x=None), -1), (dict(w=None), -1), (dict(w_scale=None), -1),
+    (dict(w_kind=5), -1), (dict(x_type=2), -1), (dict(x=P + 1), -1), (dict(out=P + 1), -1), (dict(w_scale=P + 2), -1),
+    (dict(residual=P + 1, residual_pitch=64), -1), (dict(residual=P, residual_pitch=60), -6), (dict(bias=P + 2, bias_type=2), -1)])
+def test_linear_abi_refusals(kw, code):
+    L = _lib.lib()
+    a = _linear_args(**kw)
+    assert L.st_linear(C.byref(a), None) == code and L.st_last_error()
+    need = C.c_uint64(7)
+    assert L.st_linear_workspace_bytes(C.byref(a), C.byref(need)) == code and need.value == 0
+
+
+def test_linear_abi_workspace_and_empty():
+    L = _lib.lib()
+    need = C.c_uint64()
+    assert L.st_linear(None, None) == -1 and L.st_linear_workspace_bytes(None, C.byref(need)) == -1
+    assert L.st_linear_workspace_bytes(C.byref(_linear_args()), None) == -1
+    for kw in (dict(m=0), dict(n=0)):
+        assert L.st_linear(C.byref(_linear_args(out=None, x=None, w=None, **kw)), None) == 0
+    # a long K over a small output is split: a workspace of fp32 partial results, refused where it is missing, short or misaligned
+    a = _linear_args(m=100, n=128, k=1 << 20, x_pitch=1 << 20, out_pitch=128)
+    assert L.st_linear_workspace_bytes(C.byref(a), C.byref(need)) == 0 and need.value % (100 * 128 * 4) == 0 and need.value
+    assert L.st_linear(C.byref(a), None) == -1
+    a.workspace, a.workspace_bytes = P, need.value - 1
+    assert L.st_linear(C.byref(a), None) == -1
+    a.workspace, a.workspace_bytes = P + 8, need.value
+    assert L.st_linear(C.byref(a), None) == -1
+
+
+@pytest.mark.parametrize("kw,code", [(dict(kind=0), -1), (dict(kind=5), -1), (dict(x_type=3), -1), (dict(x=None), -1), (dict(data=None), -1),
+                                     (dict(scale=None), -1), (dict(x=P + 1), -1), (dict(gate=P + 1), -1), (dict(scale=P + 2), -1),
+                                     (dict(x_pitch=100), -6), (dict(gate=P, gate_pitch=100), -6), (dict(kind=4, d=100), -6), (dict(m=1 << 31), -6),
+                                     (dict(d=1 << 31), -6)])
+def test_encode_abi_refusals(kw, code):
+    base = dict(x=P, gate=None, data=P, scale=P, m=4, d=128, x_pitch=128, gate_pitch=0, x_type=0, kind=2)
+    base.update(kw)
+    assert _lib.lib().st_encode(C.byref(_lib.EncodeArgs(**base)), None) == code
+
+
+@pytest.mark.parametrize("kw,code", [(dict(kind=1), -1), (dict(kind=5), -1), (dict(x_type=3), -1), (dict(weight_type=3), -1), (dict(out_type=3), -1),
+                                     (dict(eps=-1.0), -1), (dict(eps=float("nan")), -1), (dict(x=None), -1), (dict(out=None), -1),
+                                     (dict(kind=2, scale=None), -1), (dict(h_out=P + 1), -1), (dict(weight=P + 1), -1),
+                                     (dict(residual=P, residual_pitch=1), -6), (dict(kind=4, d=100), -6), (dict(m=1 << 31), -6)])
+def test_norm_abi_refusals(kw, code):
+    base = dict(x=P, residual=None, weight=P, h_out=None, out=P, scale=P, m=4, d=128, x_pitch=128, residual_pitch=0, eps=1e-6,
+                x_type=0, weight_type=0, out_type=0, kind=0)
+    base.update(kw)
+    assert _lib.lib().st_rms_norm(C.byref(_lib.RmsNormArgs(**base)), None) == code
+    assert _lib.lib().st_rms_norm(None, None) == -1 and _lib.lib().st_encode(None, None) == -1
+
+
+def test_reference_codes_match_torch():
+    codes = torch.arange(256, dtype=torch.uint8)
+    want = codes.view(torch.float8_e4m3fn).double()
+    got = ref.e4m3(codes.view(torch.float8_e4m3fn))
+    assert torch.equal(got.isnan(), want.isnan()) and torch.equal(got[~got.isnan()], want[~want.isnan()])
+    v = torch.randn(20000, generator=torch.Generator().manual_seed(1)) * 100
+    assert torch.equal(ref.e4m3_codes(v.double()), v.clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8) & 127)
+    e = torch.arange(255, dtype=torch.uint8).view(torch.float8_e8m0fnu)
+    assert torch.equal(ref.e8m0(e), e.float().double())
