@@ -8,11 +8,36 @@ namespace {
 using namespace st_linear_impl;
 
 Plan plan_of(const st_linear_args& g) {
-    Plan p;
+    Plan p = {};
     const bool q = is_q(g.x_type), fp4 = is_fp4(g.w_kind);
     const uint64_t xb = g.x_pitch * (q ? 1 : 2), wb = fp4 ? g.k / 2 : g.k;
     auto al = [](const void* v, uint64_t n) { return reinterpret_cast<uintptr_t>(v) % n == 0; };
     p.direct = al(g.x, 16) && al(g.w, 16) && (g.m <= 1 || xb % 16 == 0) && wb % 16 == 0;
+    // one row, and whole 16-byte pieces of K per lane
+    if (p.direct && g.m == 1 && g.k && g.k % (fp4 ? 32 : 16) == 0 && (g.w_kind != ST_KIND_NVFP4 || al(g.w_scale, 2))) {
+        const uint32_t slice = fp4 ? 2048 : 1024, slices = uint32_t((g.k + slice - 1) / slice), rounds = (slices + 3) / 4;
+        p.one = true;
+        p.waves = (slices + rounds - 1) / rounds;
+        p.splits = 1;
+        return p;
+    }
+    // few rows, and whole 64-byte pieces
+    if (p.direct && g.m <= 16 && g.k && g.k % (fp4 ? 128 : 64) == 0 && (g.w_kind != ST_KIND_NVFP4 || al(g.w_scale, 8)) &&
+        (!is_mx(g.w_kind) || al(g.w_scale, 4)) && (g.x_type != ST_X_MXFP8 || al(g.x_scale, 4))) {
+        const uint32_t turns = uint32_t((g.k + (fp4 ? 511 : 255)) / (fp4 ? 512 : 256));
+        // A weight of few rows is split over K as well (16 rows through NVFP4 [5120, 25600]: 41.8 us in four parts, 66 whole),
+        // which costs a second launch (8-bit kinds from 256 workgroups on lose by it: FP8 [4096, 12288] 14.7 us whole, 16.3 halved).
+        const uint32_t groups = few_groups(g.w_kind), waves = few_waves(g.w_kind);
+        p.few = true;
+        const uint64_t tiles = (g.n + 16 * groups - 1) / (16 * groups), want = fp4 ? 512 : 256;
+        uint32_t s = 1;
+        while (tiles * s < want && turns / (2 * s) >= waves) s *= 2;
+        p.steps = (turns + s - 1) / s;
+        p.splits = (turns + p.steps - 1) / p.steps;
+        p.waves = p.steps < waves ? p.steps : waves;
+        p.part_bytes = p.splits > 1 ? uint64_t(p.splits) * g.m * g.n * 4 : 0;
+        return p;
+    }
     const uint64_t ks = q ? 128 : 64;
     if (g.w_kind == ST_KIND_NVFP4) p.direct = p.direct && al(g.w_scale, 4) && g.k % 64 == 0;
     if (is_mx(g.w_kind)) p.direct = p.direct && al(g.w_scale, ks / 32) && g.k % ks == 0;
@@ -113,7 +138,7 @@ extern "C" st_status st_linear(const st_linear_args* args, void* stream) {
     a.m = uint32_t(g.m); a.n = uint32_t(g.n); a.k = uint32_t(g.k);
     a.act = g.activation; a.bias_type = g.bias_type; a.res_type = g.residual_type; a.out_type = g.out_type;
     a.splits = p.splits; a.steps = p.steps;
-    a.tiles_m = uint32_t((g.m + p.bm - 1) / p.bm); a.tiles_n = uint32_t((g.n + p.bn - 1) / p.bn);
+    if (p.bm) a.tiles_m = uint32_t((g.m + p.bm - 1) / p.bm), a.tiles_n = uint32_t((g.n + p.bn - 1) / p.bn);
     if (uint64_t(a.tiles_m) * a.tiles_n > 0x7FFFFFFFull) return st_fail(ST_E_SHAPE, "%s: too many tiles", kWho);
     auto quad = [](const void* v, uint32_t type, uint64_t pitch, uint64_t rows) {
         const uint64_t e = type == ST_OUT_F32 ? 4 : 2;

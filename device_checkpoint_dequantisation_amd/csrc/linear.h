@@ -12,6 +12,12 @@ constexpr bool is_q(int x) { return x >= ST_X_FP8_ROW; }
 constexpr bool is_fp4(int w) { return w == ST_KIND_NVFP4 || w == ST_KIND_MXFP4; }
 constexpr bool is_mx(int w) { return w == ST_KIND_MXFP8 || w == ST_KIND_MXFP4; }
 
+// linear_few: groups of 16 weight rows per wavefront, and wavefronts per workgroup.  Two groups halve x's traffic for
+// more registers: fp4, whose turn takes twice the x, gains (16 rows through NVFP4 [5120, 25600] on MI355X: 41.8 us with two,
+// 47 with one), the 8-bit kinds lose (block FP8 [4096, 4096], 2 rows: 8.0 against 6.6 us).
+constexpr int few_groups(int w) { return is_fp4(w) ? 2 : 1; }
+constexpr int few_waves(int w) { return is_fp4(w) ? 4 : 8; }
+
 struct Args {
     const uint8_t *x, *xs, *w, *ws, *ws2, *bias, *res;
     uint8_t* out;
@@ -28,6 +34,9 @@ struct Args {
 struct Plan {
     bool direct;                 // rows start on 16 bytes: global memory to LDS without a detour
     bool f8;                     // the f8f6f4 matrix instructions
+    bool one;                    // linear_one
+    bool few;                    // linear_few
+    uint32_t waves;              // of a workgroup of linear_one and linear_few
     uint32_t bm, bn, splits, steps;
     uint64_t part_bytes;
 };

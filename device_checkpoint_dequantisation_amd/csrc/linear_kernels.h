@@ -20,9 +20,10 @@
 // The weight is the A operand of the matrix instructions (its rows are the D rows), so a lane holds four
 // consecutive output columns of one row of y and stores them together.
 //
-// Three kernels:
-//  * linear_few: m <= 16.  Bound by the weight's bytes: each wavefront streams its part of K for a few
-//    16-row groups of the weight straight into registers, the wavefronts of a workgroup join in LDS.
+// Four kernels:
+//  * linear_one: m = 1, dot products on the vector unit at the rate the weight arrives.
+//  * linear_few: m <= 16.  Each wavefront streams its part of K for one or two 16-row groups of the weight straight
+//    into registers and the matrix instructions, the wavefronts of a workgroup join in LDS.
 //  * linear_tile: tiles of y staged through LDS, double-buffered, one barrier per step of K.  x and the weight are
 //    staged as stored and the weight is decoded on its way from LDS to the matrix instructions.
 //  * linear_join: adds the fp32 partial results where K was split over workgroups, in a fixed order.
@@ -208,6 +209,318 @@ template <int X, int WK>
 struct Dense {
     static constexpr bool F16 = X == ST_X_F16 && !is_mx(WK), SPLIT = X == ST_X_F16 && is_mx(WK);
 };
+
+// ------------------------------------------------------------------------- one row
+
+// m = 1: dot products on the vector unit.  A wavefront takes a slice of K, 16 bytes of a weight row per lane, for R
+// weight rows: its loads are contiguous, all R of them are in flight together, and its part of x stays in
+// registers.  Decoding costs half an instruction per weight and multiplying another half (two-element dot
+// products into fp32); a block's scale multiplies the block's sum.  (16x16x32 matrix instructions leave 15 of 16 columns empty for one
+// token, want NVFP4 weights multiplied by their scales first, 2 instructions each, and x once per 16 weight rows.)
+// The lanes' sums fold together within the wavefront, the slices' sums in LDS.
+template <int X_, int WK_>
+struct One {
+    static constexpr int X = X_, WK = WK_, R = 4;     // weight rows per wavefront
+    static constexpr bool Q = is_q(X), FP4 = is_fp4(WK), GROUPED = WK == ST_KIND_FP8_BLOCK128;
+    static constexpr int E = FP4 ? 32 : 16;          // elements of K per lane
+    static constexpr int SLICE = 64 * E;
+    static constexpr int PAIRS = E / 2;
+};
+
+template <bool F16>
+__device__ __forceinline__ float dot2(uint32_t a, uint32_t b, float c) {
+    if constexpr (F16) return __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, a), __builtin_bit_cast(f16x2, b), c, false);
+    else return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, a), __builtin_bit_cast(bf16x2, b), c, false);
+}
+
+// Sum over the 64 lanes of each of N values: v[0] of lane l becomes the total of value l % N.  Each step halves the values a lane
+// holds by handing the other half to the lane across.
+template <int N>
+__device__ __forceinline__ float fold(float* v) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int half = N / 2; half >= 1; half /= 2) {
+        const bool up = (lane & half) != 0;
+#pragma unroll
+        for (int i = 0; i < half; ++i) {
+            const float keep = up ? v[i + half] : v[i], give = up ? v[i] : v[i + half];
+            v[i] = keep + __shfl_xor(give, half);
+        }
+    }
+#pragma unroll
+    for (int o = N; o < 64; o *= 2) v[0] += __shfl_xor(v[0], o);
+    return v[0];
+}
+
+constexpr int kOneWaves = 4;
+
+template <class F>
+__global__ __launch_bounds__(64 * kOneWaves) void linear_one(Args a) {
+    constexpr int X = F::X, WK = F::WK, R = F::R, E = F::E, PAIRS = F::PAIRS;
+    using D = Dense<X, WK>;
+    __shared__ __align__(16) float joined[kOneWaves][R];
+    const int lane = threadIdx.x & 63;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
+    const uint32_t n0 = blockIdx.x * R;
+    const uint32_t w_row = F::FP4 ? a.k / 2 : a.k, ws_row = a.k / (WK == ST_KIND_NVFP4 ? 16 : 32);
+    const uint32_t groups = (a.k + 127) / 128;
+    float acc[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) acc[r] = 0.0f;
+
+    for (uint32_t k0 = wave * F::SLICE; k0 < a.k; k0 += waves * F::SLICE) {
+        const uint32_t k = k0 + lane * E;
+        const bool in = k < a.k;          // lanes behind K's end hold zeros
+        u32x4 w[R];
+        uint32_t ws[R];
+        // rows past the last are read as the last one; nothing of them is stored
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const uint32_t n = n0 + r < a.n ? n0 + r : a.n - 1;
+            const uint8_t* pw = a.w + uint64_t(n) * w_row;
+            const uint8_t* ps = a.ws + uint64_t(n) * ws_row;
+            w[r] = in ? *reinterpret_cast<const u32x4*>(pw + (F::FP4 ? k / 2 : k)) : u32x4{0, 0, 0, 0};
+            if constexpr (WK == ST_KIND_NVFP4) ws[r] = in ? *reinterpret_cast<const uint16_t*>(ps + k / 16) : 0;
+            else if constexpr (is_mx(WK)) ws[r] = in ? ps[k / 32] : 0;
+        }
+        uint32_t x[PAIRS], xl[D::SPLIT ? PAIRS : 1];
+        const uint8_t* px = a.x + k * (F::Q ? 1u : 2u);
+        if constexpr (F::Q) {
+            const float s = X == ST_X_MXFP8 ? scale_of<ST_KIND_MXFP8>(in ? a.xs[k / 32] : 0) : 1.0f;
+#pragma unroll
+            for (int h = 0; h < E / 16; ++h) {
+                const u32x4 c = in ? *reinterpret_cast<const u32x4*>(px + 16 * h) : u32x4{0, 0, 0, 0};
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const u32x4 t = codes8<false, ST_KIND_MXFP8>(c[2 * i], c[2 * i + 1], s);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) x[8 * h + 4 * i + j] = t[j];
+                }
+            }
+        } else {
+#pragma unroll
+            for (int h = 0; h < E / 8; ++h) {
+                u32x4 c = in ? *reinterpret_cast<const u32x4*>(px + 16 * h) : u32x4{0, 0, 0, 0}, lo;
+                if constexpr (D::SPLIT) split_f16(c, c, lo);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    x[4 * h + j] = c[j];
+                    if constexpr (D::SPLIT) xl[4 * h + j] = lo[j];
+                }
+            }
+        }
+        float f = 0.0f;                    // the lane's fp32 scale, where the kinds have one per 128 of K
+        if constexpr (F::GROUPED) {
+            if (in) f = reinterpret_cast<const float*>(a.ws)[uint64_t(n0 / 128) * groups + k / 128];
+            if (X == ST_X_FP8_GROUP128 && in) f *= reinterpret_cast<const float*>(a.xs)[k / 128];
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            // 16 elements at a time: an NVFP4 block, half an MX block
+            float part = 0.0f;
+#pragma unroll
+            for (int b = 0; b < E / 16; ++b) {
+                u32x4 v[2];
+                const float s = is_mx(WK) ? scale_of<WK>(ws[r]) : 1.0f;
+                if constexpr (WK == ST_KIND_NVFP4) {
+                    // the codes alone (exact in bf16 and fp16): the block's sum takes the scale
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if constexpr (D::F16) {
+                            v[h][0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w[r][2 * b + h], 1.0f, 0));
+                            v[h][1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w[r][2 * b + h], 1.0f, 1));
+                            v[h][2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w[r][2 * b + h], 1.0f, 2));
+                            v[h][3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w[r][2 * b + h], 1.0f, 3));
+                        } else {
+                            v[h] = codes8<false, ST_KIND_MXFP4>(w[r][2 * b + h], 0, 1.0f);
+                        }
+                    }
+                } else if constexpr (F::FP4) {
+                    v[0] = codes8<D::F16, WK>(w[r][2 * b], 0, s);
+                    v[1] = codes8<D::F16, WK>(w[r][2 * b + 1], 0, s);
+                } else {
+                    v[0] = codes8<D::F16, WK>(w[r].x, w[r].y, s);
+                    v[1] = codes8<D::F16, WK>(w[r].z, w[r].w, s);
+                }
+                float d = WK == ST_KIND_NVFP4 ? 0.0f : part;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    d = dot2<D::F16>(v[i / 4][i % 4], x[8 * b + i], d);
+                    if constexpr (D::SPLIT) d = dot2<false>(v[i / 4][i % 4], xl[8 * b + i], d);
+                }
+                if constexpr (WK == ST_KIND_NVFP4) acc[r] = __builtin_fmaf(d, scale_of<WK>(ws[r] >> (8 * b) & 0xFF), acc[r]);
+                else part = d;
+            }
+            if constexpr (WK != ST_KIND_NVFP4) acc[r] = F::GROUPED ? __builtin_fmaf(part, f, acc[r]) : acc[r] + part;
+        }
+    }
+    const float v = fold<R>(acc);
+    if (lane < R) joined[wave][lane] = v;
+    __syncthreads();
+    if (threadIdx.x == 0) {                // the slices in their order
+        f32x4 t = {0, 0, 0, 0};
+        for (uint32_t o = 0; o < waves; ++o) t += *reinterpret_cast<const f32x4*>(joined[o]);
+        finish<X, WK>(a, 0, n0, t);
+    }
+}
+
+// ------------------------------------------------------------------------- few rows
+
+// 1 < m <= 16: one 16x16x32 instruction takes all rows of x.  A wavefront holds a turn of K, 64 bytes of a weight row per lane,
+// for NT groups of 16 weight rows, all of it in flight at once straight into registers, and reads its part of x once for them; the
+// wavefronts of a workgroup take different turns of the same weight rows and join in LDS.
+template <int X_, int WK_>
+struct Few {
+    static constexpr int X = X_, WK = WK_;
+    static constexpr bool Q = is_q(X), FP4 = is_fp4(WK), GROUPED = WK == ST_KIND_FP8_BLOCK128;
+    static constexpr int NT = few_groups(WK), WAVES = few_waves(WK);
+    static constexpr int LK = FP4 ? 128 : 64;        // elements of K a lane takes per turn (64 bytes of the weight)
+    static constexpr int SS = 4 * LK;                // elements of K per turn
+    static constexpr int CK = LK / 4;                // elements per 16-byte chunk of the weight
+    static constexpr int XE = Q ? 1 : 2;             // bytes per element of x
+    static constexpr int XL = CK * XE / 16;          // 16-byte pieces of x that go with a weight chunk
+    // scale bytes of a lane's elements
+    static constexpr int WSB = WK == ST_KIND_NVFP4 ? LK / 16 : is_mx(WK) ? LK / 32 : 0;
+    static constexpr int XSB = X == ST_X_MXFP8 ? LK / 32 : 0;
+    // K of lane group q's chunk j: neighbouring chunks belong to one lane, so that its scales are adjacent; with a scale per 128
+    // of K, chunk j of all lanes together is 64 of K instead, and a scale belongs to whole instructions.
+    static __device__ __forceinline__ uint32_t k_of(uint32_t q, uint32_t j) { return GROUPED ? 64 * j + 16 * q : LK * q + CK * j; }
+};
+
+template <int BYTES>
+__device__ __forceinline__ uint64_t load_scales(const uint8_t* p) {
+    if constexpr (BYTES == 8) return *reinterpret_cast<const uint64_t*>(p);
+    else if constexpr (BYTES == 4) return *reinterpret_cast<const uint32_t*>(p);
+    else if constexpr (BYTES == 2) return *reinterpret_cast<const uint16_t*>(p);
+    else return 0;
+}
+
+template <bool V>
+struct Flag {
+    static constexpr bool value = V;
+};
+
+template <class F>
+__global__ __launch_bounds__(64 * F::WAVES) void linear_few(Args a) {
+    constexpr int X = F::X, WK = F::WK, NT = F::NT;
+    using D = Dense<X, WK>;
+    __shared__ __align__(16) float joined[F::WAVES][NT][256];
+    const int lane = threadIdx.x & 63, row = lane & 15, q = lane >> 4;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
+    const uint32_t n0 = blockIdx.x * (16 * NT);
+    const bool have = uint32_t(row) < a.m;        // lanes of rows that are not there load nothing: their column of D is not stored
+    const uint32_t xrow = have ? row : 0;
+    const uint32_t w_row = F::FP4 ? a.k / 2 : a.k, ws_row = a.k / (WK == ST_KIND_NVFP4 ? 16 : 32);
+    const uint32_t groups = (a.k + 127) / 128;
+    const uint8_t* px = a.x + xrow * a.x_pitch * F::XE;
+    f32x4 acc[NT];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) acc[i] = f32x4{0, 0, 0, 0};
+
+    // a turn: K from k0; WHOLE: all SS elements are there, else lanes (chunks) behind the end hold zeros
+    auto turn = [&](uint32_t k0, auto whole) {
+        constexpr bool WHOLE = decltype(whole)::value;
+        const bool in = WHOLE || F::GROUPED || k0 + F::LK * q < a.k;
+        u32x4 w[NT][4], xr[4][F::XL];
+        uint64_t wsc[NT], xsc = 0;
+        float gs[F::GROUPED ? NT : 1][2];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int h = 0; h < F::XL; ++h) xr[j][h] = u32x4{0, 0, 0, 0};
+        if (have) {
+            if constexpr (F::XSB != 0) xsc = in ? load_scales<F::XSB>(a.xs + xrow * uint64_t(a.k / 32) + (k0 + F::LK * q) / 32) : 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t k = k0 + F::k_of(q, j);
+#pragma unroll
+                for (int h = 0; h < F::XL; ++h)
+                    if (WHOLE || k < a.k) xr[j][h] = *reinterpret_cast<const u32x4*>(px + k * F::XE + 16 * h);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            const uint32_t r = n0 + i * 16 + row, at = r < a.n ? r : a.n - 1;
+            const uint8_t* pw = a.w + uint64_t(at) * w_row;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t k = k0 + F::k_of(q, j);
+                w[i][j] = WHOLE || k < a.k ? *reinterpret_cast<const u32x4*>(pw + (F::FP4 ? k / 2 : k)) : u32x4{0, 0, 0, 0};
+            }
+            if constexpr (F::WSB != 0)
+                wsc[i] = in ? load_scales<F::WSB>(a.ws + uint64_t(at) * ws_row + (k0 + F::LK * q) / (WK == ST_KIND_NVFP4 ? 16 : 32)) : 0;
+            if constexpr (F::GROUPED) {
+                const uint32_t nb = (n0 + i * 16) / 128, lastb = (a.n - 1) / 128;
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    const uint32_t kb = k0 / 128 + g < groups ? k0 / 128 + g : groups - 1;
+                    gs[i][g] = reinterpret_cast<const float*>(a.ws)[uint64_t(nb < lastb ? nb : lastb) * groups + kb];
+                    if constexpr (X == ST_X_FP8_GROUP128) gs[i][g] *= reinterpret_cast<const float*>(a.xs)[uint64_t(xrow) * groups + kb];
+                }
+            }
+        }
+        u32x4 xv[4][F::CK / 8], xl[D::SPLIT ? 4 : 1][D::SPLIT ? F::CK / 8 : 1];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int h = 0; h < F::XL; ++h) {
+                const u32x4 c = xr[j][h];
+                if constexpr (F::Q) {
+                    const float s = X == ST_X_MXFP8 ? scale_of<ST_KIND_MXFP8>(uint32_t(xsc >> (8 * (j * F::CK / 32))) & 0xFF) : 1.0f;
+                    xv[j][2 * h] = codes8<false, ST_KIND_MXFP8>(c.x, c.y, s);
+                    xv[j][2 * h + 1] = codes8<false, ST_KIND_MXFP8>(c.z, c.w, s);
+                } else if constexpr (D::SPLIT) {
+                    split_f16(c, xv[j][h], xl[j][h]);
+                } else {
+                    xv[j][h] = c;
+                }
+            }
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            f32x4 c = acc[i];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (F::GROUPED && (j & 1) == 0) c = f32x4{0, 0, 0, 0};
+#pragma unroll
+                for (int h = 0; h < F::CK / 8; ++h) {
+                    u32x4 wv;
+                    if constexpr (WK == ST_KIND_NVFP4) {
+                        wv = codes8<D::F16, WK>(w[i][j][h], 0, scale_of<WK>(uint32_t(wsc[i] >> (8 * (2 * j + h / 2))) & 0xFF));
+                    } else if constexpr (F::FP4) {
+                        wv = codes8<D::F16, WK>(w[i][j][h], 0, scale_of<WK>(uint32_t(wsc[i] >> (8 * j)) & 0xFF));
+                    } else {
+                        const float s = F::WSB ? scale_of<WK>(uint32_t(wsc[F::WSB ? i : 0] >> (8 * (j / 2))) & 0xFF) : 1.0f;
+                        wv = codes8<D::F16, WK>(w[i][j][2 * h], w[i][j][2 * h + 1], s);
+                    }
+                    c = mfma32<D::F16>(wv, xv[j][h], c);
+                    if constexpr (D::SPLIT) c = mfma32<false>(wv, xl[j][h], c);
+                }
+                // a group behind K's end has a sum of 0 and must not meet the last group's scale, which may be infinite
+                if (F::GROUPED && (j & 1) == 1 && (WHOLE || k0 + 64 * (j - 1) < a.k)) {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) acc[i][r] = __builtin_fmaf(c[r], gs[F::GROUPED ? i : 0][j / 2], acc[i][r]);
+                }
+            }
+            if constexpr (!F::GROUPED) acc[i] = c;
+        }
+    };
+    // K is split over blockIdx.y too: a.steps turns each
+    const uint32_t begin = blockIdx.y * a.steps * F::SS;
+    const uint32_t end = a.k - begin < a.steps * F::SS ? a.k : begin + a.steps * F::SS;
+    for (uint32_t k0 = begin + wave * F::SS; k0 < end; k0 += waves * F::SS) {
+        if (k0 + F::SS <= a.k) turn(k0, Flag<true>{});
+        else turn(k0, Flag<false>{});
+    }
+#pragma unroll
+    for (int i = 0; i < NT; ++i) *reinterpret_cast<f32x4*>(&joined[wave][i][lane * 4]) = acc[i];
+    __syncthreads();
+    // lane l of the first NT wavefronts adds up its four sums, in the order of the wavefronts
+    for (uint32_t i = wave; i < NT; i += waves) {
+        f32x4 v = *reinterpret_cast<const f32x4*>(&joined[0][i][lane * 4]);
+        for (uint32_t o = 1; o < waves; ++o) v += *reinterpret_cast<const f32x4*>(&joined[o][i][lane * 4]);
+        emit<X, WK>(a, blockIdx.y, row, n0 + i * 16 + 4 * q, v);
+    }
+}
 
 // ------------------------------------------------------------------------- tiles
 
@@ -525,7 +838,14 @@ void launch_tile(const Args& a, bool direct, hipStream_t s) {
 
 template <int X, int WK>
 void launch(const Args& a, const Plan& p, hipStream_t s) {
-    if (p.bm == 64) launch_tile<X, WK, 64, 64, false>(a, p.direct, s);
+    if (p.one) {
+        hipLaunchKernelGGL((linear_one<One<X, WK>>), dim3((a.n + One<X, WK>::R - 1) / One<X, WK>::R), dim3(64 * p.waves), 0, s, a);
+        return;
+    }
+    if (p.few) {
+        const dim3 grid((a.n + 16 * Few<X, WK>::NT - 1) / (16 * Few<X, WK>::NT), a.splits), block(64 * p.waves);
+        hipLaunchKernelGGL((linear_few<Few<X, WK>>), grid, block, 0, s, a);
+    } else if (p.bm == 64) launch_tile<X, WK, 64, 64, false>(a, p.direct, s);
     else if (!is_q(X) || !p.f8) launch_tile<X, WK, 128, 128, false>(a, p.direct, s);
     else if constexpr (is_q(X)) launch_tile<X, WK, 128, 128, true>(a, p.direct, s);
     if (a.part) {

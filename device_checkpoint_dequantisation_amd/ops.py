@@ -35,6 +35,10 @@ _XKIND = {k: i + 2 for i, k in enumerate(ACTIVATION_KINDS)}
 _E4M3, _E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
 
 
+# the current stream's handle without the Python object around it (0.1 instead of 2 us)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
+
+
 @dataclass
 class QuantizedActivation:
     """Rows in 8 bits with scales; a value is code * scale.
@@ -93,7 +97,7 @@ def _launch(fn, args, device, stream, tensors, who):
         with torch.cuda.device(device):
             return _launch(fn, args, device, stream, tensors, who)
     if stream is None:
-        raw = torch.cuda.current_stream(device).cuda_stream
+        raw = _raw_stream(device.index)
     else:
         if stream.device != device:
             raise ValueError(f"{who}: stream of {stream.device}, tensors on {device}")
