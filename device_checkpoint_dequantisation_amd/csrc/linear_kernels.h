@@ -528,8 +528,9 @@ __global__ __launch_bounds__(64 * F::WAVES) void linear_few(Args a) {
 // of e4m3.  LDS holds rows of 16-byte chunks; chunk c of row r sits at c ^ swizzle(r), so that eight lanes
 // reading the same chunk of eight consecutive rows touch all 32 banks once.
 // F8 (8-bit x): the f8f6f4 matrix instructions, at twice the bf16 rate; otherwise both sides are widened to bf16.
-template <int X_, int WK_, int BM_, int BN_, int WAVES_M_, int WAVES_N_, bool F8_>
+template <int X_, int WK_, int BM_, int BN_, int WAVES_M_, int WAVES_N_, bool F8_, int STAGES_>
 struct Tile {
+    static constexpr int STAGES = STAGES_;
     static constexpr int X = X_, WK = WK_, BM = BM_, BN = BN_, WAVES_M = WAVES_M_, WAVES_N = WAVES_N_;
     static constexpr bool Q = is_q(X), FP4 = is_fp4(WK), F8 = F8_;
     static constexpr int THREADS = 64 * WAVES_M * WAVES_N;
@@ -541,10 +542,12 @@ struct Tile {
     static constexpr int WSB = WK == ST_KIND_NVFP4 ? KS / 16 : is_mx(WK) ? KS / 32 : 0;
     static constexpr int XSB = X == ST_X_MXFP8 || X == ST_X_FP8_GROUP128 ? 4 : 0;
     static constexpr bool GROUPED = WK == ST_KIND_FP8_BLOCK128;    // sums scaled per 128 of K
+    // wavefronts that load the scale words of the tile's x rows and weight rows (a word a row and step) in the direct modes
+    static constexpr int X_WAVES = XSB ? BM / 64 : 0, W_WAVES = WSB ? BN / 64 : 0;
     static constexpr int STAGE = BM * XB + BN * WB + (XSB ? BM * 4 : 0) + (WSB ? BN * 4 : 0);
     static constexpr int X_PER = BM * XC / THREADS, W_PER = (BN * WC + THREADS - 1) / THREADS;
     static_assert(BM * XC % THREADS == 0 && BM <= THREADS && BN <= THREADS, "tile");
-    static_assert(!GROUPED || BN / WAVES_N <= 64, "a wavefront's columns lie in one scale block");
+    static_assert(!GROUPED || (BN / WAVES_N <= 64 && BN % 64 == 0), "a wavefront's columns lie in one scale block");
     static __device__ __forceinline__ int x_at(int r, int c) { return r * XB + ((c ^ (r & 7)) << 4); }
     static __device__ __forceinline__ int w_at(int r, int c) {
         return r * WB + ((c ^ ((r / (8 / WC)) & (WC - 1))) << 4);
@@ -568,13 +571,28 @@ __device__ __forceinline__ uint32_t load_codes(const uint8_t* p, int64_t avail, 
     return v;
 }
 
-// DIRECT: every row starts on 16 bytes (scale codes on a step's bytes), so whole steps go from global memory
-// straight into LDS; otherwise, and for the last step of a K that is no whole number of steps, chunks pass
-// through registers, with zeros behind the row's end.
+// DIRECT: K is whole steps and every row starts on 16 bytes (scale words on 4), so steps go from global memory straight into
+// LDS, STAGES - 1 of them on their way.  Otherwise chunks pass through registers, with zeros behind a row's end, one step ahead.
+// s_waitcnt for vmcnt(n) and lgkmcnt(0), expcnt at its maximum (gfx9 encoding: vmcnt in bits 3:0 and 15:14)
+constexpr int wait_vmem(int n) { return (n & 15) | (n >> 4) << 14 | 7 << 4; }
+// A wave-uniform fp32 that the kernel never writes, by the scalar unit.
+__device__ __forceinline__ float ld_uniform_f32(const uint8_t* p) {
+    return *reinterpret_cast<const __attribute__((address_space(4))) float*>(reinterpret_cast<uintptr_t>(p));
+}
+constexpr int kRawBufferWord3 = 0x00020000;  // V# word 3 of an untyped buffer (32-bit data format)
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_at(const uint8_t* p) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, 0x7FFFFFFF, kRawBufferWord3);
+}
+// 16 bytes per lane from base + voff + soff to LDS at `to` + 16 * lane; `to` is the same for the wavefront.
+__device__ __forceinline__ void to_lds(__amdgpu_buffer_rsrc_t base, uint8_t* to, uint32_t voff, uint32_t soff) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(base, (__attribute__((address_space(3))) void*)to, 16, int(voff), int(soff), 0, 0);
+}
+
 template <class T, bool DIRECT>
-__global__ __launch_bounds__(T::THREADS) void linear_tile(Args a) {
+__global__ __launch_bounds__(T::THREADS, 2) void linear_tile(Args a) {
     constexpr int X = T::X, WK = T::WK, MT = T::MT, NT = T::NT;
-    __shared__ __align__(128) uint8_t lds[2][T::STAGE];
+    constexpr int S = DIRECT ? T::STAGES : 2;
+    __shared__ __align__(128) uint8_t lds[S][T::STAGE];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int row = lane & 15, q = lane >> 4;
     const int wm = wave / T::WAVES_N, wn = wave % T::WAVES_N;
@@ -602,31 +620,43 @@ __global__ __launch_bounds__(T::THREADS) void linear_tile(Args a) {
     auto xr = [&](uint32_t r) { return m0 + r < a.m ? m0 + r : a.m - 1; };
     auto wr = [&](uint32_t r) { return n0 + r < a.n ? n0 + r : a.n - 1; };
 
-    u32x4 rx[T::X_PER], rw[T::W_PER];      // chunks on their way through registers
+    // Direct loads: 32-bit offsets from the tile's first row, the step's offset added by the scalar unit
+    const __amdgpu_buffer_rsrc_t bx = rows_at(a.x + m0 * x_row), bw = rows_at(a.w + n0 * w_row);
+    uint32_t x_off[T::X_PER], w_off[T::W_PER];
+    if constexpr (DIRECT) {
+#pragma unroll
+        for (int i = 0; i < T::X_PER; ++i) {
+            const int s = i * T::THREADS + tid, r = s / T::XC, c = (s % T::XC) ^ (r & 7);
+            x_off[i] = (xr(r) - m0) * uint32_t(x_row) + c * 16;
+        }
+#pragma unroll
+        for (int i = 0; i < T::W_PER; ++i) {
+            const int s = i * T::THREADS + tid, r = s / T::WC, c = (s % T::WC) ^ ((r / (8 / T::WC)) & (T::WC - 1));
+            w_off[i] = s < T::BN * T::WC ? (wr(r) - n0) * uint32_t(w_row) + c * 16 : 0;
+        }
+    }
+    const uint64_t xs_row = X == ST_X_MXFP8 ? a.k / 32 : 4ull * groups;
+    const int uwave = __builtin_amdgcn_readfirstlane(wave);
+    const bool x_scales = uwave < T::X_WAVES;
+    const __amdgpu_buffer_rsrc_t bs = rows_at(x_scales ? a.xs + m0 * xs_row : a.ws + n0 * ws_row);
+    uint32_t s_off = 0;
+    if constexpr (DIRECT && T::X_WAVES + T::W_WAVES != 0)
+        s_off = x_scales ? (xr(tid) - m0) * uint32_t(xs_row) : (wr(tid - T::X_WAVES * 64) - n0) * uint32_t(ws_row);
+    u32x4 rx[DIRECT ? 1 : T::X_PER], rw[DIRECT ? 1 : T::W_PER];      // chunks on their way through registers
     uint32_t rxs = 0, rws = 0;
-    bool in_regs = false;
 
     auto issue = [&](uint32_t step, int buf) {
         const uint64_t kb = uint64_t(step) * T::XB, wb = uint64_t(step) * T::WB;
         uint8_t* sx = lds[buf];
         uint8_t* sw = lds[buf] + T::BM * T::XB;
-        in_regs = !DIRECT || uint64_t(step + 1) * T::KS > a.k;
-        if (!in_regs) {
+        if constexpr (DIRECT) {
 #pragma unroll
-            for (int i = 0; i < T::X_PER; ++i) {
-                const int s = i * T::THREADS + tid, r = s / T::XC, c = (s % T::XC) ^ (r & 7);
-                __builtin_amdgcn_global_load_lds(
-                    (const __attribute__((address_space(1))) void*)(a.x + xr(r) * x_row + kb + c * 16),
-                    (__attribute__((address_space(3))) void*)(sx + (i * T::THREADS + wave * 64) * 16), 16, 0, 0);
-            }
+            for (int i = 0; i < T::X_PER; ++i)
+                to_lds(bx, sx + (i * T::THREADS + wave * 64) * 16, x_off[i], uint32_t(kb));
 #pragma unroll
-            for (int i = 0; i < T::W_PER; ++i) {
-                const int s = i * T::THREADS + tid, r = s / T::WC, c = (s % T::WC) ^ ((r / (8 / T::WC)) & (T::WC - 1));
-                if (T::BN * T::WC % T::THREADS == 0 || i * T::THREADS + wave * 64 < T::BN * T::WC)
-                    __builtin_amdgcn_global_load_lds(
-                        (const __attribute__((address_space(1))) void*)(a.w + wr(r) * w_row + wb + c * 16),
-                        (__attribute__((address_space(3))) void*)(sw + (i * T::THREADS + wave * 64) * 16), 16, 0, 0);
-            }
+            for (int i = 0; i < T::W_PER; ++i)
+                if (T::BN * T::WC % T::THREADS == 0 || i * T::THREADS + uwave * 64 < T::BN * T::WC)
+                    to_lds(bw, sw + (i * T::THREADS + wave * 64) * 16, w_off[i], uint32_t(wb));
         } else {
 #pragma unroll
             for (int i = 0; i < T::X_PER; ++i) {
@@ -640,30 +670,30 @@ __global__ __launch_bounds__(T::THREADS) void linear_tile(Args a) {
                     rw[i] = load_chunk(a.w + wr(r) * w_row + wb + c * 16, int64_t(w_row) - int64_t(wb + c * 16));
             }
         }
-        if constexpr (T::XSB != 0) {
+        if constexpr (DIRECT && T::X_WAVES + T::W_WAVES != 0) {
+            if (uwave < T::X_WAVES + T::W_WAVES)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                    bs, (__attribute__((address_space(3))) void*)(sw + T::BN * T::WB + wave * 256), 4, int(s_off),
+                    int(T::WSB == 2 ? step / 2 * 4 : step * 4), 0, 0);
+        }
+        if constexpr (T::XSB != 0 && !DIRECT) {
             if (tid < T::BM) {
                 if constexpr (X == ST_X_FP8_GROUP128)
                     rxs = *reinterpret_cast<const uint32_t*>(a.xs + 4 * (uint64_t(xr(tid)) * groups + step));
-                else {
-                    const uint8_t* p = a.xs + uint64_t(xr(tid)) * (a.k / 32) + step * 4ull;
-                    rxs = !in_regs ? *reinterpret_cast<const uint32_t*>(p) : load_codes(p, int64_t(a.k / 32) - step * 4ll, 4);
-                }
+                else
+                    rxs = load_codes(a.xs + uint64_t(xr(tid)) * (a.k / 32) + step * 4ull, int64_t(a.k / 32) - step * 4ll, 4);
             }
         }
-        if constexpr (T::WSB != 0) {
-            if (tid < T::BN) {
-                const uint8_t* p = a.ws + wr(tid) * ws_row + uint64_t(step) * T::WSB;
-                if (in_regs) rws = load_codes(p, int64_t(ws_row) - int64_t(step) * T::WSB, T::WSB);
-                else if constexpr (T::WSB == 4) rws = *reinterpret_cast<const uint32_t*>(p);
-                else rws = *reinterpret_cast<const uint16_t*>(p);
-            }
+        if constexpr (T::WSB != 0 && !DIRECT) {
+            if (tid < T::BN)
+                rws = load_codes(a.ws + wr(tid) * ws_row + uint64_t(step) * T::WSB, int64_t(ws_row) - int64_t(step) * T::WSB, T::WSB);
         }
     };
     // What issue() left in registers goes to LDS.
     auto commit = [&](int buf) {
-        uint8_t* sx = lds[buf];
-        uint8_t* sw = lds[buf] + T::BM * T::XB;
-        if (in_regs) {
+        if constexpr (!DIRECT) {
+            uint8_t* sx = lds[buf];
+            uint8_t* sw = lds[buf] + T::BM * T::XB;
 #pragma unroll
             for (int i = 0; i < T::X_PER; ++i) {
                 const int s = i * T::THREADS + tid;
@@ -674,14 +704,10 @@ __global__ __launch_bounds__(T::THREADS) void linear_tile(Args a) {
                 const int s = i * T::THREADS + tid;
                 if (s < T::BN * T::WC) *reinterpret_cast<u32x4*>(sw + T::w_at(s / T::WC, s % T::WC)) = rw[i];
             }
-        }
-        uint32_t* ss = reinterpret_cast<uint32_t*>(sw + T::BN * T::WB);
-        if constexpr (T::XSB != 0) {
-            if (tid < T::BM) ss[tid] = rxs;
-            ss += T::BM;
-        }
-        if constexpr (T::WSB != 0) {
-            if (tid < T::BN) ss[tid] = rws;
+            uint32_t* ss = reinterpret_cast<uint32_t*>(sw + T::BN * T::WB);
+            if (T::XSB != 0 && tid < T::BM) ss[tid] = rxs;
+            if (T::XSB != 0) ss += T::BM;
+            if (T::WSB != 0 && tid < T::BN) ss[tid] = rws;
         }
     };
 
@@ -691,14 +717,34 @@ __global__ __launch_bounds__(T::THREADS) void linear_tile(Args a) {
 #pragma unroll
         for (int j = 0; j < MT; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
 
-    if (first < last) {
-        issue(first, 0);
-        commit(0);
-    }
-    for (uint32_t step = first; step < last; ++step) {
-        const int buf = (step - first) & 1;
-        __syncthreads();       // this step's bytes are in LDS, and no wavefront reads the other buffer any more
-        if (step + 1 < last) issue(step + 1, buf ^ 1);
+    // loads of a step that this wavefront issues: BASE, one more with weight chunks left over, one more with scale words
+    constexpr int BASE = T::X_PER + T::BN * T::WC / T::THREADS;
+    const int loads = BASE + (uwave * 64 < T::BN * T::WC % T::THREADS ? 1 : 0) + (uwave < T::X_WAVES + T::W_WAVES ? 1 : 0);
+    const uint32_t count = last > first ? last - first : 0;
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i)
+        if (uint32_t(i) < count) {
+            issue(first + i, i);
+            commit(i);
+        }
+    int buf = 0;
+    for (uint32_t i = 0; i < count; ++i) {
+        const uint32_t step = first + i;
+        // This step's bytes are in LDS, and no wavefront reads the buffer that is filled next any more.  The loads of the S - 2
+        // steps behind this one may still be on their way (they end in the order they were issued).
+        if constexpr (DIRECT) {
+            if (S == 2 || count - i <= S - 2) __builtin_amdgcn_s_waitcnt(wait_vmem(0));
+            else if (loads == BASE) __builtin_amdgcn_s_waitcnt(wait_vmem((S - 2) * BASE));
+            else if (loads == BASE + 1) __builtin_amdgcn_s_waitcnt(wait_vmem((S - 2) * (BASE + 1)));
+            else __builtin_amdgcn_s_waitcnt(wait_vmem((S - 2) * (BASE + 2)));
+            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "singlethread");
+            __builtin_amdgcn_s_barrier();
+            __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "singlethread");
+        } else {
+            __syncthreads();
+        }
+        const int fill = buf + S - 1 < S ? buf + S - 1 : buf - 1;
+        if (i + S - 1 < count) issue(step + S - 1, fill);
         const uint8_t* sx = lds[buf];
         const uint8_t* sw = sx + T::BM * T::XB;
         const uint8_t* sxs = sw + T::BN * T::WB;
@@ -706,56 +752,58 @@ __global__ __launch_bounds__(T::THREADS) void linear_tile(Args a) {
         float gs = 0.0f;       // the weight's scale of this wavefront's columns and this group of K
         if constexpr (T::GROUPED) {
             const uint32_t nb = (n0 + wn * (NT * 16)) / 128, lastb = (a.n - 1) / 128;
-            gs = reinterpret_cast<const float*>(a.ws)[uint64_t(nb < lastb ? nb : lastb) * groups + uint64_t(step) * T::KS / 128];
+            // a scalar load: a vector load would wait for the steps on their way
+            const uint32_t gi = __builtin_amdgcn_readfirstlane((nb < lastb ? nb : lastb) * groups + step * T::KS / 128);
+            gs = ld_uniform_f32(a.ws + 4ull * gi);
         }
         if constexpr (!T::F8) {
             using D = Dense<X, WK>;
             // 64 of K at a time: lane group q holds 16q..16q+15 of them, 8 for each of two instructions
 #pragma unroll
             for (int h = 0; h < T::KS / 64; ++h) {
-                u32x4 xv[MT][2], xl[D::SPLIT ? MT : 1][2];
+                // the weight's operands stay, x's pass by
+                u32x4 wv[NT][2];
 #pragma unroll
-                for (int j = 0; j < MT; ++j) {
-                    const int r = (wm * MT + j) * 16 + row;
-                    if constexpr (T::Q) {
-                        const u32x4 c = *reinterpret_cast<const u32x4*>(sx + T::x_at(r, q + 4 * h));
-                        const float s = X == ST_X_MXFP8 ? scale_of<ST_KIND_MXFP8>(sxs[r * 4 + 2 * h + (q >> 1)]) : 1.0f;
-                        xv[j][0] = codes8<false, ST_KIND_MXFP8>(c.x, c.y, s);
-                        xv[j][1] = codes8<false, ST_KIND_MXFP8>(c.z, c.w, s);
+                for (int i = 0; i < NT; ++i) {
+                    const int r = (wn * NT + i) * 16 + row;
+                    const float s = T::WSB ? scale_of<WK>(sws[r * 4 + (WK == ST_KIND_NVFP4 ? q : 2 * (T::WSB == 2 ? (DIRECT ? step & 1 : 0) : h) + (q >> 1))]) : 1.0f;
+                    if constexpr (T::FP4) {
+                        const u32x2 c = *reinterpret_cast<const u32x2*>(sw + T::w_at(r, 2 * h + (q >> 1)) + (q & 1) * 8);
+                        wv[i][0] = codes8<D::F16, WK>(c.x, 0, s);
+                        wv[i][1] = codes8<D::F16, WK>(c.y, 0, s);
                     } else {
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const u32x4 v = *reinterpret_cast<const u32x4*>(sx + T::x_at(r, 2 * q + i));
-                            if constexpr (D::SPLIT) split_f16(v, xv[j][i], xl[j][i]);
-                            else xv[j][i] = v;
-                        }
+                        const u32x4 c = *reinterpret_cast<const u32x4*>(sw + T::w_at(r, q + 4 * h));
+                        wv[i][0] = codes8<D::F16, WK>(c.x, c.y, s);
+                        wv[i][1] = codes8<D::F16, WK>(c.z, c.w, s);
                     }
                 }
                 // GROUPED: sums of 128 of K start at zero and are scaled into acc at the end
                 const bool begin = T::GROUPED && (T::Q ? h == 0 : (step & 1) == 0 || step == first);
-                const bool end = T::GROUPED && (T::Q ? h == 1 : (step & 1) == 1 || step + 1 == last);
+                const bool end = T::GROUPED && (T::Q ? h == 1 : (step & 1) == 1 || i + 1 == count);
 #pragma unroll
-                for (int i = 0; i < NT; ++i) {
-                    const int r = (wn * NT + i) * 16 + row;
-                    u32x4 w0, w1;
-                    const float s = T::WSB ? scale_of<WK>(sws[r * 4 + (WK == ST_KIND_NVFP4 ? q : 2 * h + (q >> 1))]) : 1.0f;
-                    if constexpr (T::FP4) {
-                        const u32x2 c = *reinterpret_cast<const u32x2*>(sw + T::w_at(r, 2 * h + (q >> 1)) + (q & 1) * 8);
-                        w0 = codes8<D::F16, WK>(c.x, 0, s);
-                        w1 = codes8<D::F16, WK>(c.y, 0, s);
+                for (int j = 0; j < MT; ++j) {
+                    const int r = (wm * MT + j) * 16 + row;
+                    u32x4 xv[2], xl[2];
+                    if constexpr (T::Q) {
+                        const u32x4 c = *reinterpret_cast<const u32x4*>(sx + T::x_at(r, q + 4 * h));
+                        const float s = X == ST_X_MXFP8 ? scale_of<ST_KIND_MXFP8>(sxs[r * 4 + 2 * h + (q >> 1)]) : 1.0f;
+                        xv[0] = codes8<false, ST_KIND_MXFP8>(c.x, c.y, s);
+                        xv[1] = codes8<false, ST_KIND_MXFP8>(c.z, c.w, s);
                     } else {
-                        const u32x4 c = *reinterpret_cast<const u32x4*>(sw + T::w_at(r, q + 4 * h));
-                        w0 = codes8<D::F16, WK>(c.x, c.y, s);
-                        w1 = codes8<D::F16, WK>(c.z, c.w, s);
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            xv[i] = *reinterpret_cast<const u32x4*>(sx + T::x_at(r, 2 * q + i));
+                            if constexpr (D::SPLIT) split_f16(xv[i], xv[i], xl[i]);
+                        }
                     }
 #pragma unroll
-                    for (int j = 0; j < MT; ++j) {
+                    for (int i = 0; i < NT; ++i) {
                         f32x4 c = T::GROUPED ? (begin ? f32x4{0, 0, 0, 0} : part[T::GROUPED ? i : 0][T::GROUPED ? j : 0]) : acc[i][j];
-                        c = mfma32<D::F16>(w0, xv[j][0], c);
-                        c = mfma32<D::F16>(w1, xv[j][1], c);
+                        c = mfma32<D::F16>(wv[i][0], xv[0], c);
+                        c = mfma32<D::F16>(wv[i][1], xv[1], c);
                         if constexpr (D::SPLIT) {
-                            c = mfma32<false>(w0, xl[j][0], c);
-                            c = mfma32<false>(w1, xl[j][1], c);
+                            c = mfma32<false>(wv[i][0], xl[0], c);
+                            c = mfma32<false>(wv[i][1], xl[1], c);
                         }
                         if constexpr (T::GROUPED) part[i][j] = c;
                         else acc[i][j] = c;
@@ -779,61 +827,86 @@ __global__ __launch_bounds__(T::THREADS) void linear_tile(Args a) {
         } else {
             // k of lane group q in a 16x16x128 operand: e4m3 16q..16q+15 and 64+16q..64+16q+15, e2m1 32q..32q+31;
             // the scale of lane group q belongs to 32q..32q+31
-            i32x8 xv[MT];
-            int xe[MT];
-            float xf[MT];
-#pragma unroll
-            for (int j = 0; j < MT; ++j) {
-                const int r = (wm * MT + j) * 16 + row;
-                const u32x4 lo = *reinterpret_cast<const u32x4*>(sx + T::x_at(r, q));
-                const u32x4 hi = *reinterpret_cast<const u32x4*>(sx + T::x_at(r, q + 4));
-                xv[j] = i32x8{int(lo.x), int(lo.y), int(lo.z), int(lo.w), int(hi.x), int(hi.y), int(hi.z), int(hi.w)};
-                xe[j] = X == ST_X_MXFP8 ? sxs[r * 4 + q] : 127;
-                if constexpr (T::GROUPED) xf[j] = reinterpret_cast<const float*>(sxs)[r] * gs;
-            }
+            i32x8 wv[NT];
+            int we[NT];
 #pragma unroll
             for (int i = 0; i < NT; ++i) {
                 const int r = (wn * NT + i) * 16 + row;
-                i32x8 wv;
                 const u32x4 lo = *reinterpret_cast<const u32x4*>(sw + T::w_at(r, q));
                 if constexpr (T::FP4) {
-                    wv = i32x8{int(lo.x), int(lo.y), int(lo.z), int(lo.w), 0, 0, 0, 0};
+                    wv[i] = i32x8{int(lo.x), int(lo.y), int(lo.z), int(lo.w), 0, 0, 0, 0};
                 } else {
                     const u32x4 hi = *reinterpret_cast<const u32x4*>(sw + T::w_at(r, q + 4));
-                    wv = i32x8{int(lo.x), int(lo.y), int(lo.z), int(lo.w), int(hi.x), int(hi.y), int(hi.z), int(hi.w)};
+                    wv[i] = i32x8{int(lo.x), int(lo.y), int(lo.z), int(lo.w), int(hi.x), int(hi.y), int(hi.z), int(hi.w)};
                 }
-                const int we = T::WSB ? sws[r * 4 + q] : 127;
+                we[i] = T::WSB ? sws[r * 4 + q] : 127;
+            }
+            // x's operand of the next 16 rows is on its way from LDS while this one multiplies
+            i32x8 xn;
+            int en = 127;
+            float fn = 0.0f;
+            auto next = [&](int j) {
+                const int r = (wm * MT + j) * 16 + row;
+                const u32x4 lo = *reinterpret_cast<const u32x4*>(sx + T::x_at(r, q));
+                const u32x4 hi = *reinterpret_cast<const u32x4*>(sx + T::x_at(r, q + 4));
+                xn = i32x8{int(lo.x), int(lo.y), int(lo.z), int(lo.w), int(hi.x), int(hi.y), int(hi.z), int(hi.w)};
+                if constexpr (X == ST_X_MXFP8) en = sxs[r * 4 + q];
+                if constexpr (T::GROUPED) fn = reinterpret_cast<const float*>(sxs)[r];
+            };
+            next(0);
 #pragma unroll
-                for (int j = 0; j < MT; ++j) {
+            for (int j = 0; j < MT; ++j) {
+                const i32x8 xv = xn;
+                const int xe = en;
+                const float xf = fn * gs;
+                if (j + 1 < MT) next(j + 1);
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
                     if constexpr (T::GROUPED) {
-                        const f32x4 p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wv, xv[j], f32x4{0, 0, 0, 0}, 0, 0, 0,
-                                                                                         127, 0, 127);
+                        const f32x4 p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wv[i], xv, f32x4{0, 0, 0, 0}, 0, 0, 0, 127, 0, 127);
 #pragma unroll
-                        for (int t = 0; t < 4; ++t) acc[i][j][t] = __builtin_fmaf(p[t], xf[j], acc[i][j][t]);
+                        for (int t = 0; t < 4; ++t) acc[i][j][t] = __builtin_fmaf(p[t], xf, acc[i][j][t]);
                     } else {
-                        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wv, xv[j], acc[i][j], T::FP4 ? 4 : 0, 0, 0,
-                                                                                     we, 0, xe[j]);
+                        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wv[i], xv, acc[i][j], T::FP4 ? 4 : 0, 0, 0, we[i], 0, xe);
                     }
                 }
+                __builtin_amdgcn_sched_barrier(0);
             }
         }
-        if (step + 1 < last) commit(buf ^ 1);
+        if (i + S - 1 < count) commit(fill);
+        buf = buf + 1 < S ? buf + 1 : 0;
     }
+    // Two 16-row groups at a time go through LDS, so that a row's columns are stored together and the epilogue's code, with its
+    // choices of type and activation, is there once per two groups (unrolled over all of them it outgrew the instruction cache:
+    // 760 us became 2740 for 8192 rows through MXFP8 [12288, 4096] in tiles of 256).
+    constexpr int PITCH = NT * 16 + 4, PER = 64 / (NT * 4);      // floats of a row in LDS; rows a wavefront stores together
+    static_assert(T::WAVES_M * T::WAVES_N * 32 * PITCH * 4 <= 2 * T::STAGE, "the epilogue's rows fit the stages' LDS");
+    float* mine = reinterpret_cast<float*>(&lds[0][0]) + wave * 32 * PITCH;
+    __syncthreads();
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
+    for (int j0 = 0; j0 < MT; j0 += 2) {
 #pragma unroll
-        for (int j = 0; j < MT; ++j)
-            emit<X, WK>(a, split, m0 + (wm * MT + j) * 16 + row, n0 + (wn * NT + i) * 16 + 4 * q, acc[i][j]);
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+                *reinterpret_cast<f32x4*>(mine + (j * 16 + row) * PITCH + i * 16 + 4 * q) = acc[i][j0 + j];
+#pragma unroll 1
+        for (int r = lane / (NT * 4); r < 32; r += PER) {
+            const int c = lane % (NT * 4) * 4;
+            const f32x4 v = *reinterpret_cast<const f32x4*>(mine + r * PITCH + c);
+            emit<X, WK>(a, split, m0 + (wm * MT + j0) * 16 + r, n0 + wn * (NT * 16) + c, v);
+        }
+    }
 }
 
 // ------------------------------------------------------------------------- launches
 
-template <int X, int WK, int BM, int BN, bool F8>
-void launch_tile(const Args& a, bool direct, hipStream_t s) {
-    using T = Tile<X, WK, BM, BN, 2, 2, F8>;
-    const dim3 grid(a.tiles_m * a.tiles_n, a.splits);
-    if (direct) hipLaunchKernelGGL((linear_tile<T, true>), grid, dim3(T::THREADS), 0, s, a);
-    else hipLaunchKernelGGL((linear_tile<T, false>), grid, dim3(T::THREADS), 0, s, a);
+template <class T, bool ANY>
+void launch_tile(const Args& a, const Plan& p, hipStream_t s) {
+    const dim3 grid(a.tiles_m * a.tiles_n, a.splits), block(T::THREADS);
+    if (p.direct) hipLaunchKernelGGL((linear_tile<T, true>), grid, block, 0, s, a);
+    else if constexpr (ANY) hipLaunchKernelGGL((linear_tile<T, false>), grid, block, 0, s, a);
 }
 
 template <int X, int WK>
@@ -845,9 +918,15 @@ void launch(const Args& a, const Plan& p, hipStream_t s) {
     if (p.few) {
         const dim3 grid((a.n + 16 * Few<X, WK>::NT - 1) / (16 * Few<X, WK>::NT), a.splits), block(64 * p.waves);
         hipLaunchKernelGGL((linear_few<Few<X, WK>>), grid, block, 0, s, a);
-    } else if (p.bm == 64) launch_tile<X, WK, 64, 64, false>(a, p.direct, s);
-    else if (!is_q(X) || !p.f8) launch_tile<X, WK, 128, 128, false>(a, p.direct, s);
-    else if constexpr (is_q(X)) launch_tile<X, WK, 128, 128, true>(a, p.direct, s);
+    } else if (p.bm == 64) {
+        launch_tile<Tile<X, WK, 64, 64, 2, 2, false, 4>, true>(a, p, s);
+    } else if (p.bm == 128) {
+        if constexpr (is_q(X))
+            if (p.f8) launch_tile<Tile<X, WK, 128, 128, 2, 2, true, 2>, true>(a, p, s);
+        if (!is_q(X) || !p.f8) launch_tile<Tile<X, WK, 128, 128, 2, 2, false, 2>, true>(a, p, s);
+    } else if constexpr (is_q(X)) {
+        launch_tile<Tile<X, WK, 256, 256, 2, 4, true, 2>, false>(a, p, s);
+    }
     if (a.part) {
         const uint64_t items = uint64_t((a.n + 3) / 4) * a.m;
         hipLaunchKernelGGL((linear_join<X, WK>), dim3(uint32_t((items + 255) / 256)), dim3(256), 0, s, a);
