@@ -3,11 +3,16 @@
 //   rms_norm  h = x + residual;  y = h / sqrt(mean(h^2) + eps) * weight, in the output type or encoded like v
 // with s = amax / 448 per row or per 128 columns (fp32), or the power of two at or above it per 32 (E8M0).
 //
-// Arithmetic.  A code changes by a whole e4m3 step where v / s passes the middle between two codes, so what
-// decides it is kept in fp64: the sum of squares, y, amax, and the quotient, which is then rounded once, to nearest
-// even.  fp64 runs at the fp32 rate of this GPU's vector units, and these kernels wait for memory.  A quotient within
-// 2^-40 of a middle is taken as the middle itself: v and s have at most 24 bits each and a middle has 5, so an
-// inexact quotient differs from it by more than 2^-30, and what is nearer is the error of multiplying by 1 / s.
+// Arithmetic.  A code changes by a whole e4m3 step where v / s passes the middle between two codes, so which side of a middle
+// the quotient lies on is decided exactly:
+//  * encode without a gate: v, and so amax and s, are exact in fp32.  The fp32 quotient names the middle that is nearest, and the
+//    sign of fma(-middle, s, v), which is exact, says on which side of it v / s lies.
+//  * a gate or a norm: v, amax and the quotient are kept in fp64 (the sum of squares too).  For MX, whose scale is a power of two, v
+//    in fp32 decides unless it comes within 2^-19 of a middle or amax that near to a power of two's edge; then the
+//    wavefront does its chunk again in fp64 (about one in 100).
+// fp64 quotients within 2^-40 of a middle are taken as the middle itself: v and s have at most 24 bits each and a middle has
+// 5, so an inexact quotient of two such numbers differs from it by more than 2^-30, and what is nearer is the error of
+// multiplying by 1 / s.
 //
 // Both are bound by memory: every input is read once and stays in registers (chunks of 8 elements per lane, 16-byte
 // loads) while the row's sums and maxima are taken; groups of 128 and 32 columns are 16 and 4 lanes.
@@ -115,6 +120,41 @@ __device__ __forceinline__ float quotient(double v, double inv) {
     return finite(v) ? c : __builtin_nanf("");
 }
 
+// e4m3 code of v / s for exact fp32 v >= 0 and s, with inv = 1 / s to a few ulp.  The codes' middles lie at the mantissa's fourth
+// bit; below 2^-6 codes are 2^-9 apart, as in the binade above it, so the quotient is looked at with 2^-6 added.
+__device__ __forceinline__ uint32_t code_exact(float v, float s, float inv) {
+    const float q = __builtin_fminf(v * inv, kE4m3Max);
+    const bool sub = q < 0.015625f;
+    const float lift = sub ? 0.015625f : 0.0f;
+    const uint32_t z = as_u32(q + lift);
+    const float middle = as_f32((z & 0xFFF00000u) | 0x00080000u) - lift;
+    const float r = __builtin_fmaf(-middle, s, v);
+    const uint32_t c = (z >> 20) - (sub ? 968u : 960u);        // 2^-6 has code 8 and exponent field 121 = 968 / 8
+    const uint32_t up = r > 0.0f || (r == 0.0f && (c & 1)) ? 1u : 0u;
+    const uint32_t code = c + up;
+    return code < 0x7Eu ? code : 0x7Eu;
+}
+// Eight codes of exact fp32 values.
+__device__ __forceinline__ void codes_exact(const float* v, float s, float inv, uint32_t& lo, uint32_t& hi) {
+    lo = hi = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float m = __builtin_fabsf(v[i]);
+        const uint32_t c = (m <= 3.4028234663852886e38f ? code_exact(m, s, inv) : 0x7Fu) | (as_u32(v[i]) >> 24 & 0x80u);
+        (i < 4 ? lo : hi) |= c << (8 * (i & 3));
+    }
+}
+__device__ __forceinline__ float finite_abs(float v) {
+    const float m = __builtin_fabsf(v);
+    return m <= 3.4028234663852886e38f ? m : 0.0f;
+}
+template <int LANES>
+__device__ __forceinline__ float max_over(float v) {
+#pragma unroll
+    for (int o = 1; o < LANES; o *= 2) v = __builtin_fmaxf(v, __shfl_xor(v, o));
+    return v;
+}
+
 __device__ __forceinline__ uint32_t pack4(float a, float b, float c, float d) {
     int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
     return uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true));
@@ -135,8 +175,7 @@ __device__ __forceinline__ double sum_over(double v) {
 
 // Codes of eight values to columns [col, col + 8) of a row of d.
 template <bool VEC>
-__device__ __forceinline__ void store_codes(uint8_t* row, uint32_t col, uint32_t d, const float* q) {
-    const uint32_t lo = pack4(q[0], q[1], q[2], q[3]), hi = pack4(q[4], q[5], q[6], q[7]);
+__device__ __forceinline__ void store_codes(uint8_t* row, uint32_t col, uint32_t d, uint32_t lo, uint32_t hi) {
     if constexpr (VEC) {
         if (col < d) *reinterpret_cast<u32x2*>(row + col) = u32x2{lo, hi};
     } else {
@@ -145,68 +184,124 @@ __device__ __forceinline__ void store_codes(uint8_t* row, uint32_t col, uint32_t
     }
 }
 
-// Eight values of a chunk whose group is a few neighbouring lanes (128 or 32 columns): amax, scale and codes.
-template <uint32_t KIND, bool VEC>
-__device__ __forceinline__ void encode_group(const Args& a, uint64_t row, uint32_t col, const double* v) {
-    constexpr int LANES = KIND == ST_X_MXFP8 ? 4 : 16;
-    double amax = 0.0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) amax = __builtin_fmax(amax, finite(v[i]) ? __builtin_fabs(v[i]) : 0.0);
-    const Scale<KIND> s(max_over<LANES>(amax));
-    float q[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = quotient(v[i], s.inv);
-    store_codes<VEC>(a.out + row * a.d, col, a.d, q);
-    if (threadIdx.x % LANES == 0 && col < a.d) {
-        if constexpr (KIND == ST_X_MXFP8) a.scale[row * (a.d / 32) + col / 32] = uint8_t(s.bits);
-        else reinterpret_cast<uint32_t*>(a.scale)[row * ((a.d + 127) / 128) + col / 128] = s.bits;
+// A group's scale, by one lane of it.
+template <uint32_t KIND>
+__device__ __forceinline__ void store_scale(const Args& a, uint64_t row, uint32_t col, uint32_t bits) {
+    if (threadIdx.x % (KIND == ST_X_MXFP8 ? 4 : 16) == 0 && col < a.d) {
+        if constexpr (KIND == ST_X_MXFP8) a.scale[row * (a.d / 32) + col / 32] = uint8_t(bits);
+        else reinterpret_cast<uint32_t*>(a.scale)[row * ((a.d + 127) / 128) + col / 128] = bits;
     }
+}
+
+// Eight exact fp32 values of a chunk whose group is a few neighbouring lanes (128 or 32 columns): amax, scale and codes.
+template <uint32_t KIND, bool VEC>
+__device__ __forceinline__ void encode_exact(const Args& a, uint64_t row, uint32_t col, const float* v) {
+    float amax = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) amax = __builtin_fmaxf(amax, finite_abs(v[i]));
+    const Scale<KIND> s(double(max_over<(KIND == ST_X_MXFP8 ? 4 : 16)>(amax)));
+    uint32_t lo, hi;
+    codes_exact(v, KIND == ST_X_MXFP8 ? float(1.0 / s.inv) : as_f32(s.bits), float(s.inv), lo, hi);
+    store_codes<VEC>(a.out + row * a.d, col, a.d, lo, hi);
+    store_scale<KIND>(a, row, col, s.bits);
+}
+
+// The same for values known in fp64 (wide(v)), and to a few 2^-24 in fp32 (v).
+template <uint32_t KIND, bool VEC, class Wide>
+__device__ __forceinline__ void encode_group(const Args& a, uint64_t row, uint32_t col, const float* v, Wide wide) {
+    constexpr int LANES = KIND == ST_X_MXFP8 ? 4 : 16;
+    uint32_t lo, hi, bits;
+    bool again = true;
+    if constexpr (KIND == ST_X_MXFP8) {
+        float amax = 0.0f;
+        bool odd = false;       // something that fp32 does not settle
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float m = __builtin_fabsf(v[i]);
+            odd |= !(m <= 3.4028234663852886e38f);
+            amax = __builtin_fmaxf(amax, m);
+        }
+        amax = max_over<4>(amax);
+        // amax = f 2^e: its power of two changes at f = 1.75; tiny groups are left to fp64
+        odd |= ((as_u32(amax) + 32 - 0x600000u) & 0x7FFFFFu) < 64 || (amax < 1e-30f && amax != 0.0f);
+        const Scale<KIND> s((double(amax)));
+        const float inv = float(s.inv);
+        bits = s.bits;
+        float q[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            q[i] = v[i] * inv;
+            const float m = __builtin_fabsf(q[i]);
+            const uint32_t z = as_u32(m < 0.015625f ? m + 0.015625f : m);
+            odd |= ((z + 32 - 0x80000u) & 0xFFFFFu) < 64;
+        }
+        lo = pack4(q[0], q[1], q[2], q[3]);
+        hi = pack4(q[4], q[5], q[6], q[7]);
+        again = __any(odd);
+    }
+    if (again) {
+        double w[8], amax = 0.0;
+        wide(w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) amax = __builtin_fmax(amax, finite(w[i]) ? __builtin_fabs(w[i]) : 0.0);
+        const Scale<KIND> s(max_over<LANES>(amax));
+        float q[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[i] = quotient(w[i], s.inv);
+        lo = pack4(q[0], q[1], q[2], q[3]);
+        hi = pack4(q[4], q[5], q[6], q[7]);
+        bits = s.bits;
+    }
+    store_codes<VEC>(a.out + row * a.d, col, a.d, lo, hi);
+    store_scale<KIND>(a, row, col, bits);
 }
 
 // ------------------------------------------------------------------------- kernels
 
-// encode by groups of 128 or 32 columns: no row structure, a lane per chunk of 8.
-template <uint32_t E, uint32_t KIND, bool VEC>
-__global__ __launch_bounds__(kThreads) void encode_groups(Args a, uint32_t per_row) {
-    // chunks of a row rounded up to whole groups of 16, so that no group crosses rows
-    const uint64_t i = uint64_t(blockIdx.x) * kThreads + threadIdx.x;
-    uint64_t row = i / per_row;
-    uint32_t col = uint32_t(i % per_row) * 8;
-    if (row >= a.m) {
-        row = a.m - 1;
-        col = per_row * 8;      // past the row: loads zeros, stores nothing
-    }
-    const Raw<E> x = load8<E, VEC>(a.x + row * a.x_pitch * kSize<E>, col, a.d);
-    double v[8];
-    if (a.b) {
-        const Raw<E> g = load8<E, VEC>(a.b + row * a.b_pitch * kSize<E>, col, a.d);
+// encode by groups of 128 or 32 columns: no row structure, a lane per chunk of 8.  grid: chunks of a row (whole groups of 16
+// lanes, so that no group crosses rows) by rows.
+template <uint32_t E, uint32_t KIND, bool VEC, bool GATE>
+__global__ __launch_bounds__(kThreads) void encode_groups(Args a, uint32_t rows_at_once) {
+    const uint32_t col = (blockIdx.x * kThreads + threadIdx.x) * 8;      // past the row: loads zeros, stores nothing
+    for (uint64_t row = blockIdx.y; row < a.m; row += rows_at_once) {
+        const Raw<E> x = load8<E, VEC>(a.x + row * a.x_pitch * kSize<E>, col, a.d);
+        float v[8];
+        if constexpr (GATE) {
+            const Raw<E> g = load8<E, VEC>(a.b + row * a.b_pitch * kSize<E>, col, a.d);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = silu64(double(g.at(k))) * double(x.at(k));
-    } else {
+            for (int k = 0; k < 8; ++k) v[k] = silu(g.at(k)) * x.at(k);
+            encode_group<KIND, VEC>(a, row, col, v, [&](double* w) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = double(x.at(k));
+                for (int k = 0; k < 8; ++k) w[k] = silu64(double(g.at(k))) * double(x.at(k));
+            });
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = x.at(k);
+            encode_exact<KIND, VEC>(a, row, col, v);
+        }
     }
-    encode_group<KIND, VEC>(a, row, col, v);
 }
 
 enum { kNorm = 0, kEncodeRow = 1 };
 
 // One row per TPR lanes; CH chunks per lane kept in registers, or with CH == 0 any number, read again in each
 // pass.  NORM: KIND 0 writes y, else its codes.  kEncodeRow: one scale per row.
-template <int OP, uint32_t E, uint32_t KIND, bool VEC, int TPR, int CH>
-__global__ __launch_bounds__(kThreads) void rows(Args a) {
-    __shared__ double shared[2][kThreads / 64];
-    const uint64_t row = uint64_t(blockIdx.x) * (kThreads / TPR) + threadIdx.x / TPR;
+// B: there is a residual or a gate.
+template <int OP, uint32_t E, uint32_t KIND, bool VEC, int TPR, int CH, bool B>
+__global__ __launch_bounds__(TPR < int(kThreads) ? kThreads : TPR) void rows(Args a) {
+    __shared__ double shared[2][TPR < 64 ? 1 : TPR / 64];
+    constexpr uint32_t PER = TPR < int(kThreads) ? kThreads / TPR : 1;      // rows of a workgroup
+    const uint64_t row = uint64_t(blockIdx.x) * PER + threadIdx.x / TPR;
     const uint32_t t = threadIdx.x % TPR, d = a.d;
-    const bool live = row < a.m;       // TPR < kThreads: the last workgroup may hold fewer rows
+    const bool live = row < a.m;       // the last workgroup may hold fewer rows
     const uint32_t dd = live ? d : 0;  // a row that is not there is empty
     const uint8_t* px = a.x + (live ? row : 0) * a.x_pitch * kSize<E>;
-    const uint8_t* pb = a.b ? a.b + (live ? row : 0) * a.b_pitch * kSize<E> : nullptr;
+    const uint8_t* pb = a.b + (live ? row : 0) * a.b_pitch * kSize<E>;
     constexpr int N = CH ? CH : 1;
-    Raw<E> rx[N], rb[N];
+    Raw<E> rx[N], rb[B ? N : 1];
     auto fetch = [&](int c, uint32_t col) {
         rx[c] = load8<E, VEC>(px, col, dd);
-        if (pb) rb[c] = load8<E, VEC>(pb, col, dd);
+        if constexpr (B) rb[c] = load8<E, VEC>(pb, col, dd);
     };
     if constexpr (CH != 0) {
 #pragma unroll
@@ -237,7 +332,10 @@ __global__ __launch_bounds__(kThreads) void rows(Args a) {
         return v;
     };
     // h = x + residual in fp32
-    auto h_of = [&](int c, int i) { return pb ? rx[c].at(i) + rb[c].at(i) : rx[c].at(i); };
+    auto h_of = [&](int c, int i) {
+        if constexpr (B) return rx[c].at(i) + rb[c].at(i);
+        else return rx[c].at(i);
+    };
     double inv = 0.0;
     if constexpr (OP == kNorm) {
         double ss = 0.0;
@@ -248,7 +346,7 @@ __global__ __launch_bounds__(kThreads) void rows(Args a) {
                 ss = __builtin_fma(h, h, ss);
             }
         });
-        ss = reduce(sum_over<(TPR < 64 ? TPR : 64)>(ss), 0, [](double p, double q) { return p + q; });
+        ss = reduce(sum_over<64>(ss), 0, [](double p, double q) { return p + q; });
         inv = 1.0 / sqrt(ss / double(d) + a.eps);
     }
     // the weight of columns [col, col + 8); its elements may have any type
@@ -279,8 +377,8 @@ __global__ __launch_bounds__(kThreads) void rows(Args a) {
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const double x = double(rx[c].at(i));
-                v[i] = pb ? silu64(double(rb[c].at(i))) * x : x;
+                v[i] = double(rx[c].at(i));
+                if constexpr (B) v[i] *= silu64(double(rb[c].at(i)));
             }
         }
     };
@@ -319,6 +417,24 @@ __global__ __launch_bounds__(kThreads) void rows(Args a) {
             }
         });
     } else if constexpr (KIND == ST_X_FP8_ROW) {
+        if constexpr (OP == kEncodeRow && !B) {
+            float amax = 0.0f;
+            each([&](int c, uint32_t) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) amax = __builtin_fmaxf(amax, finite_abs(rx[c].at(i)));
+            });
+            const Scale<KIND> s(reduce(double(max_over<64>(amax)), 1, [](double p, double q) { return __builtin_fmax(p, q); }));
+            if (t == 0 && live) reinterpret_cast<uint32_t*>(a.scale)[row] = s.bits;
+            const float inv = float(s.inv);
+            each([&](int c, uint32_t col) {
+                float v[8];
+                uint32_t lo, hi;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = rx[c].at(i);
+                codes_exact(v, as_f32(s.bits), inv, lo, hi);
+                store_codes<VEC>(a.out + row * d, col, dd, lo, hi);
+            });
+        } else {
         double amax = 0.0;
         each([&](int c, uint32_t col) {
             double v[8];
@@ -326,7 +442,7 @@ __global__ __launch_bounds__(kThreads) void rows(Args a) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) amax = __builtin_fmax(amax, finite(v[i]) ? __builtin_fabs(v[i]) : 0.0);
         });
-        amax = reduce(max_over<(TPR < 64 ? TPR : 64)>(amax), 1, [](double p, double q) { return __builtin_fmax(p, q); });
+        amax = reduce(max_over<64>(amax), 1, [](double p, double q) { return __builtin_fmax(p, q); });
         const Scale<KIND> s(amax);
         if (t == 0 && live) reinterpret_cast<uint32_t*>(a.scale)[row] = s.bits;
         each([&](int c, uint32_t col) {
@@ -336,43 +452,55 @@ __global__ __launch_bounds__(kThreads) void rows(Args a) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) q[i] = quotient(v[i], s.inv);
             store_h(c, col);
-            store_codes<VEC>(a.out + row * d, col, dd, q);
+            store_codes<VEC>(a.out + row * d, col, dd, pack4(q[0], q[1], q[2], q[3]), pack4(q[4], q[5], q[6], q[7]));
         });
+        }
     } else {
+        const float s = float(inv);
         each([&](int c, uint32_t col) {
-            double v[8];
-            values(c, col, v);
+            float w[8], v[8];
+            weight(col, w);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = h_of(c, i) * s * w[i];
             store_h(c, col);
             // lanes of a row that is not there take part in the reductions and store nothing
-            encode_group<KIND, VEC>(a, row, live ? col : (d + 7) / 8 * 8, v);
+            encode_group<KIND, VEC>(a, row, live ? col : (d + 7) / 8 * 8, v, [&](double* y) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) y[i] = double(h_of(c, i)) * inv * double(w[i]);
+            });
         });
     }
 }
 
 // ------------------------------------------------------------------------- launches
 
-template <int OP, uint32_t E, uint32_t KIND>
+template <int OP, uint32_t E, uint32_t KIND, bool B>
 void launch_rows(const Args& a, bool vec, hipStream_t s) {
     const uint32_t chunks = (a.d + 7) / 8;
-    auto go = [&](auto kernel, uint32_t per_block) {
-        hipLaunchKernelGGL(kernel, dim3(uint32_t((a.m + per_block - 1) / per_block)), dim3(kThreads), 0, s, a);
+    auto go = [&](auto kernel, uint32_t threads, uint32_t per_block) {
+        hipLaunchKernelGGL(kernel, dim3(uint32_t((a.m + per_block - 1) / per_block)), dim3(threads), 0, s, a);
     };
     // rows that are not whole aligned chunks, or do not fit the registers, are read again in each pass
-    if (!vec || chunks > kThreads * 16 || (E == ST_OUT_F32 && chunks > kThreads * 8)) go(rows<OP, E, KIND, false, 256, 0>, 1);
-    else if (chunks <= 64) go(rows<OP, E, KIND, true, 64, 1>, 4);
-    else if (chunks <= 256) go(rows<OP, E, KIND, true, 256, 1>, 1);
-    else if (chunks <= 512) go(rows<OP, E, KIND, true, 256, 2>, 1);
-    else if (chunks <= 1024) go(rows<OP, E, KIND, true, 256, 4>, 1);
-    else if (chunks <= 2048) go(rows<OP, E, KIND, true, 256, 8>, 1);
-    else if constexpr (E != ST_OUT_F32) go(rows<OP, E, KIND, true, 256, 16>, 1);
+    if (!vec || chunks > 4096 || (E == ST_OUT_F32 && chunks > 2048)) go(rows<OP, E, KIND, false, 256, 0, B>, 256, 1);
+    else if (chunks <= 64) go(rows<OP, E, KIND, true, 64, 1, B>, 256, 4);
+    else if (chunks <= 256) go(rows<OP, E, KIND, true, 256, 1, B>, 256, 1);
+    else if (chunks <= 512) go(rows<OP, E, KIND, true, 256, 2, B>, 256, 1);
+    else if (chunks <= 1024) go(rows<OP, E, KIND, true, 256, 4, B>, 256, 1);
+    else if (chunks <= 2048) go(rows<OP, E, KIND, true, 512, 4, B>, 512, 1);
+    else if constexpr (E != ST_OUT_F32) go(rows<OP, E, KIND, true, 512, 8, B>, 512, 1);
+}
+template <int OP, uint32_t E, uint32_t KIND>
+void launch_rows(const Args& a, bool vec, hipStream_t s) {
+    a.b ? launch_rows<OP, E, KIND, true>(a, vec, s) : launch_rows<OP, E, KIND, false>(a, vec, s);
 }
 
 template <uint32_t E, uint32_t KIND>
 void launch_groups(const Args& a, bool vec, hipStream_t s) {
-    const uint32_t per_row = (a.d + 127) / 128 * 16;
-    const uint64_t blocks = (a.m * per_row + kThreads - 1) / kThreads;
-    if (vec) hipLaunchKernelGGL((encode_groups<E, KIND, true>), dim3(uint32_t(blocks)), dim3(kThreads), 0, s, a, per_row);
-    else hipLaunchKernelGGL((encode_groups<E, KIND, false>), dim3(uint32_t(blocks)), dim3(kThreads), 0, s, a, per_row);
+    const uint32_t lanes = (a.d + 127) / 128 * 16, rows_at_once = a.m < 32768 ? uint32_t(a.m) : 32768;
+    const dim3 grid((lanes + kThreads - 1) / kThreads, rows_at_once);
+    auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, s, a, rows_at_once); };
+    if (a.b) vec ? go(encode_groups<E, KIND, true, true>) : go(encode_groups<E, KIND, false, true>);
+    else vec ? go(encode_groups<E, KIND, true, false>) : go(encode_groups<E, KIND, false, false>);
 }
 
 template <uint32_t E>
@@ -433,8 +561,6 @@ extern "C" st_status st_encode(const st_encode_args* g, void* stream) {
     if (g->d && !g->data) return st_fail(ST_E_ARG, "%s: null data", who);
     if (g->kind != ST_X_MXFP8 && off(g->scale, 4)) return st_fail(ST_E_ARG, "%s: scale is not 4-byte aligned", who);
     if (g->d == 0 && g->kind != ST_X_FP8_ROW) return ST_OK;
-    const uint64_t blocks = (g->m * ((g->d + 127) / 128 * 16) + kThreads - 1) / kThreads;
-    if (g->kind != ST_X_FP8_ROW && blocks > 0x7FFFFFFFull) return st_fail(ST_E_SHAPE, "%s: too many elements in one call", who);
     Args a = {};
     a.x = static_cast<const uint8_t*>(g->x);
     a.b = static_cast<const uint8_t*>(g->gate);
