@@ -657,6 +657,17 @@ __global__ __launch_bounds__(T::THREADS, 2) void linear_tile(Args a) {
             for (int i = 0; i < T::W_PER; ++i)
                 if (T::BN * T::WC % T::THREADS == 0 || i * T::THREADS + uwave * 64 < T::BN * T::WC)
                     to_lds(bw, sw + (i * T::THREADS + wave * 64) * 16, w_off[i], uint32_t(wb));
+        } else if (uint64_t(step + 1) * T::KS <= a.k) {
+#pragma unroll
+            for (int i = 0; i < T::X_PER; ++i) {
+                const int s = i * T::THREADS + tid, r = s / T::XC, c = s % T::XC;
+                rx[i] = *reinterpret_cast<const u32x4_any*>(a.x + xr(r) * x_row + kb + c * 16);
+            }
+#pragma unroll
+            for (int i = 0; i < T::W_PER; ++i) {
+                const int s = i * T::THREADS + tid, r = s / T::WC, c = s % T::WC;
+                if (s < T::BN * T::WC) rw[i] = *reinterpret_cast<const u32x4_any*>(a.w + wr(r) * w_row + wb + c * 16);
+            }
         } else {
 #pragma unroll
             for (int i = 0; i < T::X_PER; ++i) {
@@ -666,8 +677,7 @@ __global__ __launch_bounds__(T::THREADS, 2) void linear_tile(Args a) {
 #pragma unroll
             for (int i = 0; i < T::W_PER; ++i) {
                 const int s = i * T::THREADS + tid, r = s / T::WC, c = s % T::WC;
-                if (s < T::BN * T::WC)
-                    rw[i] = load_chunk(a.w + wr(r) * w_row + wb + c * 16, int64_t(w_row) - int64_t(wb + c * 16));
+                if (s < T::BN * T::WC) rw[i] = load_chunk(a.w + wr(r) * w_row + wb + c * 16, int64_t(w_row) - int64_t(wb + c * 16));
             }
         }
         if constexpr (DIRECT && T::X_WAVES + T::W_WAVES != 0) {

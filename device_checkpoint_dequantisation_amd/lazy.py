@@ -21,7 +21,7 @@ import time
 from collections.abc import Mapping
 from dataclasses import dataclass
 
-from . import (SafeTensorIndex, StreamPlan, _quantized, _torch, materialize, read_plans, stream_file,
+from . import (QUANTIZED_KINDS, SafeTensorIndex, StreamPlan, _quantized, _torch, materialize, read_plans, stream_file,
                table_stream_stores)
 
 _ONE_STEP = 1 << 60  # chunk size that keeps a whole selection in one staging step
@@ -381,9 +381,10 @@ class StreamStateDict(Mapping):
                 self._load_direct(metas, outs, s)
         return outs
 
-    def load_quantized(self, names, stream=None) -> dict:
+    def load_quantized(self, names, stream=None, copy: bool = False) -> dict:
         """The quantised weights ``names`` as stored (no decode), read with one packed plan into a
-        device blob that the returned weight tensors view; see QuantizedWeight."""
+        device blob that the returned weight tensors view, or with ``copy`` into aligned tensors of their
+        own; see QuantizedWeight."""
         torch = _torch()
         metas = [self._meta[n] for n in names]
         plan = StreamPlan(self.index, _ONE_STEP, select=[m.index for m in metas], pack=True)
@@ -394,7 +395,7 @@ class StreamStateDict(Mapping):
             blob = torch.empty(plan.blob_bytes, dtype=torch.uint8, device=self.device)
             blob.copy_(host, non_blocking=True)
             ents = self.index.tensors()
-            return {m.name: _quantized(self.index, blob, m.index, lambda i: plan.tensor_offset(ents[i].begin), False)
+            return {m.name: _quantized(self.index, blob, m.index, lambda i: plan.tensor_offset(ents[i].begin), copy)
                     for m in metas}
 
     def _load_direct(self, metas, outs, s):
@@ -588,6 +589,11 @@ class _View(Mapping):
         got = self.base.load([self.mapping[k] for k in keys], stream=stream)
         return {k: got[self.mapping[k]] for k in keys}
 
+    def load_quantized(self, keys, stream=None, copy: bool = False) -> dict:
+        keys = list(keys)
+        got = self.base.load_quantized([self.mapping[k] for k in keys], stream=stream, copy=copy)
+        return {k: got[self.mapping[k]] for k in keys}
+
 
 class PrefixViewStateDict(_View):
     """Keys of ``base`` that start with ``prefix``, with the prefix removed (``strip=True``), or every
@@ -662,15 +668,27 @@ class LazyModuleLoader:
     ``state_dict.load`` call.  With ``max_resident_bytes`` the materialised parameters form an LRU
     (by submodule) on the device; going over the bound turns the least recently used submodules'
     parameters back into meta tensors (their DiskRefs stay).  Parameters take the state dict's
-    output type (bf16 unless the index plans f16 or f32) and do not require grad."""
+    output type (bf16 unless the index plans f16 or f32) and do not require grad.
 
-    def __init__(self, module, state_dict, max_resident_bytes: int | None = None, strict: bool = True):
+    ``quantized`` keeps quantised matrices as stored and computes on them: "weights" runs every ``nn.Linear`` whose
+    weight the checkpoint holds quantised through :func:`linear` (its weight parameter stays a meta tensor; the
+    stored weight, a half or a quarter of the decoded one, is what loads and counts against the bound) and every ``nn.RMSNorm``
+    over one dimension through :func:`rms_norm`; "activations" also encodes those linears' inputs in the 8-bit kind that goes
+    with the weight (NVFP4 weights keep dense inputs).  Inference only, for bf16 and fp16 inputs; subclasses with a
+    forward of their own are left alone."""
+
+    def __init__(self, module, state_dict, max_resident_bytes: int | None = None, strict: bool = True,
+                 quantized: str | None = None):
         torch = _torch()
+        if quantized not in (None, "weights", "activations"):
+            raise ValueError(f'quantized is None, "weights" or "activations", not {quantized!r}')
         self.module = module
         self.sd = state_dict
         self.max_resident_bytes = max_resident_bytes
+        self.quantized = quantized
         self.refs = {}            # (submodule, param name) -> DiskRef
         self._owned = collections.defaultdict(list)  # submodule -> [param name]
+        self._stored = {}         # submodule computing on its stored weight -> QuantizedWeight, None while evicted
         self._resident = collections.OrderedDict()   # submodule -> bytes, LRU order
         self.resident_bytes = 0
         self.stats = collections.Counter()
@@ -691,24 +709,54 @@ class LazyModuleLoader:
             self.refs[(mod, pname)] = DiskRef(state_dict, full, meta)
             self._owned[mod].append(pname)
             mod._parameters[pname] = torch.nn.Parameter(state_dict.meta_tensor(full), requires_grad=False)
+            if quantized and pname == "weight":
+                self._compute_on_stored(mod, meta)
         self._hooks = [mod.register_forward_pre_hook(self._pre_hook) for mod in self._owned]
+
+    def _compute_on_stored(self, mod, meta):
+        """Give ``mod`` a forward that runs the operators on stored weights, where it is a module they replace."""
+        torch = _torch()
+        from . import ops
+        if type(mod).forward is torch.nn.Linear.forward and meta.kind in QUANTIZED_KINDS:
+            self._stored[mod] = None
+            encode = {w: k for k, ws in ops.PAIRS.items() for w in ws}.get(meta.kind) if self.quantized == "activations" else None
+            names = {torch.bfloat16: "bf16", torch.float16: "f16"}
+
+            def forward(x):
+                dtype = names.get(x.dtype)      # another type is refused by the operator
+                if encode is not None and dtype is not None:
+                    x = ops.quantize_activation(x, encode)
+                return ops.linear(x, self._stored[mod], bias=mod.bias, out_dtype=dtype)
+            mod.forward = forward
+        elif type(mod).forward is torch.nn.RMSNorm.forward and len(mod.normalized_shape) == 1:
+            def forward(x):
+                return ops.rms_norm(x, mod.weight, eps=torch.finfo(x.dtype).eps if mod.eps is None else mod.eps)
+            mod.forward = forward
 
     def _pre_hook(self, mod, args):
         self.materialize(mod)
 
     def materialize(self, mod):
-        """Decode every meta parameter of submodule ``mod`` now (one load)."""
+        """Decode every meta parameter of submodule ``mod`` now (one load); a weight that is computed on as stored
+        is loaded as stored."""
         torch = _torch()
-        todo = [p for p in self._owned[mod] if mod._parameters[p].is_meta]
-        if todo:
-            keys = [self.refs[(mod, p)].key for p in todo]
-            got = self.sd.load(keys)
+        todo = [p for p in self._owned[mod] if mod._parameters[p].is_meta and not (p == "weight" and mod in self._stored)]
+        stored = mod in self._stored and self._stored[mod] is None
+        if todo or stored:
             nbytes = 0
-            for p, k in zip(todo, keys):
-                t = got[k]
-                mod._parameters[p] = torch.nn.Parameter(t, requires_grad=False)
-                nbytes += t.numel() * t.element_size()
-            self.stats["materialized"] += len(todo)
+            if todo:
+                keys = [self.refs[(mod, p)].key for p in todo]
+                got = self.sd.load(keys)
+                for p, k in zip(todo, keys):
+                    t = got[k]
+                    mod._parameters[p] = torch.nn.Parameter(t, requires_grad=False)
+                    nbytes += t.numel() * t.element_size()
+            if stored:
+                key = self.refs[(mod, "weight")].key
+                q = self.sd.load_quantized([key], copy=True)[key]
+                self._stored[mod] = q
+                nbytes += sum(t.numel() * t.element_size() for t in (q.data, q.scale, q.scale2) if t is not None)
+            self.stats["materialized"] += len(todo) + stored
             self._resident[mod] = self._resident.get(mod, 0) + nbytes
             self.resident_bytes += nbytes
         if mod in self._resident:
@@ -722,6 +770,8 @@ class LazyModuleLoader:
             ref = self.refs[(mod, p)]
             if not mod._parameters[p].is_meta:
                 mod._parameters[p] = torch.nn.Parameter(ref.source.meta_tensor(ref.key), requires_grad=False)
+        if mod in self._stored:
+            self._stored[mod] = None
         self.resident_bytes -= self._resident.pop(mod, 0)
         self.stats["evicted"] += 1
 

@@ -57,11 +57,6 @@ def _scale_shape(kind: str, shape) -> tuple:
     return (*shape[:-1], -(-shape[-1] // 128) if kind == "FP8_GROUP128" else shape[-1] // 32)
 
 
-def _expect(ok, what: str):
-    if not ok:
-        raise ValueError(what)
-
-
 def _on_device(device, tensors, who: str):
     if device.type != "cuda":
         raise ValueError(f"{who}: needs GPU tensors, got one on {device}")
@@ -114,29 +109,35 @@ def _launch(fn, args, device, stream, tensors, who):
 def _check_weight(w, who: str):
     shape = tuple(w.shape)
     kind = w.kind
-    _expect(kind in _KIND and _KIND[kind] >= 3, f"{who}: weight kind {kind!r} is not a quantised kind")
-    _expect(len(shape) == 2, f"{who}: weight of shape {shape}; a matrix [N, K] is needed")
+    if not (kind in _KIND and _KIND[kind] >= 3):
+        raise ValueError(f"{who}: weight kind {kind!r} is not a quantised kind")
+    if not (len(shape) == 2):
+        raise ValueError(f"{who}: weight of shape {shape}; a matrix [N, K] is needed")
     n, k = shape
     d, s = w.data, w.scale
     fp4 = kind == "NVFP4" or kind == "MXFP4"
-    _expect(d.dtype == (torch.uint8 if fp4 else _E4M3) and tuple(d.shape) == (n, k // 2 if fp4 else k) and d.is_contiguous(),
-            f"{who}: {kind} weight [{n}, {k}] holds {d.dtype} {tuple(d.shape)}, strides {d.stride()}")
+    if not (d.dtype == (torch.uint8 if fp4 else _E4M3) and tuple(d.shape) == (n, k // 2 if fp4 else k) and d.is_contiguous()):
+        raise ValueError(f"{who}: {kind} weight [{n}, {k}] holds {d.dtype} {tuple(d.shape)}, strides {d.stride()}")
     if kind == "FP8_TENSOR":
         want, dt = 1, torch.float32
-        _expect(s.numel() == 1, f"{who}: FP8_TENSOR scale has {s.numel()} elements")
+        if not (s.numel() == 1):
+            raise ValueError(f"{who}: FP8_TENSOR scale has {s.numel()} elements")
         want = tuple(s.shape)
     elif kind == "FP8_BLOCK128":
         want, dt = (-(-n // 128), -(-k // 128)), torch.float32
     elif kind == "NVFP4":
-        _expect(k % 16 == 0, f"{who}: NVFP4 K {k} is not a multiple of 16")
+        if not (k % 16 == 0):
+            raise ValueError(f"{who}: NVFP4 K {k} is not a multiple of 16")
         want, dt = (n, k // 16), _E4M3
         g = w.scale2
-        _expect(g is not None and g.numel() == 1 and g.dtype == torch.float32, f"{who}: NVFP4 needs one fp32 global scale")
+        if not (g is not None and g.numel() == 1 and g.dtype == torch.float32):
+            raise ValueError(f"{who}: NVFP4 needs one fp32 global scale")
     else:
-        _expect(k % 32 == 0, f"{who}: {kind} K {k} is not a multiple of 32")
+        if not (k % 32 == 0):
+            raise ValueError(f"{who}: {kind} K {k} is not a multiple of 32")
         want, dt = (n, k // 32), _E8M0
-    _expect(s.dtype == dt and tuple(s.shape) == want and s.is_contiguous(),
-            f"{who}: {kind} weight [{n}, {k}] has scales {s.dtype} {tuple(s.shape)}, strides {s.stride()}")
+    if not (s.dtype == dt and tuple(s.shape) == want and s.is_contiguous()):
+        raise ValueError(f"{who}: {kind} weight [{n}, {k}] has scales {s.dtype} {tuple(s.shape)}, strides {s.stride()}")
     return n, k
 
 
@@ -167,18 +168,19 @@ def linear(x, weight, bias=None, residual=None, activation: str | None = None, o
         if x.kind not in PAIRS or weight.kind not in PAIRS[x.kind]:
             raise ValueError(f"{who}: {x.kind} activations do not go with {weight.kind} weights")
         xd, xs, x_type = x.data, x.scale, _XKIND[x.kind]
-        _expect(xd.dtype == _E4M3 and xd.is_contiguous() and tuple(xd.shape) == tuple(x.shape),
-                f"{who}: {x.kind} activations hold {xd.dtype} {tuple(xd.shape)}, strides {xd.stride()}")
-        _expect(xs.dtype == (_E8M0 if x.kind == "MXFP8" else torch.float32) and xs.is_contiguous()
-                and tuple(xs.shape) == _scale_shape(x.kind, x.shape),
-                f"{who}: {x.kind} activations {tuple(x.shape)} have scales {xs.dtype} {tuple(xs.shape)}, strides {xs.stride()}")
+        if not (xd.dtype == _E4M3 and xd.is_contiguous() and tuple(xd.shape) == tuple(x.shape)):
+            raise ValueError(f"{who}: {x.kind} activations hold {xd.dtype} {tuple(xd.shape)}, strides {xd.stride()}")
+        if not (xs.dtype == (_E8M0 if x.kind == "MXFP8" else torch.float32) and xs.is_contiguous() and tuple(xs.shape) == _scale_shape(x.kind, x.shape)):
+            raise ValueError(f"{who}: {x.kind} activations {tuple(x.shape)} have scales {xs.dtype} {tuple(xs.shape)}, strides {xs.stride()}")
         default = torch.bfloat16
     else:
         xd, xs, default = x, None, x.dtype
         x_type = _TYPE.get(default, 2)
-        _expect(x_type < 2, f"{who}: x is {default}; bf16, fp16 or a QuantizedActivation is needed")
+        if not (x_type < 2):
+            raise ValueError(f"{who}: x is {default}; bf16, fp16 or a QuantizedActivation is needed")
     lead = xd.shape[:-1]
-    _expect(xd.dim() >= 1 and xd.shape[-1] == k, f"{who}: x {tuple(xd.shape)} against a weight of K {k}")
+    if not (xd.dim() >= 1 and xd.shape[-1] == k):
+        raise ValueError(f"{who}: x {tuple(xd.shape)} against a weight of K {k}")
     device = xd.device
     _on_device(device, (xd, xs, weight.data, weight.scale, weight.scale2, bias, residual, out), who)
     if activation not in _ACT:
@@ -186,13 +188,13 @@ def linear(x, weight, bias=None, residual=None, activation: str | None = None, o
     x2, x_pitch = _rows(xd, k, "x", who)
     m = x2.shape[0]
     if bias is not None:
-        _expect(bias.dtype in _TYPE and tuple(bias.shape) == (n,) and (n <= 1 or bias.stride(0) == 1),
-                f"{who}: bias {bias.dtype} {tuple(bias.shape)}, strides {bias.stride()}; [{n}] is needed")
+        if not (bias.dtype in _TYPE and tuple(bias.shape) == (n,) and (n <= 1 or bias.stride(0) == 1)):
+            raise ValueError(f"{who}: bias {bias.dtype} {tuple(bias.shape)}, strides {bias.stride()}; [{n}] is needed")
     shape = (*lead, n)
     r2, r_pitch = None, 0
     if residual is not None:
-        _expect(residual.dtype in _TYPE and tuple(residual.shape) == shape,
-                f"{who}: residual {residual.dtype} {tuple(residual.shape)}; {shape} is needed")
+        if not (residual.dtype in _TYPE and tuple(residual.shape) == shape):
+            raise ValueError(f"{who}: residual {residual.dtype} {tuple(residual.shape)}; {shape} is needed")
         r2, r_pitch = _rows(residual, n, "residual", who)
     if out is None:
         if out_dtype is not None and out_dtype not in _TORCH:
@@ -200,16 +202,20 @@ def linear(x, weight, bias=None, residual=None, activation: str | None = None, o
         out = torch.empty(shape, dtype=_TORCH[out_dtype] if out_dtype else default, device=device)
         o2 = out if out.dim() == 2 else out.view(m, n)
     else:
-        _expect(out.dtype in _TYPE and tuple(out.shape) == shape, f"{who}: out {out.dtype} {tuple(out.shape)}; {shape} is needed")
-        _expect(out_dtype is None or _TORCH.get(out_dtype) == out.dtype, f"{who}: out is {out.dtype}, out_dtype {out_dtype!r}")
+        if not (out.dtype in _TYPE and tuple(out.shape) == shape):
+            raise ValueError(f"{who}: out {out.dtype} {tuple(out.shape)}; {shape} is needed")
+        if not (out_dtype is None or _TORCH.get(out_dtype) == out.dtype):
+            raise ValueError(f"{who}: out is {out.dtype}, out_dtype {out_dtype!r}")
         try:
             o2 = out if out.dim() == 2 else out.view(m, n)
         except RuntimeError:
             raise ValueError(f"{who}: out {shape} with strides {out.stride()} is not a matrix of rows") from None
-        _expect((n <= 1 or o2.stride(1) == 1) and (m <= 1 or o2.stride(0) >= n), f"{who}: out has strides {out.stride()}")
+        if not ((n <= 1 or o2.stride(1) == 1) and (m <= 1 or o2.stride(0) >= n)):
+            raise ValueError(f"{who}: out has strides {out.stride()}")
         same = r2 is not None and r2.data_ptr() == o2.data_ptr() and r2.dtype == o2.dtype and r2.stride() == o2.stride()
         for t in (xd, xs, weight.data, weight.scale, weight.scale2, bias, None if same else residual):
-            _expect(not _overlaps(out, t), f"{who}: out overlaps an input")
+            if not (not _overlaps(out, t)):
+                raise ValueError(f"{who}: out overlaps an input")
     if m == 0 or n == 0:
         return out
     s2 = weight.scale2
@@ -237,7 +243,8 @@ def _new_activation(kind: str, shape, device):
 def _check_kind(kind, cols: int, who: str):
     if kind not in ACTIVATION_KINDS:
         raise ValueError(f"{who}: unknown encoding {kind!r}; one of {ACTIVATION_KINDS}")
-    _expect(kind != "MXFP8" or cols % 32 == 0, f"{who}: MXFP8 needs a multiple of 32 columns, got {cols}")
+    if not (kind != "MXFP8" or cols % 32 == 0):
+        raise ValueError(f"{who}: MXFP8 needs a multiple of 32 columns, got {cols}")
 
 
 def quantize_activation(x, kind: str, gate=None, stream=None) -> QuantizedActivation:
@@ -245,14 +252,16 @@ def quantize_activation(x, kind: str, gate=None, stream=None) -> QuantizedActiva
     ``kind`` "FP8_ROW" (fp32 amax / 448 per row), "FP8_GROUP128" (the same per 128 columns) or "MXFP8" (the power of two at
     or above it per 32 columns).  A value that is not finite becomes the NaN code and does not enter amax."""
     who = "quantize_activation"
-    _expect(x.dtype in _TYPE and x.dim() >= 1, f"{who}: x is {x.dtype} {tuple(x.shape)}; bf16, fp16 or fp32 rows are needed")
+    if not (x.dtype in _TYPE and x.dim() >= 1):
+        raise ValueError(f"{who}: x is {x.dtype} {tuple(x.shape)}; bf16, fp16 or fp32 rows are needed")
     k = x.shape[-1]
     _check_kind(kind, k, who)
     _on_device(x.device, (x, gate), who)
     x2, x_pitch = _rows(x, k, "x", who)
     g2, g_pitch = None, 0
     if gate is not None:
-        _expect(gate.dtype == x.dtype and gate.shape == x.shape, f"{who}: gate {gate.dtype} {tuple(gate.shape)}, x {x.dtype} {tuple(x.shape)}")
+        if not (gate.dtype == x.dtype and gate.shape == x.shape):
+            raise ValueError(f"{who}: gate {gate.dtype} {tuple(gate.shape)}, x {x.dtype} {tuple(x.shape)}")
         g2, g_pitch = _rows(gate, k, "gate", who)
     q = _new_activation(kind, x.shape, x.device)
     m = x2.shape[0]
@@ -272,23 +281,26 @@ def rms_norm(x, weight=None, eps: float = 1e-6, residual=None, quantize: str | N
     ``out_dtype`` (default x's type) or, with ``quantize`` (an encoding of :func:`quantize_activation`), is the
     :class:`QuantizedActivation` of the unrounded y.  ``weight`` [K] may be bf16, fp16 or fp32."""
     who = "rms_norm"
-    _expect(x.dtype in _TYPE and x.dim() >= 1, f"{who}: x is {x.dtype} {tuple(x.shape)}; bf16, fp16 or fp32 rows are needed")
+    if not (x.dtype in _TYPE and x.dim() >= 1):
+        raise ValueError(f"{who}: x is {x.dtype} {tuple(x.shape)}; bf16, fp16 or fp32 rows are needed")
     k = x.shape[-1]
     _on_device(x.device, (x, weight, residual), who)
-    _expect(eps >= 0.0, f"{who}: eps {eps} is negative")
+    if not (eps >= 0.0):
+        raise ValueError(f"{who}: eps {eps} is negative")
     x2, x_pitch = _rows(x, k, "x", who)
     m = x2.shape[0]
     if weight is not None:
-        _expect(weight.dtype in _TYPE and tuple(weight.shape) == (k,) and (k <= 1 or weight.stride(0) == 1),
-                f"{who}: weight {weight.dtype} {tuple(weight.shape)}, strides {weight.stride()}; [{k}] is needed")
+        if not (weight.dtype in _TYPE and tuple(weight.shape) == (k,) and (k <= 1 or weight.stride(0) == 1)):
+            raise ValueError(f"{who}: weight {weight.dtype} {tuple(weight.shape)}, strides {weight.stride()}; [{k}] is needed")
     r2, r_pitch, h = None, 0, None
     if residual is not None:
-        _expect(residual.dtype == x.dtype and residual.shape == x.shape,
-                f"{who}: residual {residual.dtype} {tuple(residual.shape)}, x {x.dtype} {tuple(x.shape)}")
+        if not (residual.dtype == x.dtype and residual.shape == x.shape):
+            raise ValueError(f"{who}: residual {residual.dtype} {tuple(residual.shape)}, x {x.dtype} {tuple(x.shape)}")
         r2, r_pitch = _rows(residual, k, "residual", who)
         h = torch.empty(x.shape, dtype=x.dtype, device=x.device)
     if quantize is not None:
-        _expect(out_dtype is None, f"{who}: out_dtype and quantize exclude each other")
+        if not (out_dtype is None):
+            raise ValueError(f"{who}: out_dtype and quantize exclude each other")
         _check_kind(quantize, k, who)
         y = _new_activation(quantize, x.shape, x.device)
         yd, ys, kind, out_type = y.data, y.scale, _XKIND[quantize], 0

@@ -195,3 +195,14 @@ class ShardedStateDict(Mapping):
         for part, group in by_part.values():
             out.update(part.load(group, stream=stream))
         return {n: out[n] for n in names}
+
+    def load_quantized(self, names, stream=None, copy: bool = False) -> dict:
+        """The quantised weights ``names`` as stored, one load per shard (see StreamStateDict.load_quantized)."""
+        names = list(dict.fromkeys(names))
+        by_part = {}
+        for n in names:
+            by_part.setdefault(id(self._where[n]), (self._where[n], []))[1].append(n)
+        out = {}
+        for part, group in by_part.values():
+            out.update(part.load_quantized(group, stream=stream, copy=copy))
+        return {n: out[n] for n in names}
