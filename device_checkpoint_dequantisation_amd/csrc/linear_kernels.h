@@ -790,22 +790,32 @@ __global__ __launch_bounds__(T::THREADS, 2) void linear_tile(Args a) {
                 // GROUPED: sums of 128 of K start at zero and are scaled into acc at the end
                 const bool begin = T::GROUPED && (T::Q ? h == 0 : (step & 1) == 0 || step == first);
                 const bool end = T::GROUPED && (T::Q ? h == 1 : (step & 1) == 1 || i + 1 == count);
+                // x's operands of the next 16 rows are on their way from LDS while these multiply
+                u32x4 raw[2];
+                uint32_t code = 0;
+                auto next = [&](int j) {
+                    const int r = (wm * MT + j) * 16 + row;
+                    raw[0] = *reinterpret_cast<const u32x4*>(sx + T::x_at(r, T::Q ? q + 4 * h : 2 * q));
+                    if constexpr (!T::Q) raw[1] = *reinterpret_cast<const u32x4*>(sx + T::x_at(r, 2 * q + 1));
+                    if constexpr (X == ST_X_MXFP8) code = sxs[r * 4 + 2 * h + (q >> 1)];
+                };
+                next(0);
 #pragma unroll
                 for (int j = 0; j < MT; ++j) {
-                    const int r = (wm * MT + j) * 16 + row;
                     u32x4 xv[2], xl[2];
                     if constexpr (T::Q) {
-                        const u32x4 c = *reinterpret_cast<const u32x4*>(sx + T::x_at(r, q + 4 * h));
-                        const float s = X == ST_X_MXFP8 ? scale_of<ST_KIND_MXFP8>(sxs[r * 4 + 2 * h + (q >> 1)]) : 1.0f;
-                        xv[0] = codes8<false, ST_KIND_MXFP8>(c.x, c.y, s);
-                        xv[1] = codes8<false, ST_KIND_MXFP8>(c.z, c.w, s);
+                        const float s = X == ST_X_MXFP8 ? scale_of<ST_KIND_MXFP8>(code) : 1.0f;
+                        xv[0] = codes8<false, ST_KIND_MXFP8>(raw[0].x, raw[0].y, s);
+                        xv[1] = codes8<false, ST_KIND_MXFP8>(raw[0].z, raw[0].w, s);
                     } else {
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            xv[i] = *reinterpret_cast<const u32x4*>(sx + T::x_at(r, 2 * q + i));
-                            if constexpr (D::SPLIT) split_f16(xv[i], xv[i], xl[i]);
+                            xv[i] = raw[i];
+                            if constexpr (D::SPLIT) split_f16(raw[i], xv[i], xl[i]);
                         }
                     }
+                    if (j + 1 < MT) next(j + 1);
+                    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                     for (int i = 0; i < NT; ++i) {
                         f32x4 c = T::GROUPED ? (begin ? f32x4{0, 0, 0, 0} : part[T::GROUPED ? i : 0][T::GROUPED ? j : 0]) : acc[i][j];
@@ -818,6 +828,7 @@ __global__ __launch_bounds__(T::THREADS, 2) void linear_tile(Args a) {
                         if constexpr (T::GROUPED) part[i][j] = c;
                         else acc[i][j] = c;
                     }
+                    __builtin_amdgcn_sched_barrier(0);
                 }
                 if constexpr (T::GROUPED) {
                     if (end) {

@@ -199,7 +199,7 @@ def linear(x, weight, bias=None, residual=None, activation: str | None = None, o
     if out is None:
         if out_dtype is not None and out_dtype not in _TORCH:
             raise ValueError(f"{who}: unknown out_dtype {out_dtype!r}; one of {OUT_DTYPES}")
-        out = torch.empty(shape, dtype=_TORCH[out_dtype] if out_dtype else default, device=device)
+        out = xd.new_empty(shape, dtype=_TORCH[out_dtype] if out_dtype else default)
         o2 = out if out.dim() == 2 else out.view(m, n)
     else:
         if not (out.dtype in _TYPE and tuple(out.shape) == shape):
@@ -228,16 +228,17 @@ def linear(x, weight, bias=None, residual=None, activation: str | None = None, o
     check(lib().st_linear_workspace_bytes(C.byref(args), C.byref(need)), who)
     work = None
     if need.value:
-        work = torch.empty(need.value, dtype=torch.uint8, device=device)
+        work = xd.new_empty(need.value, dtype=torch.uint8)
         args.workspace, args.workspace_bytes = work.data_ptr(), need.value
     _launch(lib().st_linear, args, device, stream, (x2, xs, weight.data, weight.scale, s2, bias, r2, o2, work), who)
     return out
 
 
-def _new_activation(kind: str, shape, device):
-    return QuantizedActivation(kind, tuple(shape), torch.empty(shape, dtype=_E4M3, device=device),
-                               torch.empty(_scale_shape(kind, shape), dtype=_E8M0 if kind == "MXFP8" else torch.float32,
-                                           device=device))
+def _new_activation(kind: str, x):
+    """An empty activation of x's shape."""
+    shape = tuple(x.shape)
+    return QuantizedActivation(kind, shape, torch.empty_like(x, dtype=_E4M3, memory_format=torch.contiguous_format),
+                               x.new_empty(_scale_shape(kind, shape), dtype=_E8M0 if kind == "MXFP8" else torch.float32))
 
 
 def _check_kind(kind, cols: int, who: str):
@@ -263,7 +264,7 @@ def quantize_activation(x, kind: str, gate=None, stream=None) -> QuantizedActiva
         if not (gate.dtype == x.dtype and gate.shape == x.shape):
             raise ValueError(f"{who}: gate {gate.dtype} {tuple(gate.shape)}, x {x.dtype} {tuple(x.shape)}")
         g2, g_pitch = _rows(gate, k, "gate", who)
-    q = _new_activation(kind, x.shape, x.device)
+    q = _new_activation(kind, x)
     m = x2.shape[0]
     if m == 0:
         return q
@@ -297,17 +298,17 @@ def rms_norm(x, weight=None, eps: float = 1e-6, residual=None, quantize: str | N
         if not (residual.dtype == x.dtype and residual.shape == x.shape):
             raise ValueError(f"{who}: residual {residual.dtype} {tuple(residual.shape)}, x {x.dtype} {tuple(x.shape)}")
         r2, r_pitch = _rows(residual, k, "residual", who)
-        h = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        h = torch.empty_like(x, memory_format=torch.contiguous_format)
     if quantize is not None:
         if not (out_dtype is None):
             raise ValueError(f"{who}: out_dtype and quantize exclude each other")
         _check_kind(quantize, k, who)
-        y = _new_activation(quantize, x.shape, x.device)
+        y = _new_activation(quantize, x)
         yd, ys, kind, out_type = y.data, y.scale, _XKIND[quantize], 0
     else:
         if out_dtype is not None and out_dtype not in _TORCH:
             raise ValueError(f"{who}: unknown out_dtype {out_dtype!r}; one of {OUT_DTYPES}")
-        y = yd = torch.empty(x.shape, dtype=_TORCH[out_dtype] if out_dtype else x.dtype, device=x.device)
+        y = yd = torch.empty_like(x, dtype=_TORCH[out_dtype] if out_dtype else x.dtype, memory_format=torch.contiguous_format)
         ys, kind, out_type = None, 0, _TYPE[y.dtype]
     if m:
         args = RmsNormArgs(x2.data_ptr(), None if r2 is None else r2.data_ptr(), None if weight is None else weight.data_ptr(),
