@@ -8,8 +8,8 @@
 //  * encode without a gate: v, and so amax and s, are exact in fp32.  The fp32 quotient names the middle that is nearest, and the
 //    sign of fma(-middle, s, v), which is exact, says on which side of it v / s lies.
 //  * a gate or a norm: v, amax and the quotient are kept in fp64 (the sum of squares too).  For MX, whose scale is a power of two, v
-//    in fp32 decides unless it comes within 2^-19 of a middle or amax that near to a power of two's edge; then the
-//    wavefront does its chunk again in fp64 (about one in 100).
+//    in fp32, good to 2^-21, decides unless it comes within 2^-20 of a middle or amax that near to a power of two's edge;
+//    then the wavefront does its chunk again in fp64 (about one in 100).
 // fp64 quotients within 2^-40 of a middle are taken as the middle itself: v and s have at most 24 bits each and a middle has
 // 5, so an inexact quotient of two such numbers differs from it by more than 2^-30, and what is nearer is the error of
 // multiplying by 1 / s.
@@ -79,6 +79,14 @@ __device__ __forceinline__ Raw<E> load8(const uint8_t* row, uint32_t col, uint32
 
 __device__ __forceinline__ bool finite(double v) { return __builtin_fabs(v) <= 1.7976931348623157e308; }
 __device__ __forceinline__ double silu64(double g) { return g / (1.0 + exp(-g)); }
+// The same to 5 * 2^-24 of itself: exp(-g) = 2^t (1 + r ln 2) with t + r = -g log2(e), t the rounded product and r the rest, and the
+// hardware's 2^t and 1 / x (an ulp each).  A value too small for the hardware's 2^t to be finite is left to silu64 by its caller.
+__device__ __forceinline__ float silu32(float g) {
+    const float t = g * -1.44269504f;                                  // the nearest fp32 to log2(e), and what it lacks
+    const float r = __builtin_fmaf(g, -1.44269504f, -t) + g * -1.92596299e-8f;
+    const float e = __builtin_amdgcn_exp2f(t);
+    return g * __builtin_amdgcn_rcpf(1.0f + __builtin_fmaf(e, r * 0.69314718f, e));
+}
 
 // ------------------------------------------------------------------------- scales and codes
 
@@ -222,21 +230,17 @@ __device__ __forceinline__ void encode_group(const Args& a, uint64_t row, uint32
             amax = __builtin_fmaxf(amax, m);
         }
         amax = max_over<4>(amax);
-        // amax = f 2^e: its power of two changes at f = 1.75; tiny groups are left to fp64
-        odd |= ((as_u32(amax) + 32 - 0x600000u) & 0x7FFFFFu) < 64 || (amax < 1e-30f && amax != 0.0f);
+        // amax = f 2^e: its power of two changes at f = 1.75; tiny groups (and empty ones) are left to fp64
+        odd |= ((as_u32(amax) + 16 - 0x600000u) & 0x7FFFFFu) < 32 || amax < 1e-30f;
         const Scale<KIND> s((double(amax)));
         const float inv = float(s.inv);
         bits = s.bits;
-        float q[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            q[i] = v[i] * inv;
-            const float m = __builtin_fabsf(q[i]);
-            const uint32_t z = as_u32(m < 0.015625f ? m + 0.015625f : m);
-            odd |= ((z + 32 - 0x80000u) & 0xFFFFFu) < 64;
-        }
-        lo = pack4(q[0], q[1], q[2], q[3]);
-        hi = pack4(q[4], q[5], q[6], q[7]);
+        // codes do not fall as values rise: where v a little lower and a little higher have the same code, v itself has it
+        const float less = inv * (1.0f - 0x1p-20f), more = inv * (1.0f + 0x1p-20f);
+        lo = pack4(v[0] * less, v[1] * less, v[2] * less, v[3] * less);
+        hi = pack4(v[4] * less, v[5] * less, v[6] * less, v[7] * less);
+        odd |= lo != pack4(v[0] * more, v[1] * more, v[2] * more, v[3] * more) ||
+               hi != pack4(v[4] * more, v[5] * more, v[6] * more, v[7] * more);
         again = __any(odd);
     }
     if (again) {
@@ -269,7 +273,7 @@ __global__ __launch_bounds__(kThreads) void encode_groups(Args a, uint32_t rows_
         if constexpr (GATE) {
             const Raw<E> g = load8<E, VEC>(a.b + row * a.b_pitch * kSize<E>, col, a.d);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = silu(g.at(k)) * x.at(k);
+            for (int k = 0; k < 8; ++k) v[k] = silu32(g.at(k)) * x.at(k);
             encode_group<KIND, VEC>(a, row, col, v, [&](double* w) {
 #pragma unroll
                 for (int k = 0; k < 8; ++k) w[k] = silu64(double(g.at(k))) * double(x.at(k));

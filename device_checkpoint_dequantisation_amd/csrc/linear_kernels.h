@@ -944,7 +944,7 @@ void launch(const Args& a, const Plan& p, hipStream_t s) {
     } else if (p.bm == 128) {
         if constexpr (is_q(X))
             if (p.f8) launch_tile<Tile<X, WK, 128, 128, 2, 2, true, 2>, true>(a, p, s);
-        if (!is_q(X) || !p.f8) launch_tile<Tile<X, WK, 128, 128, 2, 2, false, 2>, true>(a, p, s);
+        if (!is_q(X) || !p.f8) launch_tile<Tile<X, WK, 128, 128, is_fp4(WK) && !is_q(X) ? 1 : 2, is_fp4(WK) && !is_q(X) ? 4 : 2, false, 2>, true>(a, p, s);
     } else if constexpr (is_q(X)) {
         launch_tile<Tile<X, WK, 256, 256, 2, 4, true, 2>, false>(a, p, s);
     }
