@@ -403,12 +403,12 @@ __global__ __launch_bounds__(TPR < int(kThreads) ? kThreads : TPR) void rows(Arg
         }
     };
     if constexpr (KIND == 0) {
-        const float s = float(inv);
         each([&](int c, uint32_t col) {
             float w[8], y[8];
             weight(col, w);
+            // in fp64: the factor of a row of the smallest values may lie beyond fp32
 #pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = h_of(c, i) * s * w[i];
+            for (int i = 0; i < 8; ++i) y[i] = float(double(h_of(c, i)) * inv * double(w[i]));
             store_h(c, col);
             if constexpr (VEC) {
                 if (col < dd) {
@@ -489,6 +489,7 @@ void launch_rows(const Args& a, bool vec, hipStream_t s) {
     else if (chunks <= 64) go(rows<OP, E, KIND, true, 64, 1, B>, 256, 4);
     else if (chunks <= 256) go(rows<OP, E, KIND, true, 256, 1, B>, 256, 1);
     else if (chunks <= 512) go(rows<OP, E, KIND, true, 256, 2, B>, 256, 1);
+    else if (chunks <= 768) go(rows<OP, E, KIND, true, 256, 3, B>, 256, 1);
     else if (chunks <= 1024) go(rows<OP, E, KIND, true, 256, 4, B>, 256, 1);
     else if (chunks <= 2048) go(rows<OP, E, KIND, true, 512, 4, B>, 512, 1);
     else if constexpr (E != ST_OUT_F32) go(rows<OP, E, KIND, true, 512, 8, B>, 512, 1);

@@ -19,7 +19,7 @@ def _x(m, d, dt, seed, spread=3.0):
 
 
 def _bits(t):
-    return t.cpu().contiguous().view(torch.uint8)
+    return t.cpu().contiguous().view(torch.uint8) if t.dim() else t.cpu().reshape(1).view(torch.uint8)
 
 
 def _check_codes(q, v, exact=True):
@@ -208,6 +208,46 @@ def test_norm_of_zero_and_nan_rows():
         assert (s[0] == 1).all() and (s[2] == 1).all()
     # a row of zeros without eps: 0 / 0
     assert st.rms_norm(x[:1].to(DEV), eps=0.0).isnan().all()
+
+
+def test_norm_of_the_smallest_rows():
+    """Rows whose factor 1 / rms lies beyond fp32, without eps."""
+    x = torch.full((2, 64), 1e-44)
+    x[1, ::2] = -3e-45
+    want, _ = ref.rms_norm(x, None, 0.0, None)
+    y = st.rms_norm(x.to(DEV), eps=0.0)
+    assert ((y.cpu().double() - want).abs() <= want.abs() * 2.0 ** -24).all()
+    for kind in KINDS:
+        _check_codes(st.rms_norm(x.to(DEV), eps=0.0, quantize=kind), want, exact=False)
+
+
+def test_encode_one_dimensional_and_without_columns():
+    x = _x(1, 256, "bf16", 10)
+    for kind in KINDS:
+        q, q2 = st.quantize_activation(x[0].to(DEV), kind), st.quantize_activation(x.to(DEV), kind)
+        assert q.shape == (256,) and torch.equal(_bits(q.data), _bits(q2.data)[0]) and torch.equal(_bits(q.scale).reshape(-1), _bits(q2.scale).reshape(-1))
+        e = st.quantize_activation(torch.empty(3, 0, dtype=torch.bfloat16, device=DEV), kind)
+        assert e.data.shape == (3, 0) and (kind != "FP8_ROW" or (e.scale == 1).all())
+
+
+def test_encode_many_rows():
+    """More rows than one grid dimension holds."""
+    x = _x(70_001, 32, "bf16", 11, 0.5)
+    for kind in KINDS:
+        _check_codes(st.quantize_activation(x.to(DEV), kind), x.double())
+
+
+def test_calls_on_another_stream():
+    x = _x(64, 4096, "bf16", 12)
+    s = torch.cuda.Stream(DEV)
+    dx = torch.zeros(64, 4096, dtype=torch.bfloat16, device=DEV)
+    torch.cuda._sleep(20_000_000)
+    dx.copy_(x.to(DEV))
+    q = st.quantize_activation(dx, "MXFP8", stream=s)
+    y, h = st.rms_norm(dx, residual=dx, stream=s)
+    torch.cuda.current_stream().wait_stream(s)
+    _check_codes(q, x.double())
+    assert torch.equal(y, st.rms_norm(x.to(DEV), residual=x.to(DEV))[0]) and torch.equal(h.cpu(), x * 2)
 
 
 def test_norm_strided_rows_and_shapes():

@@ -107,6 +107,39 @@ def test_exact_sums(xk, wk, m, n, k):
     assert torch.equal(_run(x, w, out_dtype="f16").cpu(), want.to(torch.float16))
 
 
+@pytest.mark.parametrize("xk,wk", DENSE + EIGHT)
+@pytest.mark.parametrize("m,n,k", [(1500, 1100, 256), (4100, 4097, 128), (4096, 4352, 384)])
+def test_many_tiles(xk, wk, m, n, k):
+    """Whole and ragged bands of tiles, of every tile size; the 64-bit products on the GPU."""
+    print(f"tiles {xk} {wk} {m} {n} {k}", flush=True)
+    x, w = ref.random_rows(st, xk, m, k, 41), ref.random_weight(st, wk, n, k, 42)
+    b = ref.weight_value(w).to(DEV)
+    a = (x.double() if xk in ref.DT else ref.rows_value(x.kind, x.data, x.scale)).to(DEV)
+    want, s = torch.mm(a, b.t().contiguous()), torch.mm(a.abs(), b.abs().t().contiguous())
+    for out in ("bf16", "f32"):
+        y = _run(x, w, out_dtype=out)
+        tol = ref.linear_tolerance(want, s, k, y.dtype)
+        if xk not in ref.DT and out == "bf16":
+            tol = tol + ref.f8_tolerance(x, w).to(DEV)
+        assert ((y.double() - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("xk,wk,m", [("bf16", "FP8_TENSOR", 1), ("bf16", "FP8_TENSOR", 3), ("FP8_ROW", "FP8_TENSOR", 40), ("f16", "FP8_TENSOR", 200)])
+def test_weight_past_four_gibibytes(xk, wk, m):
+    """Rows of the weight whose bytes lie past 2^32."""
+    n, k = 140_000, 32_768
+    x = ref.random_rows(st, xk, m, k, 43)
+    data = torch.zeros(n, k, dtype=torch.uint8, device=DEV)
+    tail = ref.random_codes(torch.Generator().manual_seed(44), 70, k)
+    data[n - 70:] = tail.view(torch.uint8).to(DEV)
+    assert (n - 70) * k > 2 ** 32
+    scale = torch.tensor(0.25)
+    w = st.QuantizedWeight("w", wk, (n, k), data.view(torch.float8_e4m3fn), scale.to(DEV))
+    y = st.linear(ref.to(x, DEV), w, out_dtype="f32")
+    assert (y[:, : n - 70] == 0).all()
+    _check(x, st.QuantizedWeight("w", wk, (70, k), tail, scale), y[:, n - 70:], k)
+
+
 @pytest.mark.parametrize("xk,wk", [("bf16", "NVFP4"), ("f16", "MXFP8"), ("bf16", "FP8_BLOCK128"), ("MXFP8", "MXFP4")])
 def test_one_hot_places_every_element(xk, wk):
     """Row i of x is one at column 37 i + 5: y is that column of the weight, rounded."""
@@ -186,6 +219,11 @@ def test_leading_dimensions_and_empty():
                               torch.ones((), device=DEV))
     got = st.linear(torch.empty(5, 0, dtype=torch.bfloat16, device=DEV), flat, bias=b.to(DEV), activation="relu")
     assert torch.equal(got.cpu().float(), b.clamp_min(0).expand(5, 24))
+    for xk, wk in DENSE + EIGHT:
+        w = ref.random_weight(st, wk, 24, 0, 1)
+        for m in (1, 5, 70):
+            got = _run(ref.random_rows(st, xk, m, 0, 2), w, bias=b)
+            assert torch.equal(got.cpu().float(), b.expand(m, 24))
 
 
 @pytest.mark.parametrize("xk,wk", DENSE + EIGHT)
