@@ -9,7 +9,8 @@ memory and streams.
     ckpt.materialize()                         # one grouped kernel launch
     ckpt.tensors["model.layers.0.mlp.up_proj.weight"]   # bf16 torch tensor on the GPU
 
-or simply ``load(path)`` -> {name: bf16 tensor}.
+or simply ``load(path)`` -> {name: bf16 tensor}.  ``linear``, ``rms_norm`` and ``quantize_activation`` (ops.py) compute
+on quantised weights as stored.
 """
 from __future__ import annotations
 
@@ -379,7 +380,7 @@ def stream_file(path: str, index: SafeTensorIndex, plan: StreamPlan, blob, table
 
 @dataclass
 class QuantizedWeight:
-    """A quantised weight as stored, for consumers that compute on the quantised form (FP8 matrix
+    """A quantised weight as stored, for consumers that compute on the quantised form (:func:`linear`, FP8 matrix
     cores): no decode, the checkpoint's own bytes on the device.
       FP8_TENSOR    data float8_e4m3fn [M, N...], scale fp32 []
       FP8_BLOCK128  data float8_e4m3fn [M, N],    scale fp32 [ceil(M/128), ceil(N/128)] (multiplied)

@@ -17,6 +17,7 @@
  *   st_stage_file                    file byte ranges -> pinned ring -> device blob (side stream)
  *   st_stream_plan_build/st_stream_file  staging steps, each decoded as soon as its bytes land
  *   st_materialize                   device blob + work table -> bf16 outputs (one launch)
+ *   st_linear, st_encode, st_rms_norm  computing on quantised weights as stored (end of this header)
  *
  * Output element values (bit-exact definition; rounding is IEEE binary32 round-to-nearest-even
  * for every multiply, then round-to-nearest-even to bfloat16; any NaN result is 0x7FC0;
