@@ -53,9 +53,13 @@ Plan plan_of(const st_linear_args& g) {
     p.bn = p.bm;
     p.f8 = q && p.bm > 64 && g.out_type != ST_OUT_F32;
     const uint64_t tiles = ((g.m + p.bm - 1) / p.bm) * ((g.n + p.bn - 1) / p.bn), all = (g.k + ks - 1) / ks;
-    // Too few tiles to fill 256 CUs: split K, in whole groups of 128, while each part keeps 8 steps
+    // Too few tiles to fill 256 CUs (with two workgroups each, where tiles are small): split K, in whole groups of 128, while
+    // each part keeps 8 steps.  The parts' sums pass through memory and take a second launch, which a CU's one large tile does not
+    // earn back (block FP8 [4096, 12288] x 4096 grouped rows, 256 tiles of 256: 250 us whole, 267 in two parts) and two small
+    // ones do (FP8 [4096, 4096] x 1024 bf16 rows, 256 tiles of 128: 47.6 us whole, 45.1 in two parts).
+    const uint64_t want = p.bm == 256 ? 256 : 512;
     uint64_t s = 1;
-    while (tiles * s < 512 && all / (2 * s) >= 8) s *= 2;
+    while (tiles * s < want && all / (2 * s) >= 8) s *= 2;
     const uint64_t gran = 128 / ks;
     p.steps = uint32_t((all + s - 1) / s);
     p.steps = uint32_t((p.steps + gran - 1) / gran * gran);
