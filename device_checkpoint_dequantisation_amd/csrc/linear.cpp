@@ -13,17 +13,14 @@ Plan plan_of(const st_linear_args& g) {
     const uint64_t xb = g.x_pitch * (q ? 1 : 2), wb = fp4 ? g.k / 2 : g.k;
     auto al = [](const void* v, uint64_t n) { return reinterpret_cast<uintptr_t>(v) % n == 0; };
     p.direct = al(g.x, 16) && al(g.w, 16) && (g.m <= 1 || xb % 16 == 0) && wb % 16 == 0;
-    // one row, and whole 16-byte pieces of K per lane
-    if (p.direct && g.m == 1 && g.k && g.k % (fp4 ? 32 : 16) == 0 && (g.w_kind != ST_KIND_NVFP4 || al(g.w_scale, 2))) {
+    if (g.m == 1 && g.k) {
         const uint32_t slice = fp4 ? 2048 : 1024, slices = uint32_t((g.k + slice - 1) / slice), rounds = (slices + 3) / 4;
         p.one = true;
         p.waves = (slices + rounds - 1) / rounds;
         p.splits = 1;
         return p;
     }
-    // few rows, and whole 64-byte pieces
-    if (p.direct && g.m <= 16 && g.k && g.k % (fp4 ? 128 : 64) == 0 && (g.w_kind != ST_KIND_NVFP4 || al(g.w_scale, 8)) &&
-        (!is_mx(g.w_kind) || al(g.w_scale, 4)) && (g.x_type != ST_X_MXFP8 || al(g.x_scale, 4))) {
+    if (g.m <= 16 && g.k) {
         const uint32_t turns = uint32_t((g.k + (fp4 ? 511 : 255)) / (fp4 ? 512 : 256));
         // A weight of few rows is split over K as well (16 rows through NVFP4 [5120, 25600]: 41.8 us in four parts, 66 whole),
         // which costs a second launch (8-bit kinds from 256 workgroups on lose by it: FP8 [4096, 12288] 14.7 us whole, 16.3 halved).

@@ -24,8 +24,8 @@
 //  * linear_one: m = 1, dot products on the vector unit at the rate the weight arrives.
 //  * linear_few: m <= 16.  Each wavefront streams its part of K for one or two 16-row groups of the weight straight
 //    into registers and the matrix instructions, the wavefronts of a workgroup join in LDS.
-//  * linear_tile: tiles of y staged through LDS, double-buffered, one barrier per step of K.  x and the weight are
-//    staged as stored and the weight is decoded on its way from LDS to the matrix instructions.
+//  * linear_tile: tiles of y, x and the weight staged through LDS as stored, one barrier per step of K and up to three steps on
+//    their way; the weight is decoded on its way from LDS to the matrix instructions.
 //  * linear_join: adds the fp32 partial results where K was split over workgroups, in a fixed order.
 #pragma once
 
@@ -39,7 +39,11 @@ using namespace st_dev;
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+// global memory takes vector loads at any byte
 typedef u32x4 u32x4_any __attribute__((aligned(1)));
+typedef uint64_t u64_any __attribute__((aligned(1)));
+typedef uint32_t u32_any __attribute__((aligned(1)));
+typedef uint16_t u16_any __attribute__((aligned(1)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -210,9 +214,30 @@ struct Dense {
     static constexpr bool F16 = X == ST_X_F16 && !is_mx(WK), SPLIT = X == ST_X_F16 && is_mx(WK);
 };
 
+// ------------------------------------------------------------------------- loads of rows that start anywhere
+
+// 16 bytes at p of which `avail` lie in the row, the others 0.
+__device__ __forceinline__ u32x4 load_chunk(const uint8_t* p, int64_t avail) {
+    if (avail >= 16) return *reinterpret_cast<const u32x4_any*>(p);
+    u32x4 v = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        if (i < avail) v[i >> 2] |= uint32_t(p[i]) << (8 * (i & 3));
+    return v;
+}
+// The first `want` of the scale codes at p of which `avail` lie in the row, the others 0.
+__device__ __forceinline__ uint32_t load_codes(const uint8_t* p, int64_t avail, int want) {
+    uint32_t v = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (i < want && i < avail) v |= uint32_t(p[i]) << (8 * i);
+    return v;
+}
+
 // ------------------------------------------------------------------------- one row
 
-// m = 1: dot products on the vector unit.  A wavefront takes a slice of K, 16 bytes of a weight row per lane, for R
+// m = 1: dot products on the vector unit.  Bound by the weight's bytes (NVFP4 [5120, 25600], 73.8 MB: 15.4-16.2 us, 4.6-4.8 TB/s;
+// reading as many bytes and nothing else takes 13.9).  A wavefront takes a slice of K, 16 bytes of a weight row per lane, for R
 // weight rows: its loads are contiguous, all R of them are in flight together, and its part of x stays in
 // registers.  Decoding costs half an instruction per weight and multiplying another half (two-element dot
 // products into fp32); a block's scale multiplies the block's sum.  (16x16x32 matrix instructions leave 15 of 16 columns empty for one
@@ -270,7 +295,8 @@ __global__ __launch_bounds__(64 * kOneWaves) void linear_one(Args a) {
 
     for (uint32_t k0 = wave * F::SLICE; k0 < a.k; k0 += waves * F::SLICE) {
         const uint32_t k = k0 + lane * E;
-        const bool in = k < a.k;          // lanes behind K's end hold zeros
+        const bool in = k < a.k;          // lanes behind K's end hold zeros,
+        const bool all = k + E <= a.k;    // and the lane that it cuts the rest of its row
         u32x4 w[R];
         uint32_t ws[R];
         // rows past the last are read as the last one; nothing of them is stored
@@ -279,9 +305,21 @@ __global__ __launch_bounds__(64 * kOneWaves) void linear_one(Args a) {
             const uint32_t n = n0 + r < a.n ? n0 + r : a.n - 1;
             const uint8_t* pw = a.w + uint64_t(n) * w_row;
             const uint8_t* ps = a.ws + uint64_t(n) * ws_row;
-            w[r] = in ? *reinterpret_cast<const u32x4*>(pw + (F::FP4 ? k / 2 : k)) : u32x4{0, 0, 0, 0};
-            if constexpr (WK == ST_KIND_NVFP4) ws[r] = in ? *reinterpret_cast<const uint16_t*>(ps + k / 16) : 0;
-            else if constexpr (is_mx(WK)) ws[r] = in ? ps[k / 32] : 0;
+            const uint32_t at = F::FP4 ? k / 2 : k;
+            w[r] = u32x4{0, 0, 0, 0};
+            ws[r] = 0;
+            if (all) w[r] = *reinterpret_cast<const u32x4_any*>(pw + at);
+            if constexpr (WK == ST_KIND_NVFP4) {
+                if (all) ws[r] = *reinterpret_cast<const u16_any*>(ps + k / 16);
+            } else if constexpr (is_mx(WK)) {
+                if (in) ws[r] = ps[k / 32];
+            }
+            if constexpr (!is_mx(WK)) {
+                if (in && !all) {
+                    w[r] = load_chunk(pw + at, int64_t(w_row) - at);
+                    if constexpr (WK == ST_KIND_NVFP4) ws[r] = ps[k / 16];
+                }
+            }
         }
         uint32_t x[PAIRS], xl[D::SPLIT ? PAIRS : 1];
         const uint8_t* px = a.x + k * (F::Q ? 1u : 2u);
@@ -289,7 +327,9 @@ __global__ __launch_bounds__(64 * kOneWaves) void linear_one(Args a) {
             const float s = X == ST_X_MXFP8 ? scale_of<ST_KIND_MXFP8>(in ? a.xs[k / 32] : 0) : 1.0f;
 #pragma unroll
             for (int h = 0; h < E / 16; ++h) {
-                const u32x4 c = in ? *reinterpret_cast<const u32x4*>(px + 16 * h) : u32x4{0, 0, 0, 0};
+                u32x4 c = {0, 0, 0, 0};
+                if (all) c = *reinterpret_cast<const u32x4_any*>(px + 16 * h);
+                else if (in) c = load_chunk(px + 16 * h, int64_t(a.k) - (k + 16 * h));
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const u32x4 t = codes8<false, ST_KIND_MXFP8>(c[2 * i], c[2 * i + 1], s);
@@ -300,7 +340,9 @@ __global__ __launch_bounds__(64 * kOneWaves) void linear_one(Args a) {
         } else {
 #pragma unroll
             for (int h = 0; h < E / 8; ++h) {
-                u32x4 c = in ? *reinterpret_cast<const u32x4*>(px + 16 * h) : u32x4{0, 0, 0, 0}, lo;
+                u32x4 c = {0, 0, 0, 0}, lo;
+                if (all) c = *reinterpret_cast<const u32x4_any*>(px + 16 * h);
+                else if (in) c = load_chunk(px + 16 * h, 2 * (int64_t(a.k) - (k + 8 * h)));
                 if constexpr (D::SPLIT) split_f16(c, c, lo);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -366,7 +408,8 @@ __global__ __launch_bounds__(64 * kOneWaves) void linear_one(Args a) {
 
 // ------------------------------------------------------------------------- few rows
 
-// 1 < m <= 16: one 16x16x32 instruction takes all rows of x.  A wavefront holds a turn of K, 64 bytes of a weight row per lane,
+// 1 < m <= 16: one 16x16x32 instruction takes all rows of x.  Bound by the weight's bytes and x's, which every workgroup reads from L2
+// (block FP8 [12288, 4096], 8 rows: 16.0 us; 12.1 without reading x; reading the weight alone takes 11.5).  A wavefront holds a turn of K, 64 bytes of a weight row per lane,
 // for NT groups of 16 weight rows, all of it in flight at once straight into registers, and reads its part of x once for them; the
 // wavefronts of a workgroup take different turns of the same weight rows and join in LDS.
 template <int X_, int WK_>
@@ -387,12 +430,19 @@ struct Few {
     static __device__ __forceinline__ uint32_t k_of(uint32_t q, uint32_t j) { return GROUPED ? 64 * j + 16 * q : LK * q + CK * j; }
 };
 
-template <int BYTES>
-__device__ __forceinline__ uint64_t load_scales(const uint8_t* p) {
-    if constexpr (BYTES == 8) return *reinterpret_cast<const uint64_t*>(p);
-    else if constexpr (BYTES == 4) return *reinterpret_cast<const uint32_t*>(p);
-    else if constexpr (BYTES == 2) return *reinterpret_cast<const uint16_t*>(p);
-    else return 0;
+// BYTES scale codes at p; not WHOLE: `avail` of them lie in the row, the others are 0.
+template <int BYTES, bool WHOLE>
+__device__ __forceinline__ uint64_t load_scales(const uint8_t* p, int64_t avail) {
+    if constexpr (BYTES == 0) return 0;
+    else if constexpr (!WHOLE) return load_codes(p, avail, BYTES < 4 ? BYTES : 4) | (BYTES == 8 ? uint64_t(load_codes(p + 4, avail - 4, 4)) << 32 : 0);
+    else if constexpr (BYTES == 8) return *reinterpret_cast<const u64_any*>(p);
+    else if constexpr (BYTES == 4) return *reinterpret_cast<const u32_any*>(p);
+    else return *reinterpret_cast<const u16_any*>(p);
+}
+template <bool WHOLE>
+__device__ __forceinline__ u32x4 load_piece(const uint8_t* p, int64_t avail) {
+    if constexpr (WHOLE) return *reinterpret_cast<const u32x4_any*>(p);
+    else return load_chunk(p, avail);
 }
 
 template <bool V>
@@ -417,10 +467,10 @@ __global__ __launch_bounds__(64 * F::WAVES) void linear_few(Args a) {
 #pragma unroll
     for (int i = 0; i < NT; ++i) acc[i] = f32x4{0, 0, 0, 0};
 
-    // a turn: K from k0; WHOLE: all SS elements are there, else lanes (chunks) behind the end hold zeros
+    // a turn: K from k0; WHOLE: all SS elements are there, else there are zeros behind the end
     auto turn = [&](uint32_t k0, auto whole) {
         constexpr bool WHOLE = decltype(whole)::value;
-        const bool in = WHOLE || F::GROUPED || k0 + F::LK * q < a.k;
+        const uint32_t kq = k0 + F::LK * q;        // K of this lane's scales
         u32x4 w[NT][4], xr[4][F::XL];
         uint64_t wsc[NT], xsc = 0;
         float gs[F::GROUPED ? NT : 1][2];
@@ -429,13 +479,13 @@ __global__ __launch_bounds__(64 * F::WAVES) void linear_few(Args a) {
 #pragma unroll
             for (int h = 0; h < F::XL; ++h) xr[j][h] = u32x4{0, 0, 0, 0};
         if (have) {
-            if constexpr (F::XSB != 0) xsc = in ? load_scales<F::XSB>(a.xs + xrow * uint64_t(a.k / 32) + (k0 + F::LK * q) / 32) : 0;
+            if constexpr (F::XSB != 0) xsc = load_scales<F::XSB, WHOLE>(a.xs + xrow * uint64_t(a.k / 32) + kq / 32, int64_t(a.k / 32) - kq / 32);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const uint32_t k = k0 + F::k_of(q, j);
 #pragma unroll
                 for (int h = 0; h < F::XL; ++h)
-                    if (WHOLE || k < a.k) xr[j][h] = *reinterpret_cast<const u32x4*>(px + k * F::XE + 16 * h);
+                    xr[j][h] = load_piece<WHOLE>(px + k * F::XE + 16 * h, (int64_t(a.k) - k) * F::XE - 16 * h);
             }
         }
 #pragma unroll
@@ -445,10 +495,13 @@ __global__ __launch_bounds__(64 * F::WAVES) void linear_few(Args a) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const uint32_t k = k0 + F::k_of(q, j);
-                w[i][j] = WHOLE || k < a.k ? *reinterpret_cast<const u32x4*>(pw + (F::FP4 ? k / 2 : k)) : u32x4{0, 0, 0, 0};
+                const uint32_t to = F::FP4 ? k / 2 : k;
+                w[i][j] = load_piece<WHOLE>(pw + to, int64_t(w_row) - to);
             }
-            if constexpr (F::WSB != 0)
-                wsc[i] = in ? load_scales<F::WSB>(a.ws + uint64_t(at) * ws_row + (k0 + F::LK * q) / (WK == ST_KIND_NVFP4 ? 16 : 32)) : 0;
+            if constexpr (F::WSB != 0) {
+                const uint32_t to = kq / (WK == ST_KIND_NVFP4 ? 16 : 32);
+                wsc[i] = load_scales<F::WSB, WHOLE>(a.ws + uint64_t(at) * ws_row + to, int64_t(ws_row) - to);
+            }
             if constexpr (F::GROUPED) {
                 const uint32_t nb = (n0 + i * 16) / 128, lastb = (a.n - 1) / 128;
 #pragma unroll
@@ -524,6 +577,10 @@ __global__ __launch_bounds__(64 * F::WAVES) void linear_few(Args a) {
 
 // ------------------------------------------------------------------------- tiles
 
+// What bounds it: 8-bit rows, tiles of 256: the matrix instructions (MXFP8 [12288, 4096] x 8192 rows: 472 us, of which they are busy
+// 164; LDS reads take 90, the rest is waiting at the barrier and for LDS at a step's start).  Dense rows, tiles of 128: matrix
+// instructions, decoding and LDS reads count 215, 125 and 220 us of NVFP4 [25600, 5120] x 2048 rows' 546 us and overlap in part.
+//
 // A tile of BM x BN outputs by WAVES_M x WAVES_N wavefronts; a step of K is 128 bytes of x: 64 elements, or 128
 // of e4m3.  LDS holds rows of 16-byte chunks; chunk c of row r sits at c ^ swizzle(r), so that eight lanes
 // reading the same chunk of eight consecutive rows touch all 32 banks once.
@@ -553,23 +610,6 @@ struct Tile {
         return r * WB + ((c ^ ((r / (8 / WC)) & (WC - 1))) << 4);
     }
 };
-
-// 16 bytes at p of which `avail` lie in the row, the others 0.
-__device__ __forceinline__ u32x4 load_chunk(const uint8_t* p, int64_t avail) {
-    if (avail >= 16) return *reinterpret_cast<const u32x4_any*>(p);
-    u32x4 v = {0, 0, 0, 0};
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-        if (i < avail) v[i >> 2] |= uint32_t(p[i]) << (8 * (i & 3));
-    return v;
-}
-__device__ __forceinline__ uint32_t load_codes(const uint8_t* p, int64_t avail, int want) {
-    uint32_t v = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (i < want && i < avail) v |= uint32_t(p[i]) << (8 * i);
-    return v;
-}
 
 // DIRECT: K is whole steps and every row starts on 16 bytes (scale words on 4), so steps go from global memory straight into
 // LDS, STAGES - 1 of them on their way.  Otherwise chunks pass through registers, with zeros behind a row's end, one step ahead.
@@ -944,6 +984,8 @@ void launch(const Args& a, const Plan& p, hipStream_t s) {
     } else if (p.bm == 128) {
         if constexpr (is_q(X))
             if (p.f8) launch_tile<Tile<X, WK, 128, 128, 2, 2, true, 2>, true>(a, p, s);
+        // Packed fp4 under dense rows: a wavefront takes all rows of the tile, so that each code is decoded once (NVFP4 [25600, 5120]
+        // x 2048 rows: 546 us against 611 with a quadrant each); the 8-bit kinds, cheaper to decode, read less LDS in quadrants.
         if (!is_q(X) || !p.f8) launch_tile<Tile<X, WK, 128, 128, is_fp4(WK) && !is_q(X) ? 1 : 2, is_fp4(WK) && !is_q(X) ? 4 : 2, false, 2>, true>(a, p, s);
     } else if constexpr (is_q(X)) {
         launch_tile<Tile<X, WK, 256, 256, 2, 4, true, 2>, false>(a, p, s);

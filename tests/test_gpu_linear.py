@@ -12,8 +12,8 @@ DEV = "cuda:0"
 DENSE = [(x, w) for x in ("bf16", "f16") for w in ("FP8_TENSOR", "FP8_BLOCK128", "NVFP4", "MXFP8", "MXFP4")]
 EIGHT = [("FP8_ROW", "FP8_TENSOR"), ("FP8_GROUP128", "FP8_BLOCK128"), ("MXFP8", "MXFP8"), ("MXFP8", "MXFP4")]
 SHAPES = [(1, 1, 32), (1, 64, 128), (3, 65, 96), (16, 80, 512), (17, 129, 160), (64, 64, 640), (65, 130, 320),
-          (130, 200, 1056), (5, 48, 4096), (257, 384, 256), (33, 16, 25600)]
-ODD_K = [(1, 5, 1), (2, 3, 15), (7, 33, 131), (66, 70, 257), (200, 128, 1001)]   # fp8 kinds: any K
+          (130, 200, 1056), (5, 48, 4096), (257, 384, 256), (33, 16, 25600), (1, 40, 2080), (11, 24, 1568)]
+ODD_K = [(1, 5, 1), (2, 3, 15), (7, 33, 131), (66, 70, 257), (200, 128, 1001), (1, 30, 1039), (1, 7, 5003), (16, 40, 2311), (3, 65, 513)]   # fp8 kinds: any K
 
 
 def _check(x, w, got, k, **kw):
@@ -48,7 +48,7 @@ def test_odd_k(xk, wk, m, n, k):
 
 
 @pytest.mark.parametrize("xk", ["bf16", "f16"])
-@pytest.mark.parametrize("m,n,k", [(1, 33, 16), (4, 20, 48), (70, 65, 5136)])
+@pytest.mark.parametrize("m,n,k", [(1, 33, 16), (4, 20, 48), (70, 65, 5136), (1, 34, 5136), (9, 33, 2608)])
 def test_nvfp4_k_of_16(xk, m, n, k):
     print(f"linear nvfp4 {xk} {m} {n} {k}", flush=True)
     x, w = ref.random_rows(st, xk, m, k, 5), ref.random_weight(st, "NVFP4", n, k, 6)
@@ -160,7 +160,7 @@ def test_one_hot_places_every_element(xk, wk):
 
 @pytest.mark.parametrize("xk,wk", [("bf16", "FP8_TENSOR"), ("f16", "NVFP4"), ("bf16", "MXFP4"), ("MXFP8", "MXFP8"),
                                    ("FP8_GROUP128", "FP8_BLOCK128")])
-@pytest.mark.parametrize("m", [1, 20])
+@pytest.mark.parametrize("m", [1, 5, 20])
 def test_weights_and_rows_at_any_byte(xk, wk, m):
     """Weights and scales as views into a blob at odd offsets, dense rows at an odd pitch."""
     n, k = 70, 320
