@@ -237,6 +237,30 @@ def test_encode_many_rows():
         _check_codes(st.quantize_activation(x.to(DEV), kind), x.double())
 
 
+@pytest.mark.parametrize("d", [512, 5120, 33024, 333])
+@pytest.mark.parametrize("kind", [0, 2, 4])
+@pytest.mark.parametrize("place", ["x", "residual"])
+def test_h_in_place(d, kind, place):
+    """Through the C entry: h may replace x or the residual."""
+    import ctypes as C
+
+    from device_checkpoint_dequantisation_amd import _lib
+    m, d = 5, d if kind != 4 else -(-d // 32) * 32
+    x, r, w = _norm_inputs(m, d, "bf16", 13, True, "bf16")
+    dx, dr, dw = x.to(DEV), r.to(DEV), w.to(DEV)
+    name = {0: None, 2: "FP8_ROW", 4: "MXFP8"}[kind]
+    want, h = st.rms_norm(dx, dw, residual=dr, quantize=name)
+    out = torch.zeros(m, d, dtype=torch.bfloat16 if kind == 0 else torch.uint8, device=DEV)
+    scale = torch.zeros(m * d, dtype=torch.uint8, device=DEV)
+    to = dx if place == "x" else dr
+    a = _lib.RmsNormArgs(dx.data_ptr(), dr.data_ptr(), dw.data_ptr(), to.data_ptr(), out.data_ptr(), scale.data_ptr(), m, d, d, d,
+                         1e-6, 0, 0, 0, kind)
+    _lib.check(_lib.lib().st_rms_norm(C.byref(a), torch.cuda.current_stream().cuda_stream), "st_rms_norm")
+    torch.cuda.synchronize()
+    assert torch.equal(to, h)
+    assert torch.equal(_bits(out), _bits(want if kind == 0 else want.data))
+
+
 def test_calls_on_another_stream():
     x = _x(64, 4096, "bf16", 12)
     s = torch.cuda.Stream(DEV)

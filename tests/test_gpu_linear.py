@@ -301,6 +301,54 @@ def test_captured_calls_replay(xk, wk, m):
             assert torch.equal(y, want)
 
 
+def test_two_streams_at_once():
+    """Products whose K is split, on two streams at the same time: each has its own workspace."""
+    w = ref.to(ref.random_weight(st, "NVFP4", 256, 16384, 50), DEV)
+    xs = [ref.random_rows(st, "bf16", m, 16384, 51).to(DEV) for m in (4, 40)]
+    want = [st.linear(x, w) for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(DEV) for _ in xs]
+    got = [[], []]
+    for _ in range(8):
+        for i, (x, s) in enumerate(zip(xs, streams)):
+            with torch.cuda.stream(s):
+                got[i].append(st.linear(x, w))
+    torch.cuda.synchronize()
+    for ys, y in zip(got, want):
+        assert all(torch.equal(t, y) for t in ys)
+
+
+def test_refusals_on_the_gpu():
+    x, w = ref.random_rows(st, "bf16", 4, 64, 52).to(DEV), ref.to(ref.random_weight(st, "FP8_TENSOR", 64, 64, 53), DEV)
+    with pytest.raises(ValueError, match="overlaps"):
+        st.linear(x, w, out=x)
+    buf = torch.zeros(5, 64, dtype=torch.bfloat16, device=DEV)
+    with pytest.raises(ValueError, match="overlaps"):
+        st.linear(x, w, residual=buf[:4], out=buf[1:])
+    with pytest.raises(ValueError, match="stride 1"):
+        st.linear(torch.zeros(64, 4, dtype=torch.bfloat16, device=DEV).t(), w)
+    with pytest.raises(ValueError, match="bias"):
+        st.linear(x, w, bias=torch.zeros(63, device=DEV))
+    with pytest.raises(ValueError, match="residual"):
+        st.linear(x, w, residual=torch.zeros(64, device=DEV))
+    with pytest.raises(ValueError, match="tensors on"):
+        st.linear(x, w, bias=torch.zeros(64))
+    with pytest.raises(ValueError, match="activation"):
+        st.linear(x, w, activation="tanh")
+    with pytest.raises(ValueError, match="out_dtype"):
+        st.linear(x, w, out_dtype="f64")
+    with pytest.raises(ValueError, match="out is"):
+        st.linear(x, w, out=buf[:4], out_dtype="f32")
+    with pytest.raises(RuntimeError, match="no backward"):
+        st.linear(x.clone().requires_grad_(), w)
+    with pytest.raises(ValueError, match="residual"):
+        st.rms_norm(x, residual=x.float())
+    with pytest.raises(ValueError, match="gate"):
+        st.quantize_activation(x, "MXFP8", gate=x[:2])
+    with pytest.raises(ValueError, match="exclude"):
+        st.rms_norm(x, quantize="MXFP8", out_dtype="f32")
+
+
 def test_same_bits_every_time():
     """K split over workgroups joins in a fixed order."""
     x, w = ref.random_rows(st, "bf16", 4, 16384, 30).to(DEV), ref.to(ref.random_weight(st, "FP8_TENSOR", 100, 16384, 31), DEV)
