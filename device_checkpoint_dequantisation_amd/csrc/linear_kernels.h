@@ -921,7 +921,6 @@ __global__ __launch_bounds__(T::THREADS, 2) void linear_tile(Args a) {
                 const int xe = en;
                 const float xf = fn * gs;
                 if (j + 1 < MT) next(j + 1);
-                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int i = 0; i < NT; ++i) {
                     if constexpr (T::GROUPED) {
@@ -932,7 +931,6 @@ __global__ __launch_bounds__(T::THREADS, 2) void linear_tile(Args a) {
                         acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wv[i], xv, acc[i][j], T::FP4 ? 4 : 0, 0, 0, we[i], 0, xe);
                     }
                 }
-                __builtin_amdgcn_sched_barrier(0);
             }
         }
         if (i + S - 1 < count) commit(fill);
