@@ -29,6 +29,8 @@
 //  * linear_join: adds the fp32 partial results where K was split over workgroups, in a fixed order.
 #pragma once
 
+#include <type_traits>
+
 #include "linear.h"
 #include "st_device.h"
 
@@ -660,20 +662,21 @@ __global__ __launch_bounds__(T::THREADS, 2) void linear_tile(Args a) {
     auto xr = [&](uint32_t r) { return m0 + r < a.m ? m0 + r : a.m - 1; };
     auto wr = [&](uint32_t r) { return n0 + r < a.n ? n0 + r : a.n - 1; };
 
-    // Direct loads: 32-bit offsets from the tile's first row, the step's offset added by the scalar unit
+    // Offsets from the tile's first row, the step's offset added by the scalar unit.  DIRECT loads take 32-bit ones (the host
+    // sends rows too far apart for them the other way) and swap chunks on the way, since their place in LDS is fixed; the others
+    // swap when they write LDS.
+    using Off = std::conditional_t<DIRECT, uint32_t, uint64_t>;
     const __amdgpu_buffer_rsrc_t bx = rows_at(a.x + m0 * x_row), bw = rows_at(a.w + n0 * w_row);
-    uint32_t x_off[T::X_PER], w_off[T::W_PER];
-    if constexpr (DIRECT) {
+    Off x_off[T::X_PER], w_off[T::W_PER];
 #pragma unroll
-        for (int i = 0; i < T::X_PER; ++i) {
-            const int s = i * T::THREADS + tid, r = s / T::XC, c = (s % T::XC) ^ (r & 7);
-            x_off[i] = (xr(r) - m0) * uint32_t(x_row) + c * 16;
-        }
+    for (int i = 0; i < T::X_PER; ++i) {
+        const int s = i * T::THREADS + tid, r = s / T::XC, c = (s % T::XC) ^ (DIRECT ? r & 7 : 0);
+        x_off[i] = Off(xr(r) - m0) * Off(x_row) + c * 16;
+    }
 #pragma unroll
-        for (int i = 0; i < T::W_PER; ++i) {
-            const int s = i * T::THREADS + tid, r = s / T::WC, c = (s % T::WC) ^ ((r / (8 / T::WC)) & (T::WC - 1));
-            w_off[i] = s < T::BN * T::WC ? (wr(r) - n0) * uint32_t(w_row) + c * 16 : 0;
-        }
+    for (int i = 0; i < T::W_PER; ++i) {
+        const int s = i * T::THREADS + tid, r = s / T::WC, c = (s % T::WC) ^ (DIRECT ? (r / (8 / T::WC)) & (T::WC - 1) : 0);
+        w_off[i] = s < T::BN * T::WC ? Off(wr(r) - n0) * Off(w_row) + c * 16 : 0;
     }
     const uint64_t xs_row = X == ST_X_MXFP8 ? a.k / 32 : 4ull * groups;
     const int uwave = __builtin_amdgcn_readfirstlane(wave);
@@ -697,27 +700,21 @@ __global__ __launch_bounds__(T::THREADS, 2) void linear_tile(Args a) {
             for (int i = 0; i < T::W_PER; ++i)
                 if (T::BN * T::WC % T::THREADS == 0 || i * T::THREADS + uwave * 64 < T::BN * T::WC)
                     to_lds(bw, sw + (i * T::THREADS + wave * 64) * 16, w_off[i], uint32_t(wb));
-        } else if (uint64_t(step + 1) * T::KS <= a.k) {
-#pragma unroll
-            for (int i = 0; i < T::X_PER; ++i) {
-                const int s = i * T::THREADS + tid, r = s / T::XC, c = s % T::XC;
-                rx[i] = *reinterpret_cast<const u32x4_any*>(a.x + xr(r) * x_row + kb + c * 16);
-            }
-#pragma unroll
-            for (int i = 0; i < T::W_PER; ++i) {
-                const int s = i * T::THREADS + tid, r = s / T::WC, c = s % T::WC;
-                if (s < T::BN * T::WC) rw[i] = *reinterpret_cast<const u32x4_any*>(a.w + wr(r) * w_row + wb + c * 16);
-            }
         } else {
+            const uint8_t* px = a.x + m0 * x_row + kb;
+            const uint8_t* pw = a.w + n0 * w_row + wb;
+            if (uint64_t(step + 1) * T::KS <= a.k) {
 #pragma unroll
-            for (int i = 0; i < T::X_PER; ++i) {
-                const int s = i * T::THREADS + tid, r = s / T::XC, c = s % T::XC;
-                rx[i] = load_chunk(a.x + xr(r) * x_row + kb + c * 16, int64_t(x_len) - int64_t(kb + c * 16));
-            }
+                for (int i = 0; i < T::X_PER; ++i) rx[i] = *reinterpret_cast<const u32x4_any*>(px + x_off[i]);
 #pragma unroll
-            for (int i = 0; i < T::W_PER; ++i) {
-                const int s = i * T::THREADS + tid, r = s / T::WC, c = s % T::WC;
-                if (s < T::BN * T::WC) rw[i] = load_chunk(a.w + wr(r) * w_row + wb + c * 16, int64_t(w_row) - int64_t(wb + c * 16));
+                for (int i = 0; i < T::W_PER; ++i) rw[i] = *reinterpret_cast<const u32x4_any*>(pw + w_off[i]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < T::X_PER; ++i)
+                    rx[i] = load_chunk(px + x_off[i], int64_t(x_len) - int64_t(kb + (i * T::THREADS + tid) % T::XC * 16));
+#pragma unroll
+                for (int i = 0; i < T::W_PER; ++i)
+                    rw[i] = load_chunk(pw + w_off[i], int64_t(w_row) - int64_t(wb + (i * T::THREADS + tid) % T::WC * 16));
             }
         }
         if constexpr (DIRECT && T::X_WAVES + T::W_WAVES != 0) {
