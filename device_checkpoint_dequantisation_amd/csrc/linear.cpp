@@ -37,16 +37,20 @@ Plan plan_of(const st_linear_args& g) {
     }
     const uint64_t ks = q ? 128 : 64;
     p.direct = p.direct && xb < (1u << 22) && wb < (1u << 22);     // 256 rows within 32-bit offsets
-    p.direct = p.direct && g.k % ks == 0;
-    if (is_mx(g.w_kind) || g.w_kind == ST_KIND_NVFP4) p.direct = p.direct && al(g.w_scale, 4) && (q || !is_mx(g.w_kind) || g.k % 128 == 0);
-    if (g.x_type == ST_X_MXFP8) p.direct = p.direct && al(g.x_scale, 4);
+    bool whole = g.k % ks == 0;
+    if (is_mx(g.w_kind) || g.w_kind == ST_KIND_NVFP4) whole = whole && al(g.w_scale, 4) && (q || !is_mx(g.w_kind) || g.k % 128 == 0);
+    if (g.x_type == ST_X_MXFP8) whole = whole && al(g.x_scale, 4);
+    p.tail = p.direct && !whole;
     p.bm = g.m <= 64 ? 64 : 128;
     // e4m3 x, 16-bit output: tiles of 256 halve the bytes that pass through L2 and LDS per product, and leave one workgroup
     // per CU (8192 rows through MXFP8 [12288, 4096]: 475 us against 601 in tiles of 128; 4096 rows through block FP8
     // [4096, 12288], 256 tiles: 269 against 284; with fewer tiles than CUs the smaller ones win).  bf16 and fp16 x gain nothing
     // (NVFP4 prefill 623 against 615 us).
+    // Blocks' scale words that pass through registers do not fit beside the sums of a tile of 256 (6000 rows through MXFP8
+    // [6000, 5024], a partial last step: 744 us in tiles of 256, 336 in tiles of 128).
     const uint64_t tiles256 = ((g.m + 255) / 256) * ((g.n + 255) / 256);
-    if (q && p.direct && g.m > 64 && g.out_type != ST_OUT_F32 && tiles256 >= 256) p.bm = 256;
+    const bool fits = p.direct && !(p.tail && is_mx(g.w_kind));
+    if (q && fits && g.m > 64 && g.out_type != ST_OUT_F32 && tiles256 >= 256) p.bm = 256;
     p.bn = p.bm;
     p.f8 = q && p.bm > 64 && g.out_type != ST_OUT_F32;
     const uint64_t tiles = ((g.m + p.bm - 1) / p.bm) * ((g.n + p.bn - 1) / p.bn), all = (g.k + ks - 1) / ks;

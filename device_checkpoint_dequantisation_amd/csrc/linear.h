@@ -32,7 +32,8 @@ struct Args {
 
 // How a product is cut into workgroups.
 struct Plan {
-    bool direct;                 // rows start on 16 bytes and K is whole steps: global memory to LDS without a detour
+    bool direct;                 // rows start and end on 16 bytes: global memory to LDS without a detour
+    bool tail;                   // direct, with a partial last step of K or scale words off 4 bytes
     bool f8;                     // the f8f6f4 matrix instructions
     bool one;                    // linear_one
     bool few;                    // linear_few

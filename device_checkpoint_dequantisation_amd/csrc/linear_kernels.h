@@ -613,8 +613,12 @@ struct Tile {
     }
 };
 
-// DIRECT: K is whole steps and every row starts on 16 bytes (scale words on 4), so steps go from global memory straight into
-// LDS, STAGES - 1 of them on their way.  Otherwise chunks pass through registers, with zeros behind a row's end, one step ahead.
+// How a step's bytes reach LDS.  WHOLE: K is whole steps and every row starts on 16 bytes (scale words on 4), so they go there
+// straight from global memory, STAGES - 1 steps on their way.  TAIL: rows start and end on 16 bytes; as WHOLE, except that a
+// last, partial step (zeros behind the rows' ends) and the scale words of blocks pass through registers.  ANY: all of it passes through
+// registers, one step ahead.  2000 bf16 rows through FP8 [5000, K]: K 4992 WHOLE 104 us, K 5008 TAIL 128 (ANY 162), K 5003 ANY 196;
+// through MXFP8 with MXFP8 rows: K 4992 WHOLE 93, K 5024 TAIL 129 (ANY 210).
+enum Path { ANY, TAIL, WHOLE };
 // s_waitcnt for vmcnt(n) and lgkmcnt(0), expcnt at its maximum (gfx9 encoding: vmcnt in bits 3:0 and 15:14)
 constexpr int wait_vmem(int n) { return (n & 15) | (n >> 4) << 14 | 7 << 4; }
 // A wave-uniform fp32 that the kernel never writes, by the scalar unit.
@@ -630,9 +634,12 @@ __device__ __forceinline__ void to_lds(__amdgpu_buffer_rsrc_t base, uint8_t* to,
     __builtin_amdgcn_raw_ptr_buffer_load_lds(base, (__attribute__((address_space(3))) void*)to, 16, int(voff), int(soff), 0, 0);
 }
 
-template <class T, bool DIRECT>
+template <class T, Path PATH>
 __global__ __launch_bounds__(T::THREADS, 2) void linear_tile(Args a) {
     constexpr int X = T::X, WK = T::WK, MT = T::MT, NT = T::NT;
+    constexpr bool DIRECT = PATH != ANY;
+    // scale words straight to LDS: a group's fp32 are whole words in every row
+    constexpr bool SCALES = T::X_WAVES + T::W_WAVES != 0, WORDS = SCALES && (PATH == WHOLE || (DIRECT && X == ST_X_FP8_GROUP128));
     constexpr int S = DIRECT ? T::STAGES : 2;
     __shared__ __align__(128) uint8_t lds[S][T::STAGE];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -681,18 +688,30 @@ __global__ __launch_bounds__(T::THREADS, 2) void linear_tile(Args a) {
     const uint64_t xs_row = X == ST_X_MXFP8 ? a.k / 32 : 4ull * groups;
     const int uwave = __builtin_amdgcn_readfirstlane(wave);
     const bool x_scales = uwave < T::X_WAVES;
-    const __amdgpu_buffer_rsrc_t bs = rows_at(x_scales ? a.xs + m0 * xs_row : a.ws + n0 * ws_row);
+    const uint8_t* scales = x_scales ? a.xs + m0 * xs_row : a.ws + n0 * ws_row;
+    const __amdgpu_buffer_rsrc_t bs = rows_at(scales);
     uint32_t s_off = 0;
-    if constexpr (DIRECT && T::X_WAVES + T::W_WAVES != 0)
+    if constexpr (SCALES)
         s_off = x_scales ? (xr(tid) - m0) * uint32_t(xs_row) : (wr(tid - T::X_WAVES * 64) - n0) * uint32_t(ws_row);
     u32x4 rx[DIRECT ? 1 : T::X_PER], rw[DIRECT ? 1 : T::W_PER];      // chunks on their way through registers
-    uint32_t rxs = 0, rws = 0;
+    uint32_t word = 0;                                               // and a row's scales
 
     auto issue = [&](uint32_t step, int buf) {
         const uint64_t kb = uint64_t(step) * T::XB, wb = uint64_t(step) * T::WB;
         uint8_t* sx = lds[buf];
         uint8_t* sw = lds[buf] + T::BM * T::XB;
-        if constexpr (DIRECT) {
+        const bool whole = uint64_t(step + 1) * T::KS <= a.k;
+        if constexpr (SCALES && !WORDS) {
+            if (uwave < T::X_WAVES + T::W_WAVES) {
+                const uint32_t bytes = x_scales ? T::XSB : T::WSB, at = step * bytes;
+                const uint8_t* p = scales + at + s_off;
+                if (!whole && !(X == ST_X_FP8_GROUP128 && x_scales))
+                    word = load_codes(p, int64_t(x_scales ? xs_row : ws_row) - at, bytes);
+                else if (bytes == 4) word = *reinterpret_cast<const u32_any*>(p);
+                else word = *reinterpret_cast<const u16_any*>(p);
+            }
+        }
+        if (DIRECT && (PATH == WHOLE || whole)) {
 #pragma unroll
             for (int i = 0; i < T::X_PER; ++i)
                 to_lds(bx, sx + (i * T::THREADS + wave * 64) * 16, x_off[i], uint32_t(kb));
@@ -700,10 +719,28 @@ __global__ __launch_bounds__(T::THREADS, 2) void linear_tile(Args a) {
             for (int i = 0; i < T::W_PER; ++i)
                 if (T::BN * T::WC % T::THREADS == 0 || i * T::THREADS + uwave * 64 < T::BN * T::WC)
                     to_lds(bw, sw + (i * T::THREADS + wave * 64) * 16, w_off[i], uint32_t(wb));
-        } else {
+        } else if constexpr (PATH == TAIL) {
+            // once per tile: a loop that keeps the registers of the others free
+#pragma unroll 1
+            for (int s = tid; s < T::BM * T::XC; s += T::THREADS) {
+                const int r = s / T::XC, c = (s % T::XC) ^ (r & 7);
+                u32x4 v = {0, 0, 0, 0};
+                if (kb + c * 16 < x_len) v = *reinterpret_cast<const u32x4*>(a.x + xr(r) * x_row + kb + c * 16);
+                *reinterpret_cast<u32x4*>(sx + s * 16) = v;
+            }
+#pragma unroll 1
+            for (int s = tid; s < T::BN * T::WC; s += T::THREADS) {
+                const int r = s / T::WC, c = (s % T::WC) ^ ((r / (8 / T::WC)) & (T::WC - 1));
+                u32x4 v = {0, 0, 0, 0};
+                if (wb + c * 16 < w_row) v = *reinterpret_cast<const u32x4*>(a.w + wr(r) * w_row + wb + c * 16);
+                *reinterpret_cast<u32x4*>(sw + s * 16) = v;
+            }
+            // a wavefront with no chunk of this step has loaded nothing, which the loop's counts do not know
+            __builtin_amdgcn_s_waitcnt(wait_vmem(0));
+        } else if constexpr (PATH == ANY) {
             const uint8_t* px = a.x + m0 * x_row + kb;
             const uint8_t* pw = a.w + n0 * w_row + wb;
-            if (uint64_t(step + 1) * T::KS <= a.k) {
+            if (whole) {
 #pragma unroll
                 for (int i = 0; i < T::X_PER; ++i) rx[i] = *reinterpret_cast<const u32x4_any*>(px + x_off[i]);
 #pragma unroll
@@ -717,30 +754,18 @@ __global__ __launch_bounds__(T::THREADS, 2) void linear_tile(Args a) {
                     rw[i] = load_chunk(pw + w_off[i], int64_t(w_row) - int64_t(wb + (i * T::THREADS + tid) % T::WC * 16));
             }
         }
-        if constexpr (DIRECT && T::X_WAVES + T::W_WAVES != 0) {
+        if constexpr (WORDS) {
             if (uwave < T::X_WAVES + T::W_WAVES)
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(
                     bs, (__attribute__((address_space(3))) void*)(sw + T::BN * T::WB + wave * 256), 4, int(s_off),
                     int(T::WSB == 2 ? step / 2 * 4 : step * 4), 0, 0);
         }
-        if constexpr (T::XSB != 0 && !DIRECT) {
-            if (tid < T::BM) {
-                if constexpr (X == ST_X_FP8_GROUP128)
-                    rxs = *reinterpret_cast<const uint32_t*>(a.xs + 4 * (uint64_t(xr(tid)) * groups + step));
-                else
-                    rxs = load_codes(a.xs + uint64_t(xr(tid)) * (a.k / 32) + step * 4ull, int64_t(a.k / 32) - step * 4ll, 4);
-            }
-        }
-        if constexpr (T::WSB != 0 && !DIRECT) {
-            if (tid < T::BN)
-                rws = load_codes(a.ws + wr(tid) * ws_row + uint64_t(step) * T::WSB, int64_t(ws_row) - int64_t(step) * T::WSB, T::WSB);
-        }
     };
     // What issue() left in registers goes to LDS.
     auto commit = [&](int buf) {
-        if constexpr (!DIRECT) {
-            uint8_t* sx = lds[buf];
-            uint8_t* sw = lds[buf] + T::BM * T::XB;
+        uint8_t* sx = lds[buf];
+        uint8_t* sw = lds[buf] + T::BM * T::XB;
+        if constexpr (PATH == ANY) {
 #pragma unroll
             for (int i = 0; i < T::X_PER; ++i) {
                 const int s = i * T::THREADS + tid;
@@ -751,10 +776,9 @@ __global__ __launch_bounds__(T::THREADS, 2) void linear_tile(Args a) {
                 const int s = i * T::THREADS + tid;
                 if (s < T::BN * T::WC) *reinterpret_cast<u32x4*>(sw + T::w_at(s / T::WC, s % T::WC)) = rw[i];
             }
-            uint32_t* ss = reinterpret_cast<uint32_t*>(sw + T::BN * T::WB);
-            if (T::XSB != 0 && tid < T::BM) ss[tid] = rxs;
-            if (T::XSB != 0) ss += T::BM;
-            if (T::WSB != 0 && tid < T::BN) ss[tid] = rws;
+        }
+        if constexpr (SCALES && !WORDS) {
+            if (uwave < T::X_WAVES + T::W_WAVES) reinterpret_cast<uint32_t*>(sw + T::BN * T::WB)[tid] = word;
         }
     };
 
@@ -766,7 +790,7 @@ __global__ __launch_bounds__(T::THREADS, 2) void linear_tile(Args a) {
 
     // loads of a step that this wavefront issues: BASE, one more with weight chunks left over, one more with scale words
     constexpr int BASE = T::X_PER + T::BN * T::WC / T::THREADS;
-    const int loads = BASE + (uwave * 64 < T::BN * T::WC % T::THREADS ? 1 : 0) + (uwave < T::X_WAVES + T::W_WAVES ? 1 : 0);
+    const int loads = BASE + (uwave * 64 < T::BN * T::WC % T::THREADS ? 1 : 0) + (WORDS && uwave < T::X_WAVES + T::W_WAVES ? 1 : 0);
     const uint32_t count = last > first ? last - first : 0;
 #pragma unroll
     for (int i = 0; i < S - 1; ++i)
@@ -813,7 +837,7 @@ __global__ __launch_bounds__(T::THREADS, 2) void linear_tile(Args a) {
 #pragma unroll
                 for (int i = 0; i < NT; ++i) {
                     const int r = (wn * NT + i) * 16 + row;
-                    const float s = T::WSB ? scale_of<WK>(sws[r * 4 + (WK == ST_KIND_NVFP4 ? q : 2 * (T::WSB == 2 ? (DIRECT ? step & 1 : 0) : h) + (q >> 1))]) : 1.0f;
+                    const float s = T::WSB ? scale_of<WK>(sws[r * 4 + (WK == ST_KIND_NVFP4 ? q : 2 * (T::WSB == 2 ? (PATH == WHOLE ? step & 1 : 0) : h) + (q >> 1))]) : 1.0f;
                     if constexpr (T::FP4) {
                         const u32x2 c = *reinterpret_cast<const u32x2*>(sw + T::w_at(r, 2 * h + (q >> 1)) + (q & 1) * 8);
                         wv[i][0] = codes8<D::F16, WK>(c.x, 0, s);
@@ -958,11 +982,14 @@ __global__ __launch_bounds__(T::THREADS, 2) void linear_tile(Args a) {
 
 // ------------------------------------------------------------------------- launches
 
-template <class T, bool ANY>
+template <class T, bool LARGE>
 void launch_tile(const Args& a, const Plan& p, hipStream_t s) {
     const dim3 grid(a.tiles_m * a.tiles_n, a.splits), block(T::THREADS);
-    if (p.direct) hipLaunchKernelGGL((linear_tile<T, true>), grid, block, 0, s, a);
-    else if constexpr (ANY) hipLaunchKernelGGL((linear_tile<T, false>), grid, block, 0, s, a);
+    if (p.direct && !p.tail) hipLaunchKernelGGL((linear_tile<T, WHOLE>), grid, block, 0, s, a);
+    if constexpr (!LARGE || !is_mx(T::WK))
+        if (p.direct && p.tail) hipLaunchKernelGGL((linear_tile<T, TAIL>), grid, block, 0, s, a);
+    if constexpr (!LARGE)
+        if (!p.direct) hipLaunchKernelGGL((linear_tile<T, ANY>), grid, block, 0, s, a);
 }
 
 template <int X, int WK>
@@ -975,15 +1002,15 @@ void launch(const Args& a, const Plan& p, hipStream_t s) {
         const dim3 grid((a.n + 16 * Few<X, WK>::NT - 1) / (16 * Few<X, WK>::NT), a.splits), block(64 * p.waves);
         hipLaunchKernelGGL((linear_few<Few<X, WK>>), grid, block, 0, s, a);
     } else if (p.bm == 64) {
-        launch_tile<Tile<X, WK, 64, 64, 2, 2, false, 4>, true>(a, p, s);
+        launch_tile<Tile<X, WK, 64, 64, 2, 2, false, 4>, false>(a, p, s);
     } else if (p.bm == 128) {
         if constexpr (is_q(X))
-            if (p.f8) launch_tile<Tile<X, WK, 128, 128, 2, 2, true, 2>, true>(a, p, s);
+            if (p.f8) launch_tile<Tile<X, WK, 128, 128, 2, 2, true, 2>, false>(a, p, s);
         // Packed fp4 under dense rows: a wavefront takes all rows of the tile, so that each code is decoded once (NVFP4 [25600, 5120]
         // x 2048 rows: 546 us against 611 with a quadrant each); the 8-bit kinds, cheaper to decode, read less LDS in quadrants.
-        if (!is_q(X) || !p.f8) launch_tile<Tile<X, WK, 128, 128, is_fp4(WK) && !is_q(X) ? 1 : 2, is_fp4(WK) && !is_q(X) ? 4 : 2, false, 2>, true>(a, p, s);
+        if (!is_q(X) || !p.f8) launch_tile<Tile<X, WK, 128, 128, is_fp4(WK) && !is_q(X) ? 1 : 2, is_fp4(WK) && !is_q(X) ? 4 : 2, false, 2>, false>(a, p, s);
     } else if constexpr (is_q(X)) {
-        launch_tile<Tile<X, WK, 256, 256, 2, 4, true, 2>, false>(a, p, s);
+        launch_tile<Tile<X, WK, 256, 256, 2, 4, true, 2>, true>(a, p, s);
     }
     if (a.part) {
         const uint64_t items = uint64_t((a.n + 3) / 4) * a.m;

@@ -108,6 +108,30 @@ def test_exact_sums(xk, wk, m, n, k):
 
 
 @pytest.mark.parametrize("xk,wk", DENSE + EIGHT)
+@pytest.mark.parametrize("m,n,k", [(20, 70, 32), (50, 65, 96), (40, 70, 2080), (130, 140, 160), (200, 300, 1056), (140, 130, 5152)])
+@pytest.mark.parametrize("at", [0, 1])
+def test_partial_last_step(xk, wk, m, n, k, at):
+    """Rows that start and end on 16 bytes with K off the tiles' steps, the scale words on and off 4 bytes."""
+    print(f"tail {xk} {wk} {m} {n} {k} {at}", flush=True)
+    x, w = ref.random_rows(st, xk, m, k, 51), ref.random_weight(st, wk, n, k, 52)
+    xd, wd = ref.to(x, DEV), ref.to(w, DEV)
+    for t in (xd, wd):
+        if at and not torch.is_tensor(t) and t.scale.dtype != torch.float32:
+            raw = torch.empty(t.scale.numel() + 1, dtype=torch.uint8, device=DEV)[1:]
+            raw.copy_(t.scale.view(torch.uint8).flatten())
+            t.scale = raw.view(t.scale.dtype).view(t.scale.shape)
+    _check(x, w, st.linear(xd, wd, out_dtype="f32"), k)
+    _check(x, w, st.linear(xd, wd), k)
+
+
+@pytest.mark.parametrize("xk,wk", DENSE + EIGHT)
+@pytest.mark.parametrize("m,n,k", [(4100, 4097, 160), (4096, 4352, 416)])
+def test_many_tiles_partial_last_step(xk, wk, m, n, k):
+    """As test_many_tiles."""
+    test_many_tiles(xk, wk, m, n, k)
+
+
+@pytest.mark.parametrize("xk,wk", DENSE + EIGHT)
 @pytest.mark.parametrize("m,n,k", [(1500, 1100, 256), (4100, 4097, 128), (4096, 4352, 384)])
 def test_many_tiles(xk, wk, m, n, k):
     """Whole and ragged bands of tiles, of every tile size; the 64-bit products on the GPU."""
