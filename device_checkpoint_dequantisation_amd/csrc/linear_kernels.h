@@ -690,9 +690,9 @@ __global__ __launch_bounds__(T::THREADS, 2) void linear_tile(Args a) {
     const bool x_scales = uwave < T::X_WAVES;
     const uint8_t* scales = x_scales ? a.xs + m0 * xs_row : a.ws + n0 * ws_row;
     const __amdgpu_buffer_rsrc_t bs = rows_at(scales);
-    uint32_t s_off = 0;
+    Off s_off = 0;
     if constexpr (SCALES)
-        s_off = x_scales ? (xr(tid) - m0) * uint32_t(xs_row) : (wr(tid - T::X_WAVES * 64) - n0) * uint32_t(ws_row);
+        s_off = x_scales ? Off(xr(tid) - m0) * Off(xs_row) : Off(wr(tid - T::X_WAVES * 64) - n0) * Off(ws_row);
     u32x4 rx[DIRECT ? 1 : T::X_PER], rw[DIRECT ? 1 : T::W_PER];      // chunks on their way through registers
     uint32_t word = 0;                                               // and a row's scales
 
