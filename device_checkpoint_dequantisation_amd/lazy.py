@@ -730,7 +730,8 @@ class LazyModuleLoader:
             mod.forward = forward
         elif type(mod).forward is torch.nn.RMSNorm.forward and len(mod.normalized_shape) == 1:
             def forward(x):
-                return ops.rms_norm(x, mod.weight, eps=torch.finfo(x.dtype).eps if mod.eps is None else mod.eps)
+                # a norm without an eps computes in fp32 for 16-bit rows too, and takes fp32's
+                return ops.rms_norm(x, mod.weight, eps=torch.finfo(torch.float32).eps if mod.eps is None else mod.eps)
             mod.forward = forward
 
     def _pre_hook(self, mod, args):

@@ -134,3 +134,22 @@ def test_refusals(tmp_path):
     with pytest.raises(RuntimeError, match="no backward"):
         lin(torch.zeros(2, 320, device=DEV, dtype=torch.bfloat16, requires_grad=True))
     loader.detach()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_norm_without_an_eps_of_its_own(dtype, tmp_path):
+    """nn.RMSNorm's default eps against torch's norm, over rows from 1e-4 to 10."""
+    sd = st.StreamStateDict(_file(tmp_path, 3), DEV)
+    root = torch.nn.Module()
+    root.norm = torch.nn.RMSNorm(320, device="meta", dtype=torch.bfloat16)
+    loader = st.LazyModuleLoader(root, st.RenameViewStateDict(sd, {"model.layers.0.input_layernorm.weight": "norm.weight"}),
+                                 strict=False, quantized="weights")
+    g = torch.Generator().manual_seed(4)
+    x = torch.cat([torch.randn(3, 320, generator=g) * 10.0 ** e for e in range(-4, 2)]).to(dtype)
+    w = sd["model.layers.0.input_layernorm.weight"].cpu()
+    want = torch.nn.functional.rms_norm(x.float(), (320,), w.float()).double()
+    got = root.norm(x.to(DEV)).cpu().double()
+    # one rounding to the rows' type, and the 32-bit form's own handful
+    t = torch.finfo(dtype)
+    assert ((got - want).abs() <= want.abs() * (t.eps / 2 + 16 * 2.0 ** -24) + t.smallest_normal * t.eps / 2).all()
+    loader.detach()
