@@ -661,6 +661,47 @@ class DiskRef:
     meta: OutputMeta
 
 
+def _stored_bytes(q) -> int:
+    return sum(t.numel() * t.element_size() for t in (q.data, q.scale, q.scale2) if t is not None)
+
+
+class _Forward:
+    """A module's forward through the operators, while ``loader`` is attached; afterwards the module's own.  An
+    object and not a closure, so that a deep copy of the module takes the copied loader and module."""
+
+    def __init__(self, loader, mod):
+        self.loader, self.mod = loader, mod
+
+
+class _StoredLinear(_Forward):
+    def __init__(self, loader, mod, encode: str | None):
+        super().__init__(loader, mod)
+        self.encode = encode      # the inputs' 8-bit kind, or None
+
+    def __call__(self, x):
+        mod = self.mod
+        if self.loader is None or not mod.weight.is_meta:      # detached, or a weight that was assigned since
+            return type(mod).forward(mod, x)
+        from . import ops
+        if self.loader._stored[mod] is None:
+            self.loader.materialize(mod)
+        torch = _torch()
+        dtype = {torch.bfloat16: "bf16", torch.float16: "f16"}.get(x.dtype)      # another type is refused by the operator
+        if self.encode is not None and dtype is not None:
+            x = ops.quantize_activation(x, self.encode)
+        return ops.linear(x, self.loader._stored[mod], bias=mod.bias, out_dtype=dtype)
+
+
+class _OperatorNorm(_Forward):
+    def __call__(self, x):
+        mod = self.mod
+        if self.loader is None:
+            return type(mod).forward(mod, x)
+        from . import ops
+        # a norm without an eps computes in fp32 for 16-bit rows too, and takes fp32's
+        return ops.rms_norm(x, mod.weight, eps=_torch().finfo(_torch().float32).eps if mod.eps is None else mod.eps)
+
+
 class LazyModuleLoader:
     """Turns the parameters of ``module`` that ``state_dict`` holds into meta tensors with a
     :class:`DiskRef` each, and registers a ``forward_pre_hook`` on every submodule owning such a
@@ -675,7 +716,8 @@ class LazyModuleLoader:
     stored weight, a half or a quarter of the decoded one, is what loads and counts against the bound) and every ``nn.RMSNorm``
     over one dimension through :func:`rms_norm`; "activations" also encodes those linears' inputs in the 8-bit kind that goes
     with the weight (NVFP4 weights keep dense inputs).  Inference only, for bf16 and fp16 inputs; subclasses with a
-    forward of their own are left alone."""
+    forward of their own are left alone.  A module takes one such loader at a time; :meth:`detach` gives it its own
+    forward back, and its stored weight up."""
 
     def __init__(self, module, state_dict, max_resident_bytes: int | None = None, strict: bool = True,
                  quantized: str | None = None):
@@ -689,6 +731,7 @@ class LazyModuleLoader:
         self.refs = {}            # (submodule, param name) -> DiskRef
         self._owned = collections.defaultdict(list)  # submodule -> [param name]
         self._stored = {}         # submodule computing on its stored weight -> QuantizedWeight, None while evicted
+        self._forwards = {}       # submodule -> the forward it has from this loader
         self._resident = collections.OrderedDict()   # submodule -> bytes, LRU order
         self.resident_bytes = 0
         self.stats = collections.Counter()
@@ -700,6 +743,9 @@ class LazyModuleLoader:
         missing = [n for n in names if n not in state_dict]
         if strict and missing:
             raise KeyError(f"{len(missing)} parameters are not in the state dict, e.g. {missing[:3]}")
+        for full, (mod, _, _) in names.items():
+            if isinstance(mod.__dict__.get("forward"), _Forward):
+                raise ValueError(f"{full}: its module computes on the stored weights of another loader; detach that one first")
         for full, (mod, pname, p) in names.items():
             if full not in state_dict:
                 continue
@@ -709,30 +755,24 @@ class LazyModuleLoader:
             self.refs[(mod, pname)] = DiskRef(state_dict, full, meta)
             self._owned[mod].append(pname)
             mod._parameters[pname] = torch.nn.Parameter(state_dict.meta_tensor(full), requires_grad=False)
-            if quantized and pname == "weight":
-                self._compute_on_stored(mod, meta)
+        if quantized:
+            for (mod, pname), ref in self.refs.items():
+                fwd = self._compute_on_stored(mod, ref.meta) if pname == "weight" else None
+                if fwd is not None:
+                    mod.forward = self._forwards[mod] = fwd
         self._hooks = [mod.register_forward_pre_hook(self._pre_hook) for mod in self._owned]
 
     def _compute_on_stored(self, mod, meta):
-        """Give ``mod`` a forward that runs the operators on stored weights, where it is a module they replace."""
+        """The forward for ``mod`` that runs the operators on stored weights, or None if it is no module they replace."""
         torch = _torch()
         from . import ops
         if type(mod).forward is torch.nn.Linear.forward and meta.kind in QUANTIZED_KINDS:
             self._stored[mod] = None
             encode = {w: k for k, ws in ops.PAIRS.items() for w in ws}.get(meta.kind) if self.quantized == "activations" else None
-            names = {torch.bfloat16: "bf16", torch.float16: "f16"}
-
-            def forward(x):
-                dtype = names.get(x.dtype)      # another type is refused by the operator
-                if encode is not None and dtype is not None:
-                    x = ops.quantize_activation(x, encode)
-                return ops.linear(x, self._stored[mod], bias=mod.bias, out_dtype=dtype)
-            mod.forward = forward
-        elif type(mod).forward is torch.nn.RMSNorm.forward and len(mod.normalized_shape) == 1:
-            def forward(x):
-                # a norm without an eps computes in fp32 for 16-bit rows too, and takes fp32's
-                return ops.rms_norm(x, mod.weight, eps=torch.finfo(torch.float32).eps if mod.eps is None else mod.eps)
-            mod.forward = forward
+            return _StoredLinear(self, mod, encode)
+        if type(mod).forward is torch.nn.RMSNorm.forward and len(mod.normalized_shape) == 1:
+            return _OperatorNorm(self, mod)
+        return None
 
     def _pre_hook(self, mod, args):
         self.materialize(mod)
@@ -756,7 +796,7 @@ class LazyModuleLoader:
                 key = self.refs[(mod, "weight")].key
                 q = self.sd.load_quantized([key], copy=True)[key]
                 self._stored[mod] = q
-                nbytes += sum(t.numel() * t.element_size() for t in (q.data, q.scale, q.scale2) if t is not None)
+                nbytes += _stored_bytes(q)
             self.stats["materialized"] += len(todo) + stored
             self._resident[mod] = self._resident.get(mod, 0) + nbytes
             self.resident_bytes += nbytes
@@ -790,7 +830,20 @@ class LazyModuleLoader:
             self.evict(mod)
 
     def detach(self):
-        """Remove the hooks (parameters keep their current state)."""
+        """Remove the hooks, and the forwards that compute on stored weights.  Parameters keep their current state; stored
+        weights are let go, so those modules' weight parameters are the meta tensors they were."""
         for h in self._hooks:
             h.remove()
         self._hooks = []
+        for mod, fwd in self._forwards.items():
+            fwd.loader = None          # should a wrapper have kept it
+            if mod.__dict__.get("forward") is fwd:
+                del mod.forward
+        self._forwards = {}
+        for mod, q in self._stored.items():
+            if q is not None:
+                self._resident[mod] -= _stored_bytes(q)
+                self.resident_bytes -= _stored_bytes(q)
+                if not self._resident[mod]:
+                    del self._resident[mod]
+        self._stored = {}

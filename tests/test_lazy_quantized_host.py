@@ -58,3 +58,121 @@ def test_norm_uses_the_modules_eps(dtype, eps):
     # both are rounded to x's type; torch's 32-bit form takes a handful of roundings of its own
     step = torch.finfo(dtype).eps / 2
     assert ((got - want).abs() <= want.abs() * (2 * step + 16 * 2.0 ** -24) + torch.finfo(dtype).smallest_normal * step * 2).all()
+
+
+def _checkpoint(seed, bias=True):
+    sd = _Memory(weight=ref.random_weight(st, "FP8_TENSOR", 24, 64, seed))
+    if bias:
+        sd["bias"] = _x(24, seed=seed + 100)
+    return sd
+
+
+def _linear(bias=True):
+    return torch.nn.Linear(64, 24, bias=bias, device="meta", dtype=torch.bfloat16)
+
+
+def _decoded(sd, x):
+    return torch.nn.functional.linear(x, ref.weight_value(sd["weight"]).to(torch.bfloat16), sd.get("bias"))
+
+
+def test_another_checkpoint_after_detach():
+    """A module that another checkpoint is attached to computes with that checkpoint's weight, whichever loader it had before."""
+    a, b = _checkpoint(1), _checkpoint(2)
+    lin, x = _linear(), _x(5, 64, seed=3)
+    for evict in (False, True):
+        loader = st.LazyModuleLoader(lin, a, quantized="weights")
+        want = ops.linear(x, a["weight"], bias=a["bias"], out_dtype="bf16")
+        assert torch.equal(lin(x), want)
+        if evict:
+            loader.evict_all()
+        loader.detach()
+        assert "forward" not in lin.__dict__
+        plain = st.LazyModuleLoader(lin, b)
+        assert torch.equal(lin(x), _decoded(b, x))
+        plain.detach()
+        assert torch.equal(lin(x), _decoded(b, x))
+
+
+def test_detach_leaves_a_meta_weight_and_counts_it_out():
+    a = _checkpoint(1)
+    lin, x = _linear(), _x(5, 64, seed=3)
+    loader = st.LazyModuleLoader(lin, a, quantized="weights")
+    lin(x)
+    stored = a["weight"].data.numel() + 4
+    assert loader.resident_bytes == stored + 48
+    loader.detach()
+    assert lin.weight.is_meta and not lin.bias.is_meta and loader.resident_bytes == 48
+    loader.materialize(lin)                      # by hand: decoded, as without `quantized`
+    assert torch.equal(lin(x), _decoded(a, x)) and loader.resident_bytes == 48 + 2 * 24 * 64
+    lin.weight = torch.nn.Parameter(torch.zeros(24, 64, dtype=torch.bfloat16), requires_grad=False)
+    assert torch.equal(lin(x), a["bias"].expand(5, 24))
+
+
+def test_a_weight_assigned_while_attached_is_used():
+    a = _checkpoint(1)
+    lin, x = _linear(), _x(5, 64, seed=3)
+    loader = st.LazyModuleLoader(lin, a, quantized="weights")
+    lin(x)
+    lin.weight = torch.nn.Parameter(torch.zeros(24, 64, dtype=torch.bfloat16), requires_grad=False)
+    assert torch.equal(lin(x), a["bias"].expand(5, 24))
+    loader.detach()
+
+
+def test_a_module_takes_one_quantized_loader_at_a_time():
+    a, b = _checkpoint(1), _checkpoint(2)
+    lin, x = _linear(), _x(5, 64, seed=3)
+    loader = st.LazyModuleLoader(lin, a, quantized="weights")
+    want = lin(x)
+    for mode in (None, "weights", "activations"):
+        with pytest.raises(ValueError, match="detach"):
+            st.LazyModuleLoader(lin, b, quantized=mode)
+    assert torch.equal(lin(x), want)
+    loader.detach()
+    st.LazyModuleLoader(lin, b, quantized="weights")
+    assert torch.equal(lin(x), ops.linear(x, b["weight"], bias=b["bias"], out_dtype="bf16"))
+
+
+def test_a_copy_of_a_module_is_its_own():
+    """copy.deepcopy copies the loader along: copy and original stay apart, and neither outlives its detach."""
+    import copy
+    a = _checkpoint(1)
+    root = torch.nn.Sequential(_linear())
+    loader = st.LazyModuleLoader(root, _Memory({"0." + k: v for k, v in a.items()}), quantized="weights")
+    x = _x(5, 64, seed=3)
+    want = root(x)
+    twin = copy.deepcopy(root)
+    twin[0].bias.data.zero_()
+    assert torch.equal(root(x), want)
+    assert torch.equal(twin(x), ops.linear(x, a["weight"], out_dtype="bf16"))
+    loader.detach()
+    root[0].weight = torch.nn.Parameter(torch.zeros(24, 64, dtype=torch.bfloat16), requires_grad=False)
+    assert torch.equal(root(x), a["bias"].expand(5, 24)) and torch.equal(twin(x), ops.linear(x, a["weight"], out_dtype="bf16"))
+
+
+def test_a_forward_kept_by_a_wrapper_is_the_modules_own_after_detach():
+    a = _checkpoint(1)
+    lin, x = _linear(), _x(5, 64, seed=3)
+    loader = st.LazyModuleLoader(lin, a, quantized="weights")
+    inner = lin.forward
+    lin.forward = lambda t: 2 * inner(t)
+    assert torch.equal(lin(x), 2 * ops.linear(x, a["weight"], bias=a["bias"], out_dtype="bf16"))
+    loader.detach()
+    loader.materialize(lin)
+    assert torch.equal(lin(x), 2 * _decoded(a, x))
+
+
+def test_a_failed_attach_replaces_no_forward():
+    sd = _Memory({"0.weight": ref.random_weight(st, "FP8_TENSOR", 24, 64, 1), "1.weight": ref.random_weight(st, "FP8_TENSOR", 24, 32, 1)})
+    root = torch.nn.Sequential(_linear(bias=False), torch.nn.Linear(24, 8, bias=False, device="meta"))
+    with pytest.raises(ValueError, match="checkpoint shape"):
+        st.LazyModuleLoader(root, sd, quantized="weights")
+    assert "forward" not in root[0].__dict__
+
+
+def test_norms_forward_goes_with_its_loader():
+    weight = torch.full((64,), 2.0, dtype=torch.bfloat16)
+    norm, x = torch.nn.RMSNorm(64, eps=1e-6, device="meta", dtype=torch.bfloat16), _x(3, 64)
+    loader = st.LazyModuleLoader(norm, _Memory(weight=weight), quantized="weights")
+    assert "forward" in norm.__dict__ and torch.equal(norm(x), ops.rms_norm(x, weight))
+    loader.detach()
+    assert "forward" not in norm.__dict__ and not norm.weight.is_meta
