@@ -715,8 +715,8 @@ class LazyModuleLoader:
     weight the checkpoint holds quantised through :func:`linear` (its weight parameter stays a meta tensor; the
     stored weight, a half or a quarter of the decoded one, is what loads and counts against the bound) and every ``nn.RMSNorm``
     over one dimension through :func:`rms_norm`; "activations" also encodes those linears' inputs in the 8-bit kind that goes
-    with the weight (NVFP4 weights keep dense inputs).  Inference only, for bf16 and fp16 inputs; subclasses with a
-    forward of their own are left alone.  A module takes one such loader at a time; :meth:`detach` gives it its own
+    with the weight (NVFP4 weights keep dense inputs).  Inference only, for bf16 and fp16 inputs; subclasses and
+    modules with a forward of their own are left alone.  A module takes one such loader at a time; :meth:`detach` gives it its own
     forward back, and its stored weight up."""
 
     def __init__(self, module, state_dict, max_resident_bytes: int | None = None, strict: bool = True,
@@ -766,6 +766,8 @@ class LazyModuleLoader:
         """The forward for ``mod`` that runs the operators on stored weights, or None if it is no module they replace."""
         torch = _torch()
         from . import ops
+        if "forward" in mod.__dict__:      # an adapter's
+            return None
         if type(mod).forward is torch.nn.Linear.forward and meta.kind in QUANTIZED_KINDS:
             self._stored[mod] = None
             encode = {w: k for k, ws in ops.PAIRS.items() for w in ws}.get(meta.kind) if self.quantized == "activations" else None

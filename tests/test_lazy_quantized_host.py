@@ -176,3 +176,19 @@ def test_norms_forward_goes_with_its_loader():
     assert "forward" in norm.__dict__ and torch.equal(norm(x), ops.rms_norm(x, weight))
     loader.detach()
     assert "forward" not in norm.__dict__ and not norm.weight.is_meta
+
+
+def test_a_forward_of_the_instance_is_left_alone():
+    """An adapter's forward, set on the module itself, runs as before, on the decoded weight."""
+    a = _checkpoint(1)
+    lin, x = _linear(), _x(5, 64, seed=3)
+    lin.forward = lambda t: 3 * torch.nn.functional.linear(t, lin.weight, lin.bias)
+    patched = lin.forward
+    loader = st.LazyModuleLoader(lin, a, quantized="weights")
+    assert lin.forward is patched and torch.equal(lin(x), 3 * _decoded(a, x))
+    loader.detach()
+    assert lin.forward is patched
+    norm = torch.nn.RMSNorm(64, eps=1e-6, device="meta", dtype=torch.bfloat16)
+    norm.forward = lambda t: t
+    st.LazyModuleLoader(norm, _Memory(weight=torch.ones(64, dtype=torch.bfloat16)), quantized="weights")
+    assert norm(x) is x
