@@ -678,8 +678,8 @@ class _StoredLinear(_Forward):
         super().__init__(loader, mod)
         self.encode = encode      # the inputs' 8-bit kind, or None
 
-    def __call__(self, x):
-        mod = self.mod
+    def __call__(self, input):      # named as nn.Linear.forward names it
+        x, mod = input, self.mod
         if self.loader is None or not mod.weight.is_meta:      # detached, or a weight that was assigned since
             return type(mod).forward(mod, x)
         from . import ops

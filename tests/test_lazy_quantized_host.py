@@ -192,3 +192,14 @@ def test_a_forward_of_the_instance_is_left_alone():
     norm.forward = lambda t: t
     st.LazyModuleLoader(norm, _Memory(weight=torch.ones(64, dtype=torch.bfloat16)), quantized="weights")
     assert norm(x) is x
+
+
+def test_inputs_by_name():
+    """nn.Linear.forward names its argument input, nn.RMSNorm.forward x."""
+    a = _checkpoint(1)
+    lin, x = _linear(), _x(5, 64, seed=3)
+    st.LazyModuleLoader(lin, a, quantized="weights")
+    assert torch.equal(lin(input=x), lin(x))
+    norm = torch.nn.RMSNorm(64, eps=1e-6, device="meta", dtype=torch.bfloat16)
+    st.LazyModuleLoader(norm, _Memory(weight=torch.ones(64, dtype=torch.bfloat16)), quantized="weights")
+    assert torch.equal(norm(x=x), norm(x))
