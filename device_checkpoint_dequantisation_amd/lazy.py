@@ -787,6 +787,10 @@ class LazyModuleLoader:
         stored = mod in self._stored and self._stored[mod] is None
         if todo or stored:
             nbytes = 0
+            q = None
+            if stored:      # both loads before either result is kept: one that fails leaves the module as it was
+                key = self.refs[(mod, "weight")].key
+                q = self.sd.load_quantized([key], copy=True)[key]
             if todo:
                 keys = [self.refs[(mod, p)].key for p in todo]
                 got = self.sd.load(keys)
@@ -795,8 +799,6 @@ class LazyModuleLoader:
                     mod._parameters[p] = torch.nn.Parameter(t, requires_grad=False)
                     nbytes += t.numel() * t.element_size()
             if stored:
-                key = self.refs[(mod, "weight")].key
-                q = self.sd.load_quantized([key], copy=True)[key]
                 self._stored[mod] = q
                 nbytes += _stored_bytes(q)
             self.stats["materialized"] += len(todo) + stored

@@ -203,3 +203,22 @@ def test_inputs_by_name():
     norm = torch.nn.RMSNorm(64, eps=1e-6, device="meta", dtype=torch.bfloat16)
     st.LazyModuleLoader(norm, _Memory(weight=torch.ones(64, dtype=torch.bfloat16)), quantized="weights")
     assert torch.equal(norm(x=x), norm(x))
+
+
+def test_a_failed_load_counts_nothing():
+    """A stored weight that cannot be read leaves its module as it was, bias and byte counts included."""
+    a = _checkpoint(1)
+    lin, x = _linear(), _x(5, 64, seed=3)
+    loader = st.LazyModuleLoader(lin, a, quantized="weights")
+
+    def broken(names, stream=None, copy=False):
+        raise OSError("short read")
+    a.load_quantized = broken
+    with pytest.raises(OSError, match="short read"):
+        lin(x)
+    assert lin.bias.is_meta and loader.resident_bytes == 0
+    del a.load_quantized
+    assert torch.equal(lin(x), ops.linear(x, a["weight"], bias=a["bias"], out_dtype="bf16"))
+    assert loader.resident_bytes == a["weight"].data.numel() + 4 + 48
+    loader.evict_all()
+    assert loader.resident_bytes == 0 and lin.bias.is_meta
