@@ -82,7 +82,9 @@ __device__ __forceinline__ Raw<E> load8(const uint8_t* row, uint32_t col, uint32
 __device__ __forceinline__ bool finite(double v) { return __builtin_fabs(v) <= 1.7976931348623157e308; }
 __device__ __forceinline__ double silu64(double g) { return g / (1.0 + exp(-g)); }
 // The same to 5 * 2^-24 of itself: exp(-g) = 2^t (1 + r ln 2) with t + r = -g log2(e), t the rounded product and r the rest, and the
-// hardware's 2^t and 1 / x (an ulp each).  A value too small for the hardware's 2^t to be finite is left to silu64 by its caller.
+// hardware's 2^t and 1 / x (an ulp each).  For g from kSiluLeast up; below, 2^t passes fp32's range (1 / x becomes subnormal, then 0,
+// with a result that may be finite or NaN) and the caller takes silu64.
+constexpr float kSiluLeast = -87.0f;
 __device__ __forceinline__ float silu32(float g) {
     const float t = g * -1.44269504f;                                  // the nearest fp32 to log2(e), and what it lacks
     const float r = __builtin_fmaf(g, -1.44269504f, -t) + g * -1.92596299e-8f;
@@ -216,15 +218,15 @@ __device__ __forceinline__ void encode_exact(const Args& a, uint64_t row, uint32
     store_scale<KIND>(a, row, col, s.bits);
 }
 
-// The same for values known in fp64 (wide(v)), and to a few 2^-24 in fp32 (v).
+// The same for values known in fp64 (wide(v)), and to a few 2^-24 in fp32 (v) unless this lane is `odd`.
 template <uint32_t KIND, bool VEC, class Wide>
-__device__ __forceinline__ void encode_group(const Args& a, uint64_t row, uint32_t col, const float* v, Wide wide) {
+__device__ __forceinline__ void encode_group(const Args& a, uint64_t row, uint32_t col, const float* v, bool odd, Wide wide) {
     constexpr int LANES = KIND == ST_X_MXFP8 ? 4 : 16;
     uint32_t lo, hi, bits;
     bool again = true;
     if constexpr (KIND == ST_X_MXFP8) {
         float amax = 0.0f;
-        bool odd = false;       // something that fp32 does not settle
+        // odd: something that fp32 does not settle
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const float m = __builtin_fabsf(v[i]);
@@ -274,9 +276,13 @@ __global__ __launch_bounds__(kThreads) void encode_groups(Args a, uint32_t rows_
         float v[8];
         if constexpr (GATE) {
             const Raw<E> g = load8<E, VEC>(a.b + row * a.b_pitch * kSize<E>, col, a.d);
+            float least = 0.0f;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = silu32(g.at(k)) * x.at(k);
-            encode_group<KIND, VEC>(a, row, col, v, [&](double* w) {
+            for (int k = 0; k < 8; ++k) {
+                least = __builtin_fminf(least, g.at(k));
+                v[k] = silu32(g.at(k)) * x.at(k);
+            }
+            encode_group<KIND, VEC>(a, row, col, v, least < kSiluLeast, [&](double* w) {
 #pragma unroll
                 for (int k = 0; k < 8; ++k) w[k] = silu64(double(g.at(k))) * double(x.at(k));
             });
@@ -470,7 +476,7 @@ __global__ __launch_bounds__(TPR < int(kThreads) ? kThreads : TPR) void rows(Arg
             for (int i = 0; i < 8; ++i) v[i] = h_of(c, i) * s * w[i];
             store_h(c, col);
             // lanes of a row that is not there take part in the reductions and store nothing
-            encode_group<KIND, VEC>(a, row, live ? col : (d + 7) / 8 * 8, v, [&](double* y) {
+            encode_group<KIND, VEC>(a, row, live ? col : (d + 7) / 8 * 8, v, false, [&](double* y) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) y[i] = double(h_of(c, i)) * inv * double(w[i]);
             });
