@@ -10,9 +10,9 @@
 //  * a gate or a norm: v, amax and the quotient are kept in fp64 (the sum of squares too).  For MX, whose scale is a power of two, v
 //    in fp32, good to 2^-21, decides unless it comes within 2^-20 of a middle or amax that near to a power of two's edge;
 //    then the wavefront does its chunk again in fp64 (about one in 100).
-// fp64 quotients within 2^-40 of a middle are taken as the middle itself: v and s have at most 24 bits each and a middle has
-// 5, so an inexact quotient of two such numbers differs from it by more than 2^-30, and what is nearer is the error of
-// multiplying by 1 / s.
+// A fp64 quotient is rounded correctly: a middle has 5 bits, s 24 and v 53, so a quotient that is not a middle is not rounded to one.
+// (A gate of 31 makes x * silu(gate) differ from x * gate by 2^-45 of itself: such values do lie that near to middles.)  A norm's own
+// fp64 roundings come to a few 2^-53: its quotients within 2^-49 of a middle count as the middle.
 //
 // Both are bound by memory: every input is read once and stays in registers (chunks of 8 elements per lane, 16-byte
 // loads) while the row's sums and maxima are taken; groups of 128 and 32 columns are 16 and 4 lanes.  Measured on MI355X: norm of
@@ -99,6 +99,7 @@ template <uint32_t KIND>
 struct Scale {
     uint32_t bits;    // fp32 bits, or the E8M0 code
     double inv;
+    __device__ __forceinline__ double value() const { return KIND == ST_X_MXFP8 ? 1.0 / inv : double(as_f32(bits)); }
     __device__ __forceinline__ explicit Scale(double amax) {
         if constexpr (KIND == ST_X_MXFP8) {
             // 448 = 1.75 * 2^8: with amax = f * 2^e, f in [1, 2), the power is e - 8 up to f = 1.75 and e - 7 above
@@ -120,9 +121,13 @@ struct Scale {
 
 // v / s as an fp32 number that rounds to e4m3 as v / s itself does: truncated, with the lowest bit set where
 // anything was cut off (a second rounding, to fewer bits, then sees on which side of a middle the value lies).
-__device__ __forceinline__ float quotient(double v, double inv) {
-    double t = v * inv;
-    t = __builtin_bit_cast(double, (__builtin_bit_cast(uint64_t, t) + 0x800u) & ~uint64_t(0xFFF));
+// NORM: v may be off by a few 2^-53 of itself.
+template <uint32_t KIND, bool NORM>
+__device__ __forceinline__ float quotient(double v, const Scale<KIND>& s) {
+    double t = v * s.inv;
+    // the correctly rounded quotient (a power of two's product is exact)
+    if constexpr (KIND != ST_X_MXFP8) t = __builtin_fma(__builtin_fma(-t, s.value(), v), s.inv, t);
+    if constexpr (NORM) t = __builtin_bit_cast(double, (__builtin_bit_cast(uint64_t, t) + 0x8u) & ~uint64_t(0xF));
     const float f = float(t);
     const double back = double(f);
     uint32_t u = as_u32(f);
@@ -219,7 +224,7 @@ __device__ __forceinline__ void encode_exact(const Args& a, uint64_t row, uint32
 }
 
 // The same for values known in fp64 (wide(v)), and to a few 2^-24 in fp32 (v) unless this lane is `odd`.
-template <uint32_t KIND, bool VEC, class Wide>
+template <uint32_t KIND, bool VEC, bool NORM, class Wide>
 __device__ __forceinline__ void encode_group(const Args& a, uint64_t row, uint32_t col, const float* v, bool odd, Wide wide) {
     constexpr int LANES = KIND == ST_X_MXFP8 ? 4 : 16;
     uint32_t lo, hi, bits;
@@ -255,7 +260,7 @@ __device__ __forceinline__ void encode_group(const Args& a, uint64_t row, uint32
         const Scale<KIND> s(max_over<LANES>(amax));
         float q[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) q[i] = quotient(w[i], s.inv);
+        for (int i = 0; i < 8; ++i) q[i] = quotient<KIND, NORM>(w[i], s);
         lo = pack4(q[0], q[1], q[2], q[3]);
         hi = pack4(q[4], q[5], q[6], q[7]);
         bits = s.bits;
@@ -282,7 +287,7 @@ __global__ __launch_bounds__(kThreads) void encode_groups(Args a, uint32_t rows_
                 least = __builtin_fminf(least, g.at(k));
                 v[k] = silu32(g.at(k)) * x.at(k);
             }
-            encode_group<KIND, VEC>(a, row, col, v, least < kSiluLeast, [&](double* w) {
+            encode_group<KIND, VEC, false>(a, row, col, v, least < kSiluLeast, [&](double* w) {
 #pragma unroll
                 for (int k = 0; k < 8; ++k) w[k] = silu64(double(g.at(k))) * double(x.at(k));
             });
@@ -462,7 +467,7 @@ __global__ __launch_bounds__(TPR < int(kThreads) ? kThreads : TPR) void rows(Arg
             float q[8];
             values(c, col, v);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) q[i] = quotient(v[i], s.inv);
+            for (int i = 0; i < 8; ++i) q[i] = quotient<KIND, OP == kNorm>(v[i], s);
             store_h(c, col);
             store_codes<VEC>(a.out + row * d, col, dd, pack4(q[0], q[1], q[2], q[3]), pack4(q[4], q[5], q[6], q[7]));
         });
@@ -476,7 +481,7 @@ __global__ __launch_bounds__(TPR < int(kThreads) ? kThreads : TPR) void rows(Arg
             for (int i = 0; i < 8; ++i) v[i] = h_of(c, i) * s * w[i];
             store_h(c, col);
             // lanes of a row that is not there take part in the reductions and store nothing
-            encode_group<KIND, VEC>(a, row, live ? col : (d + 7) / 8 * 8, v, false, [&](double* y) {
+            encode_group<KIND, VEC, true>(a, row, live ? col : (d + 7) / 8 * 8, v, false, [&](double* y) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) y[i] = double(h_of(c, i)) * inv * double(w[i]);
             });

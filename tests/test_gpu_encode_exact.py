@@ -30,3 +30,31 @@ def test_gates_far_below_zero(kind, dt, far, near):
     g[torch.arange(m), at], x[torch.arange(m), at] = gates, -far
     g, x = g.to(ref.DT[dt]), x.to(ref.DT[dt])
     _check_codes(st.quantize_activation(x.to(DEV), kind, gate=g.to(DEV)), x.double() * _silu(g))
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("spread", [1.0, 20.0])
+def test_gated_codes_equal_the_definition(kind, dt, spread):
+    g = torch.Generator().manual_seed(2)
+    x = (torch.randn(96, 4096, generator=g) * 30).to(ref.DT[dt])
+    gate = (torch.randn(96, 4096, generator=g) * spread).to(ref.DT[dt])
+    _check_codes(st.quantize_activation(x.to(DEV), kind, gate=gate.to(DEV)), x.double() * _silu(gate))
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_gates_that_almost_pass_x(kind, dt):
+    """x / s at every middle between two codes and gates from 20 to 40: silu(gate) lies below the gate by 2^-24 to 2^-53 of
+    itself, and so does the value below the middle."""
+    codes = torch.arange(127, dtype=torch.uint8).view(torch.float8_e4m3fn).double()
+    mid = torch.cat([(codes[1:] + codes[:-1]) / 2, torch.tensor([448.0, 0.0])])
+    gates = torch.tensor([20.0, 24.0, 26.0, 28.0, 30.0, 31.0, 32.0, 34.0, 36.0, 37.0, 40.0, 64.0])
+    x = torch.zeros(gates.numel(), 128 * 32)
+    g = gates[:, None].expand_as(x).clone()
+    x.view(-1, 128, 32)[:, :, 7] = mid.float()           # a group of 32 or 128 around each, its largest value at the end
+    x.view(-1, 128, 32)[:, :, 31] = 448.0
+    # an fp32 scale is the gate itself (448 silu(gate) / 448, rounded), a power of two at or above it
+    x, g = x.to(ref.DT[dt]), g.to(ref.DT[dt])
+    assert (x.double().view(-1, 128, 32)[:, :, 7] == mid).all()
+    _check_codes(st.quantize_activation(x.to(DEV), kind, gate=g.to(DEV)), x.double() * _silu(g))
