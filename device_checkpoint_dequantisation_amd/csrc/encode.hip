@@ -7,7 +7,7 @@
 // the quotient lies on is decided exactly:
 //  * encode without a gate: v, and so amax and s, are exact in fp32.  The fp32 quotient names the middle that is nearest, and the
 //    sign of fma(-middle, s, v), which is exact, says on which side of it v / s lies.
-//  * a gate or a norm: v, amax and the quotient are kept in fp64 (the sum of squares too).  For MX, whose scale is a power of two, v
+//  * a gate or a norm: v, amax and the quotient are kept in fp64 (x + residual and the sum of squares too).  For MX, whose scale is a power of two, v
 //    in fp32, good to 2^-21, decides unless it comes within 2^-20 of a middle or amax that near to a power of two's edge;
 //    then the wavefront does its chunk again in fp64 (about one in 100).
 // A fp64 quotient is rounded correctly: a middle has 5 bits, s 24 and v 53, so a quotient that is not a middle is not rounded to one.
@@ -348,10 +348,14 @@ __global__ __launch_bounds__(TPR < int(kThreads) ? kThreads : TPR) void rows(Arg
         }
         return v;
     };
-    // h = x + residual in fp32
+    // h = x + residual: rounded to fp32 (from there h_out's 16-bit types round as they would from the sum itself), and as it is
     auto h_of = [&](int c, int i) {
         if constexpr (B) return rx[c].at(i) + rb[c].at(i);
         else return rx[c].at(i);
+    };
+    auto h64 = [&](int c, int i) {
+        if constexpr (B) return double(rx[c].at(i)) + double(rb[c].at(i));
+        else return double(rx[c].at(i));
     };
     double inv = 0.0;
     if constexpr (OP == kNorm) {
@@ -359,7 +363,7 @@ __global__ __launch_bounds__(TPR < int(kThreads) ? kThreads : TPR) void rows(Arg
         each([&](int c, uint32_t) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const double h = double(h_of(c, i));
+                const double h = h64(c, i);
                 ss = __builtin_fma(h, h, ss);
             }
         });
@@ -390,7 +394,7 @@ __global__ __launch_bounds__(TPR < int(kThreads) ? kThreads : TPR) void rows(Arg
             float w[8];
             weight(col, w);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = double(h_of(c, i)) * inv * double(w[i]);
+            for (int i = 0; i < 8; ++i) v[i] = h64(c, i) * inv * double(w[i]);
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -421,7 +425,7 @@ __global__ __launch_bounds__(TPR < int(kThreads) ? kThreads : TPR) void rows(Arg
             weight(col, w);
             // in fp64: the factor of a row of the smallest values may lie beyond fp32
 #pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = float(double(h_of(c, i)) * inv * double(w[i]));
+            for (int i = 0; i < 8; ++i) y[i] = float(h64(c, i) * inv * double(w[i]));
             store_h(c, col);
             if constexpr (VEC) {
                 if (col < dd) {
@@ -452,9 +456,12 @@ __global__ __launch_bounds__(TPR < int(kThreads) ? kThreads : TPR) void rows(Arg
                 store_codes<VEC>(a.out + row * d, col, dd, lo, hi);
             });
         } else {
+        // up to four chunks of fp64 values stay in registers between the passes (8192 x 5120 with residual: 81 us, 99 computed twice)
+        constexpr bool KEEP = CH != 0 && CH <= 4;
+        double kept[KEEP ? CH : 1][8];
         double amax = 0.0;
         each([&](int c, uint32_t col) {
-            double v[8];
+            double* v = kept[KEEP ? c : 0];
             values(c, col, v);
 #pragma unroll
             for (int i = 0; i < 8; ++i) amax = __builtin_fmax(amax, finite(v[i]) ? __builtin_fabs(v[i]) : 0.0);
@@ -463,9 +470,9 @@ __global__ __launch_bounds__(TPR < int(kThreads) ? kThreads : TPR) void rows(Arg
         const Scale<KIND> s(amax);
         if (t == 0 && live) reinterpret_cast<uint32_t*>(a.scale)[row] = s.bits;
         each([&](int c, uint32_t col) {
-            double v[8];
+            double* v = kept[KEEP ? c : 0];
             float q[8];
-            values(c, col, v);
+            if constexpr (!KEEP) values(c, col, v);
 #pragma unroll
             for (int i = 0; i < 8; ++i) q[i] = quotient<KIND, OP == kNorm>(v[i], s);
             store_h(c, col);
@@ -483,7 +490,7 @@ __global__ __launch_bounds__(TPR < int(kThreads) ? kThreads : TPR) void rows(Arg
             // lanes of a row that is not there take part in the reductions and store nothing
             encode_group<KIND, VEC, true>(a, row, live ? col : (d + 7) / 8 * 8, v, false, [&](double* y) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) y[i] = double(h_of(c, i)) * inv * double(w[i]);
+                for (int i = 0; i < 8; ++i) y[i] = h64(c, i) * inv * double(w[i]);
             });
         });
     }

@@ -58,3 +58,47 @@ def test_gates_that_almost_pass_x(kind, dt):
     x, g = x.to(ref.DT[dt]), g.to(ref.DT[dt])
     assert (x.double().view(-1, 128, 32)[:, :, 7] == mid).all()
     _check_codes(st.quantize_activation(x.to(DEV), kind, gate=g.to(DEV)), x.double() * _silu(g))
+
+
+# ------------------------------------------------------------------------------------------------ norm
+
+def _norm_rows(m, d, dt, seed):
+    """Rows and a residual whose sums mostly do not fit fp32's 24 bits."""
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(m, d, generator=g)
+    r = torch.randn(m, d, generator=g) * 2.0 ** (-torch.randint(6, 20, (m, d), generator=g).float())
+    return x.to(ref.DT[dt]), r.to(ref.DT[dt]), 1 + 0.1 * torch.randn(d, generator=g)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("m,d", [(40, 512), (20, 1000), (9, 5120), (3, 33024), (5, 333)])
+def test_norm_of_the_unrounded_sum(dt, m, d):
+    """An fp32 result is the 64-bit one rounded once: half a step, and 2^-40 for the 64-bit sum in another order."""
+    x, r, w = _norm_rows(m, d, dt, d)
+    want, h = ref.rms_norm(x, w, 1e-6, r)
+    y, gh = st.rms_norm(x.to(DEV), w.to(DEV), eps=1e-6, residual=r.to(DEV), out_dtype="f32")
+    assert ((y.cpu().double() - want).abs() <= want.abs() * (2.0 ** -24 + 2.0 ** -40) + 2.0 ** -150).all()
+    assert torch.equal(gh.cpu(), h.to(ref.DT[dt]))
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("m,d", [(96, 4096), (40, 5120), (7, 33024)])
+def test_norm_codes_equal_the_definition(kind, dt, m, d):
+    x, r, w = _norm_rows(m, d, dt, d + 1)
+    want, _ = ref.rms_norm(x, w, 1e-6, r)
+    _check_codes(st.rms_norm(x.to(DEV), w.to(DEV), eps=1e-6, residual=r.to(DEV), quantize=kind)[0], want)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [128, 544])
+def test_norm_of_sums_beyond_fp32(dt, d):
+    """x + residual past fp32's largest number: h is infinite in x's type, y is not."""
+    x = (3e38 * torch.where(torch.arange(d) % 3 == 0, -1.0, 1.0)).repeat(3, 1).to(ref.DT[dt])
+    want, _ = ref.rms_norm(x, None, 1e-6, x)
+    y, h = st.rms_norm(x.to(DEV), eps=1e-6, residual=x.to(DEV), out_dtype="f32")
+    assert ((y.cpu().double() - want).abs() <= want.abs() * 2.0 ** -23).all() and h.isinf().all()
+    for kind in KINDS:
+        q, h = st.rms_norm(x.to(DEV), eps=1e-6, residual=x.to(DEV), quantize=kind)
+        _check_codes(q, want)
+        assert h.isinf().all() and ((_bits(q.data) & 127) != 127).all()
