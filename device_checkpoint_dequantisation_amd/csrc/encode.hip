@@ -498,11 +498,23 @@ __global__ __launch_bounds__(TPR < int(kThreads) ? kThreads : TPR) void rows(Arg
 
 // ------------------------------------------------------------------------- launches
 
+constexpr uint32_t kMostBlocks = 1u << 22;     // of up to 512 threads
+
 template <int OP, uint32_t E, uint32_t KIND, bool B>
 void launch_rows(const Args& a, bool vec, hipStream_t s) {
     const uint32_t chunks = (a.d + 7) / 8;
     auto go = [&](auto kernel, uint32_t threads, uint32_t per_block) {
-        hipLaunchKernelGGL(kernel, dim3(uint32_t((a.m + per_block - 1) / per_block)), dim3(threads), 0, s, a);
+        // A grid holds fewer than 2^32 threads: more rows are launched in parts.  (A second grid dimension costs each call 1%.)
+        Args part = a;
+        for (uint64_t done = 0, most = uint64_t(kMostBlocks) * per_block; done < a.m; done += most) {
+            part.m = a.m - done < most ? a.m - done : most;
+            hipLaunchKernelGGL(kernel, dim3(uint32_t((part.m + per_block - 1) / per_block)), dim3(threads), 0, s, part);
+            part.x += most * a.x_pitch * kSize<E>;
+            if (B) part.b += most * a.b_pitch * kSize<E>;
+            if (a.h) part.h += most * a.d * kSize<E>;
+            part.out += most * a.d * (KIND != 0 ? 1 : a.out_type == ST_OUT_F32 ? 4 : 2);
+            if (KIND != 0) part.scale += most * (KIND == ST_X_FP8_ROW ? 4 : KIND == ST_X_MXFP8 ? a.d / 32 : uint64_t(a.d + 127) / 128 * 4);
+        }
     };
     // rows that are not whole aligned chunks, or do not fit the registers, are read again in each pass
     if (!vec || chunks > 4096 || (E == ST_OUT_F32 && chunks > 2048)) go(rows<OP, E, KIND, false, 256, 0, B>, 256, 1);

@@ -102,3 +102,34 @@ def test_norm_of_sums_beyond_fp32(dt, d):
         q, h = st.rms_norm(x.to(DEV), eps=1e-6, residual=x.to(DEV), quantize=kind)
         _check_codes(q, want)
         assert h.isinf().all() and ((_bits(q.data) & 127) != 127).all()
+
+
+# ------------------------------------------------------------------------------------------------ more rows than one launch takes
+
+@pytest.mark.parametrize("d", [7, 32])
+def test_more_rows_than_one_launch_takes(d):
+    """Past 2^32 threads and 2^22 workgroups, of one row (odd width) or of four: every form of the output, next to the parts'
+    ends against the same rows by themselves."""
+    m = (2 ** 24 if d == 32 else 2 ** 22) * 2 + 3
+    x = torch.randn(m, d, generator=torch.Generator(DEV).manual_seed(7), device=DEV).to(torch.bfloat16)
+    r = x.flip(0)
+    w = torch.rand(d, device=DEV)
+    parts = [slice(max(0, a - 300), a + 300) for a in range(0, m, 2 ** 22)] + [slice(m - 300, m)]
+    if d == 7:
+        grid = 2 ** 24 + 3        # past 2^32 threads in workgroups of 256
+        big = torch.randn(grid, 1, generator=torch.Generator(DEV).manual_seed(8), device=DEV).to(torch.bfloat16)
+        q = st.quantize_activation(big, "FP8_ROW")
+        assert torch.equal(q.data.float().abs(), torch.where(big == 0, 0.0, 448.0)) and torch.equal(q.scale, torch.where(big == 0, 1.0, big.double().abs() / 448)[:, 0].float())
+    for kind in (None, "FP8_ROW", "FP8_GROUP128") + (("MXFP8",) if d == 32 else ()):
+        print(f"many rows {kind} {d}", flush=True)
+        y, h = st.rms_norm(x, w, eps=1e-6, residual=r, quantize=kind)
+        q = None if kind is None else st.quantize_activation(x, kind)
+        assert torch.equal(h, x + r)
+        for p in parts:
+            y1, _ = st.rms_norm(x[p].contiguous(), w, eps=1e-6, residual=r[p].contiguous(), quantize=kind)
+            if kind is None:
+                assert torch.equal(y[p], y1)
+                continue
+            for whole, one in ((y, y1), (q, st.quantize_activation(x[p].contiguous(), kind))):
+                assert torch.equal(whole.data[p].view(torch.uint8), one.data.view(torch.uint8))
+                assert torch.equal(whole.scale[p].view(torch.uint8), one.scale.view(torch.uint8))
