@@ -71,6 +71,13 @@ Plan plan_of(const st_linear_args& g) {
     return p;
 }
 
+// Threads of the product's launch; a grid dimension holds fewer than 2^32.
+uint64_t threads_of(const st_linear_args& g, const Plan& p) {
+    if (p.one) return (g.n + kOneRows - 1) / kOneRows * 64 * p.waves;
+    if (p.few) return (g.n + 16 * few_groups(g.w_kind) - 1) / (16 * few_groups(g.w_kind)) * 64 * p.waves;
+    return ((g.m + p.bm - 1) / p.bm) * ((g.n + p.bn - 1) / p.bn) * (p.bm == 256 ? 512 : 256);
+}
+
 static_assert(sizeof(st_linear_args) == 152, "the ctypes declaration has this size");
 
 const char* kWho = "st_linear";
@@ -116,6 +123,14 @@ st_status check_args(const st_linear_args* g) {
     return ST_OK;
 }
 
+st_status plan_checked(const st_linear_args& g, Plan* p) {
+    *p = plan_of(g);
+    if (threads_of(g, *p) >> 32)
+        return st_fail(ST_E_SHAPE, "%s: m %llu, n %llu take more threads than one launch holds", kWho, (unsigned long long)g.m,
+                       (unsigned long long)g.n);
+    return ST_OK;
+}
+
 }  // namespace
 
 extern "C" st_status st_linear_workspace_bytes(const st_linear_args* args, uint64_t* bytes) {
@@ -123,8 +138,11 @@ extern "C" st_status st_linear_workspace_bytes(const st_linear_args* args, uint6
     *bytes = 0;
     const st_status r = check_args(args);
     if (r != ST_OK) return r;
-    if (args->m && args->n) *bytes = plan_of(*args).part_bytes;
-    return ST_OK;
+    if (args->m == 0 || args->n == 0) return ST_OK;
+    Plan p;
+    const st_status f = plan_checked(*args, &p);
+    if (f == ST_OK) *bytes = p.part_bytes;
+    return f;
 }
 
 extern "C" st_status st_linear(const st_linear_args* args, void* stream) {
@@ -132,7 +150,9 @@ extern "C" st_status st_linear(const st_linear_args* args, void* stream) {
     if (r != ST_OK) return r;
     const st_linear_args& g = *args;
     if (g.m == 0 || g.n == 0) return ST_OK;
-    const Plan p = plan_of(g);
+    Plan p;
+    const st_status f = plan_checked(g, &p);
+    if (f != ST_OK) return f;
     if (p.part_bytes) {
         if (!g.workspace || g.workspace_bytes < p.part_bytes)
             return st_fail(ST_E_ARG, "%s: %llu bytes of workspace, %llu are needed", kWho,
@@ -151,7 +171,6 @@ extern "C" st_status st_linear(const st_linear_args* args, void* stream) {
     a.act = g.activation; a.bias_type = g.bias_type; a.res_type = g.residual_type; a.out_type = g.out_type;
     a.splits = p.splits; a.steps = p.steps;
     if (p.bm) a.tiles_m = uint32_t((g.m + p.bm - 1) / p.bm), a.tiles_n = uint32_t((g.n + p.bn - 1) / p.bn);
-    if (uint64_t(a.tiles_m) * a.tiles_n > 0x7FFFFFFFull) return st_fail(ST_E_SHAPE, "%s: too many tiles", kWho);
     auto quad = [](const void* v, uint32_t type, uint64_t pitch, uint64_t rows) {
         const uint64_t e = type == ST_OUT_F32 ? 4 : 2;
         return reinterpret_cast<uintptr_t>(v) % (4 * e) == 0 && (rows <= 1 || pitch % 4 == 0);

@@ -12,6 +12,9 @@ constexpr bool is_q(int x) { return x >= ST_X_FP8_ROW; }
 constexpr bool is_fp4(int w) { return w == ST_KIND_NVFP4 || w == ST_KIND_MXFP4; }
 constexpr bool is_mx(int w) { return w == ST_KIND_MXFP8 || w == ST_KIND_MXFP4; }
 
+// linear_one: weight rows per wavefront.
+constexpr int kOneRows = 4;
+
 // linear_few: groups of 16 weight rows per wavefront, and wavefronts per workgroup.  Two groups halve x's traffic for
 // more registers: fp4, whose turn takes twice the x, gains (16 rows through NVFP4 [5120, 25600] on MI355X: 41.8 us with two,
 // 47 with one), the 8-bit kinds lose (block FP8 [4096, 4096], 2 rows: 8.0 against 6.6 us).

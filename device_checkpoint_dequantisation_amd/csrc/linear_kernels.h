@@ -247,7 +247,7 @@ __device__ __forceinline__ uint32_t load_codes(const uint8_t* p, int64_t avail, 
 // The lanes' sums fold together within the wavefront, the slices' sums in LDS.
 template <int X_, int WK_>
 struct One {
-    static constexpr int X = X_, WK = WK_, R = 4;     // weight rows per wavefront
+    static constexpr int X = X_, WK = WK_, R = kOneRows;     // weight rows per wavefront
     static constexpr bool Q = is_q(X), FP4 = is_fp4(WK), GROUPED = WK == ST_KIND_FP8_BLOCK128;
     static constexpr int E = FP4 ? 32 : 16;          // elements of K per lane
     static constexpr int SLICE = 64 * E;

@@ -574,7 +574,8 @@ typedef struct st_linear_args {
  * output alone is too small to fill the GPU).  Everything but the workspace fields must be set. */
 st_status st_linear_workspace_bytes(const st_linear_args* args, uint64_t* bytes);
 /* Errors: ST_E_ARG (null or misaligned pointers, unknown types, an x type that does not go with the weight kind,
- * too little workspace), ST_E_SHAPE (NVFP4 k % 16, MX k % 32, pitches, size limits), ST_E_HIP (the launch). */
+ * too little workspace), ST_E_SHAPE (NVFP4 k % 16, MX k % 32, pitches, size limits; also where m and n take 2^32 threads or more:
+ * from n = 2^26 on for one row, 2^27 for up to 16, or 2^24 tiles of 64 x 64 or more outputs), ST_E_HIP (the launch). */
 st_status st_linear(const st_linear_args* args, void* stream);
 
 /* Rows x [m, d] (bf16, fp16 or fp32, rows `x_pitch` elements apart) to e4m3 codes [m, d] and scales:

@@ -168,3 +168,17 @@ def test_reference_codes_match_torch():
     assert torch.equal(ref.e4m3_codes(v.double()), v.clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8) & 127)
     e = torch.arange(255, dtype=torch.uint8).view(torch.float8_e8m0fnu)
     assert torch.equal(ref.e8m0(e), e.float().double())
+
+
+@pytest.mark.parametrize("kw", [dict(m=1, n=1 << 26, k=4096), dict(m=16, n=1 << 27, k=4096), dict(m=16, n=1 << 29, k=4096, w_kind=7),
+                                dict(m=20, n=1 << 30, k=128), dict(m=(1 << 31) - 1, n=1, k=128, out_pitch=1)])
+def test_linear_refuses_more_threads_than_a_launch_holds(kw):
+    """Sizes whose grid would hold 2^32 threads are refused before anything is launched."""
+    L = _lib.lib()
+    a = _linear_args(**{"x_pitch": kw["k"], "out_pitch": kw["n"], **kw})
+    need = C.c_uint64(7)
+    assert L.st_linear(C.byref(a), None) == -6 and b"threads" in L.st_last_error()
+    assert L.st_linear_workspace_bytes(C.byref(a), C.byref(need)) == -6 and need.value == 0
+    a.n = a.out_pitch = kw["n"] - 512 if kw["n"] > 512 else 1
+    a.m = kw["m"] if kw["n"] > 512 else kw["m"] - 256
+    assert L.st_linear_workspace_bytes(C.byref(a), C.byref(need)) == 0
