@@ -11,13 +11,15 @@ marshals arguments; the kernels are in the library and there is no fallback.
 or, with the activations left in bf16, ``linear(x, q["up.weight"], activation="silu")``.
 
 They run on the current stream (or ``stream``), allocate their outputs with torch, synchronise nothing and can be
-captured into a HIP graph.  They have no backward pass: with grad mode on, inputs that require grad are refused."""
+captured into a HIP graph.  They have no backward pass: with grad mode on, inputs that require grad are refused, and
+so are inputs with a forward-mode tangent."""
 from __future__ import annotations
 
 import ctypes as C
 from dataclasses import dataclass
 
 import torch
+import torch.autograd.forward_ad as _fwd
 
 from . import _lib
 from ._lib import EncodeArgs, LinearArgs, OUT_DTYPES, RmsNormArgs, check, lib
@@ -61,6 +63,7 @@ def _on_device(device, tensors, who: str):
     if device.type != "cuda":
         raise ValueError(f"{who}: needs GPU tensors, got one on {device}")
     grad = torch.is_grad_enabled()
+    forward = getattr(_fwd, "_current_level", 0) >= 0      # inside a forward-mode level: a dual tensor does not require grad
     for t in tensors:
         if t is None:
             continue
@@ -68,6 +71,8 @@ def _on_device(device, tensors, who: str):
             raise ValueError(f"{who}: tensors on {device} and {t.device}")
         if grad and t.requires_grad:
             raise RuntimeError(f"{who}: has no backward pass; call it under torch.no_grad() or detach its inputs")
+        if forward and _fwd.unpack_dual(t).tangent is not None:
+            raise RuntimeError(f"{who}: has no derivative; an input carries a forward-mode tangent, which would be lost")
 
 
 def _rows(t, cols: int, name: str, who: str):

@@ -182,3 +182,27 @@ def test_linear_refuses_more_threads_than_a_launch_holds(kw):
     a.n = a.out_pitch = kw["n"] - 512 if kw["n"] > 512 else 1
     a.m = kw["m"] if kw["n"] > 512 else kw["m"] - 256
     assert L.st_linear_workspace_bytes(C.byref(a), C.byref(need)) == 0
+
+
+def test_operators_refuse_forward_mode_tangents(monkeypatch):
+    """A dual tensor does not require grad; its tangent would be lost without a word."""
+    import torch.autograd.forward_ad as fwd
+    from device_checkpoint_dequantisation_amd import ops
+    check = ops._on_device                 # CPU tensors are refused for their device: let them pass as GPU ones
+    gpu = type("Device", (), {"type": "cuda", "__eq__": lambda a, b: True, "__ne__": lambda a, b: False})()
+    monkeypatch.setattr(ops, "_on_device", lambda device, tensors, who: check(gpu, tensors, who))
+
+    def dual(*shape, dtype=torch.bfloat16):
+        return fwd.make_dual(torch.zeros(shape, dtype=dtype), torch.ones(shape, dtype=dtype))
+    with fwd.dual_level():
+        x, w = _x(), _weight()
+        for grad in (True, False):
+            with torch.set_grad_enabled(grad):
+                for call in (lambda: st.linear(dual(4, 128), w), lambda: st.linear(dual(4, 128)[:2], w),
+                             lambda: st.linear(x, w, bias=dual(64)), lambda: st.linear(x, w, residual=dual(4, 64)),
+                             lambda: st.rms_norm(dual(4, 128)), lambda: st.rms_norm(x, dual(128, dtype=torch.float32)),
+                             lambda: st.rms_norm(x, residual=dual(4, 128)), lambda: st.quantize_activation(dual(4, 128), "MXFP8"),
+                             lambda: st.quantize_activation(x, "MXFP8", gate=dual(4, 128))):
+                    with pytest.raises(RuntimeError, match="tangent"):
+                        call()
+        ops._on_device(gpu, (None, x, w.data, w.scale, _weight("MXFP8").scale), "linear")
