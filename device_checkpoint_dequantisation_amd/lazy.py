@@ -686,6 +686,8 @@ class _StoredLinear(_Forward):
         if self.loader._stored[mod] is None:
             self.loader.materialize(mod)
         torch = _torch()
+        if x.dim() == 2:       # nn.Linear takes any strides
+            x = ops.adjacent_rows(x)
         dtype = {torch.bfloat16: "bf16", torch.float16: "f16"}.get(x.dtype)      # another type is refused by the operator
         if self.encode is not None and dtype is not None:
             x = ops.quantize_activation(x, self.encode)
@@ -698,6 +700,8 @@ class _OperatorNorm(_Forward):
         if self.loader is None:
             return type(mod).forward(mod, x)
         from . import ops
+        if x.dim() == 2:
+            x = ops.adjacent_rows(x)
         # a norm without an eps computes in fp32 for 16-bit rows too, and takes fp32's
         return ops.rms_norm(x, mod.weight, eps=_torch().finfo(_torch().float32).eps if mod.eps is None else mod.eps)
 

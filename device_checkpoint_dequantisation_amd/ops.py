@@ -75,10 +75,17 @@ def _on_device(device, tensors, who: str):
             raise RuntimeError(f"{who}: has no derivative; an input carries a forward-mode tangent, which would be lost")
 
 
+def adjacent_rows(t):
+    """t [M, K], or a copy of it where its rows' elements are not adjacent or its rows overlap (one row for all is neither)."""
+    ok = (t.shape[1] <= 1 or t.stride(1) == 1) and (t.shape[0] <= 1 or t.stride(0) == 0 or t.stride(0) >= t.shape[1])
+    return t if ok else t.contiguous()
+
+
 def _rows(t, cols: int, name: str, who: str):
-    """t as [rows, cols] with adjacent columns: (tensor, pitch in elements)."""
+    """t as [rows, cols] with adjacent columns: (tensor, pitch in elements).  A matrix is taken as it is, other shapes are copied
+    where they are no such rows (whether reshape itself copies depends on the batch)."""
     if t.dim() != 2:
-        t = t.reshape(-1, cols) if t.numel() else t.new_empty((_count(t.shape[:-1]), cols))
+        t = adjacent_rows(t.reshape(-1, cols)) if t.numel() else t.new_empty((_count(t.shape[:-1]), cols))
     if cols > 1 and t.stride(1) != 1:
         raise ValueError(f"{who}: the last dimension of {name} must be contiguous (stride 1, got {t.stride(1)})")
     return t, t.stride(0)
@@ -165,7 +172,8 @@ def linear(x, weight, bias=None, residual=None, activation: str | None = None, o
     (FP8_ROW with FP8_TENSOR, FP8_GROUP128 with FP8_BLOCK128, MXFP8 with MXFP8 and MXFP4).  ``bias`` [N] and ``residual``
     [..., N] are bf16, fp16 or fp32; ``activation`` is None, "relu", "silu", "gelu" (erf) or "gelu_tanh".  The result
     has ``out_dtype`` (bf16, f16 or f32; default x's type, bf16 for 8-bit x), or goes to ``out``, which may be
-    ``residual`` itself.  The weight's exact values enter (code times scale, not rounded to bf16 first), sums are fp32
+    ``residual`` itself.  The rows of a matrix (and of ``residual``) are read where they are, at any pitch, and have to have
+    adjacent elements; inputs of other shapes are copied where they have not.  The weight's exact values enter (code times scale, not rounded to bf16 first), sums are fp32
     and the result is rounded once."""
     who = "linear"
     n, k = _check_weight(weight, who)

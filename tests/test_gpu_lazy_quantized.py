@@ -153,3 +153,24 @@ def test_norm_without_an_eps_of_its_own(dtype, tmp_path):
     t = torch.finfo(dtype)
     assert ((got - want).abs() <= want.abs() * (t.eps / 2 + 16 * 2.0 ** -24) + t.smallest_normal * t.eps / 2).all()
     loader.detach()
+
+
+def test_inputs_of_any_layout(tmp_path):
+    """Transposed, strided, overlapping and broadcast rows through the modules, and through the operator where they are
+    no matrix, for one image as for two."""
+    sd = st.StreamStateDict(_file(tmp_path, 3), DEV)
+    root, lin = _module(3)
+    loader = st.LazyModuleLoader(root, sd, quantized="activations")
+    g = torch.Generator().manual_seed(5)
+    long = torch.randn(960 * 8, generator=g).to(torch.bfloat16).to(DEV)
+    t = torch.randn(2, 960, 3, 4, generator=g).to(torch.bfloat16).to(DEV)
+    for x in (t[0, :, 0].t(), long.unfold(0, 960, 8), long[::8], long[:960].expand(3, 960), t.flatten(2).transpose(1, 2),
+              t[:1].flatten(2).transpose(1, 2)):
+        assert torch.equal(lin(x), lin(x.contiguous()))
+    w = sd.load_quantized([LINEARS[3][0] + ".weight"], copy=True)[LINEARS[3][0] + ".weight"]
+    for x in (t.flatten(2).transpose(1, 2), t[:1].flatten(2).transpose(1, 2)):
+        flat = x.contiguous()
+        assert torch.equal(st.linear(x, w), st.linear(flat, w)) and torch.equal(st.rms_norm(x, residual=x)[0], st.rms_norm(flat, residual=flat)[0])
+        q, p = st.quantize_activation(x, "MXFP8", gate=x), st.quantize_activation(flat, "MXFP8", gate=flat)
+        assert torch.equal(q.data.view(torch.uint8), p.data.view(torch.uint8)) and torch.equal(q.scale.view(torch.uint8), p.scale.view(torch.uint8))
+    loader.detach()

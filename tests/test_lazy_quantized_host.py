@@ -222,3 +222,25 @@ def test_a_failed_load_counts_nothing():
     assert loader.resident_bytes == a["weight"].data.numel() + 4 + 48
     loader.evict_all()
     assert loader.resident_bytes == 0 and lin.bias.is_meta
+
+
+def test_inputs_of_any_layout(monkeypatch):
+    """nn.Linear and nn.RMSNorm take transposed and overlapping rows; the operators get adjacent ones."""
+    inner = {n: getattr(ops, n) for n in ("linear", "rms_norm")}
+
+    def adjacent(name):
+        def call(x, *args, **kw):
+            rows, pitch = ops._rows(x, x.shape[-1], "x", name)      # refuses what the operator refuses
+            assert rows.shape[0] == 1 or pitch == 0 or pitch >= x.shape[-1]
+            return inner[name](x, *args, **kw)
+        return call
+    for n in inner:
+        monkeypatch.setattr(ops, n, adjacent(n))
+    a = _checkpoint(1)
+    lin, norm = _linear(), torch.nn.RMSNorm(64, eps=1e-6, device="meta", dtype=torch.bfloat16)
+    st.LazyModuleLoader(lin, a, quantized="weights")
+    st.LazyModuleLoader(norm, _Memory(weight=torch.ones(64, dtype=torch.bfloat16)), quantized="weights")
+    long = _x(64 * 8)
+    for x in (_x(64, 5).t(), long.unfold(0, 64, 8), long[::8], long[:64].expand(3, 64), _x(2, 64, 5).transpose(1, 2)):
+        for mod in (lin, norm):
+            assert torch.equal(mod(x), mod(x.contiguous()))

@@ -206,3 +206,25 @@ def test_operators_refuse_forward_mode_tangents(monkeypatch):
                     with pytest.raises(RuntimeError, match="tangent"):
                         call()
         ops._on_device(gpu, (None, x, w.data, w.scale, _weight("MXFP8").scale), "linear")
+
+
+def test_rows_of_any_layout_are_made_adjacent_whatever_the_batch():
+    """[..., K] inputs whose elements are not adjacent are copied for one image as for two; a matrix of such rows is refused."""
+    from device_checkpoint_dequantisation_amd import ops
+    for batch in (1, 2):
+        image = torch.randn(batch, 6, 2, 5)                        # [B, K, H, W], the usual patch embedding
+        t = image.flatten(2).transpose(1, 2)
+        rows, pitch = ops._rows(t, 6, "x", "linear")
+        assert rows.stride(1) == 1 and pitch == rows.stride(0) >= 6 and torch.equal(rows, t.reshape(-1, 6))
+        windows = torch.arange(20.0).unfold(0, 6, 2)[None].expand(batch, 8, 6)      # rows that overlap
+        rows, pitch = ops._rows(windows, 6, "x", "linear")
+        assert pitch >= 6 and torch.equal(rows, windows.reshape(-1, 6))
+        row = torch.randn(6)
+        rows, pitch = ops._rows(row.expand(batch, 3, 6), 6, "residual", "linear")
+        assert torch.equal(rows, row.expand(3 * batch, 6)) and pitch in (0, 6)
+    rows, pitch = ops._rows(torch.arange(12.0)[::2], 6, "x", "linear")
+    assert rows.shape == (1, 6) and rows.stride(1) == 1
+    t = torch.randn(4, 3, 6)                                       # adjacent already: no copy
+    assert ops._rows(t, 6, "x", "linear")[0].data_ptr() == t.data_ptr()
+    with pytest.raises(ValueError, match="stride 1"):
+        ops._rows(torch.randn(6, 4).t(), 6, "x", "linear")
