@@ -58,7 +58,8 @@ __device__ __forceinline__ float activate(float v, uint32_t act) {
     switch (act) {
         case ST_ACT_RELU: return v != v ? v : fmaxf(v, 0.0f);
         case ST_ACT_SILU: return silu(v);
-        case ST_ACT_GELU: return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
+        // (1 + erf z) / 2 as erfc(-z) / 2: 1 + erf cancels for negative z (4% off at v = -5, 0 from -5.5 on)
+        case ST_ACT_GELU: return 0.5f * v * erfcf(v * -0.70710678118654752f);
         // (1 + tanh u) / 2 is the logistic function of 2u
         case ST_ACT_GELU_TANH: {
             const float u = 1.5957691216057308f * v * (1.0f + 0.044715f * v * v);
