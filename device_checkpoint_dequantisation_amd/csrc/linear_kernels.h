@@ -4,12 +4,14 @@
 // bf16 or fp16, or in e4m3 with scales (FP8_ROW, FP8_GROUP128, MXFP8).
 //
 // Arithmetic.  w[n, k] is the code's value times its scales, not rounded to bf16 as a decoded weight is.
-// Every product is exact and every sum is kept in fp32:
+// Every product is exact and every sum is kept in fp32, but for the f8f6f4 instructions below:
 //  * dense x: e4m3 and e2m1 codes, an e2m1 code times its e4m3 block scale (at most 6 significant
 //    bits) and a code times a power of two are exact in bf16; the first three are exact in fp16 too, so the
 //    weight enters the bf16 or fp16 matrix instructions without rounding.  fp16 rows against an MX
-//    weight, whose scales reach beyond fp16, are split into two bf16 terms (x = hi + lo, exact).
-//  * e4m3 x: widened to bf16 (times its E8M0 scale, exact) like the weight; or, for large products with 16-bit outputs,
+//    weight, whose scales reach beyond fp16, are split into two bf16 terms (x = hi + lo, exact).  An MX value outside bf16's range
+//    is the exception: 2^128 or more (e4m3 under scales from 2^120 on, e2m1 under 2^126 and 2^127) becomes an infinity, and what
+//    lies below 2^-126 a multiple of 2^-133 (e4m3 under 2^-125 and less; e2m1 loses nothing).
+//  * e4m3 x: widened to bf16 (times its E8M0 scale) like the weight; or, for large products with 16-bit outputs,
 //    the f8f6f4 matrix instructions, which run at twice the rate and apply the E8M0 scales of both sides
 //    themselves.  Of 16 products that lie in one lane these cut what is below 2^-13 of the largest (measured: such
 //    a product next to a larger one is lost; across lanes the sum is whole): at most 15 * 2^-13 of that largest product
@@ -138,7 +140,7 @@ __global__ __launch_bounds__(256) void linear_join(Args a) {
 // ------------------------------------------------------------------------- weight codes to matrix operands
 
 // Eight codes to eight bf16 or fp16 values times 2^e (s = 2^e; NVFP4: times the e4m3 block scale's value s).
-// Exact in every case (see the top of the file).  lo and hi: the eight e4m3 codes; fp4: lo alone.
+// Exact within bf16's range (see the top of the file).  lo and hi: the eight e4m3 codes; fp4: lo alone.
 template <bool F16, int WK>
 __device__ __forceinline__ u32x4 codes8(uint32_t lo, uint32_t hi, float s) {
     u32x4 r;

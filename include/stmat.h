@@ -547,7 +547,8 @@ typedef enum st_activation {
 
 /* out[m, n] = act(sum_k x[m, k] w[n, k] + bias[n]) + residual[m, n].
  * w is a quantised weight as stored (contiguous [n, k], the kinds from ST_KIND_FP8_TENSOR on); its value is
- * code * scale(s) in exact arithmetic, not the bf16 value st_materialize rounds it to.  Sums are kept in fp32
+ * code * scale(s) in exact arithmetic, not the bf16 value st_materialize rounds it to; an MX value, of x or w, of 2^128 or more may
+ * enter as an infinity, as fp32 would hold it, and one below 2^-126 as the nearest multiple of 2^-133.  Sums are kept in fp32
  * and the result is rounded once.  Pitches are in elements between rows of x, residual and out (the elements of a
  * row are adjacent; a residual pitch of 0 adds one row to every row; ignored for m <= 1).  out may be the
  * residual itself; otherwise out must not overlap an input. */

@@ -33,3 +33,39 @@ def test_activations_relative_to_their_value(act, m):
     }[act]
     bad = (got - want).abs() > want.abs() * steps * 2.0 ** -24 + 2.0 ** -149
     assert not bad.any(), f"{int(bad.sum())} of {bad.numel()}, first at {v[bad.nonzero()[0, 1]].item()}"
+
+
+def _hot(xk, m, k, p):
+    """Rows that are p = 2^e at one column each."""
+    hot = torch.zeros(m, k, dtype=torch.float64)
+    cols = (torch.arange(m) * 37 + 5) % k
+    hot[torch.arange(m), cols] = p if xk in ref.DT else 1.0
+    if xk in ref.DT:
+        return hot.to(ref.DT[xk]), cols
+    s = torch.full((m, k // 32), 127 + int(math.log2(p)), dtype=torch.uint8).view(torch.float8_e8m0fnu)
+    return st.QuantizedActivation(xk, (m, k), hot.to(torch.float8_e4m3fn), s), cols
+
+
+@pytest.mark.parametrize("xk,wk", [(x, w) for x in ("bf16", "f16", "MXFP8") for w in ("MXFP8", "MXFP4")])
+@pytest.mark.parametrize("m", [1, 5, 40, 130])
+def test_mx_scales_at_both_ends(xk, wk, m):
+    """Every E8M0 code, with weights whose values fp32 holds, times a power of two that keeps the product in range.  Values
+    below 2^-126 are taken to multiples of 2^-133, bf16's smallest step."""
+    k, n = 256, 64
+    for code in (0, 1, 2, 3, 10, 120, 246, 247, 250, 253, 254):
+        w = ref.random_weight(st, wk, n, k, code)
+        w.scale = torch.full((n, k // 32), code, dtype=torch.uint8).view(torch.float8_e8m0fnu)
+        if code > 240:        # magnitudes below 2 (and codes of them alone)
+            keep = 0x3F if wk == "MXFP8" else None
+            w.data = ((w.data.view(torch.uint8) & (keep | 0x80)).view(torch.float8_e4m3fn) if keep else w.data & 0xBB)
+        v = ref.weight_value(w)
+        assert (v.abs() < 2.0 ** 128).all()
+        p = 2.0 ** -14 if code > 64 else 2.0 ** 15
+        x, cols = _hot(xk, m, k, p)
+        print(f"mx ends {xk} {wk} {m} {code}", flush=True)
+        got = _run(x, w, out_dtype="f32").cpu().double()
+        want = v.to(torch.bfloat16).double()[:, cols].t() * p
+        assert torch.equal(got, want)
+        if xk == "MXFP8" and m > 64:      # the scaled instructions take the value as it is
+            got = _run(x, w, out_dtype="bf16").cpu()
+            assert torch.equal(got, (v[:, cols].t() * p).to(torch.bfloat16))
