@@ -42,7 +42,7 @@ Plan plan_of(const st_linear_args& g) {
     if (g.x_type == ST_X_MXFP8) whole = whole && al(g.x_scale, 4);
     p.tail = p.direct && !whole;
     p.bm = g.m <= 64 ? 64 : 128;
-    // e4m3 x, 16-bit output: tiles of 256 halve the bytes that pass through L2 and LDS per product, and leave one workgroup
+    // e4m3 x, bf16 output: tiles of 256 halve the bytes that pass through L2 and LDS per product, and leave one workgroup
     // per CU (8192 rows through MXFP8 [12288, 4096]: 475 us against 601 in tiles of 128; 4096 rows through block FP8
     // [4096, 12288], 256 tiles: 269 against 284; with fewer tiles than CUs the smaller ones win).  bf16 and fp16 x gain nothing
     // (NVFP4 prefill 623 against 615 us).
@@ -50,9 +50,11 @@ Plan plan_of(const st_linear_args& g) {
     // [6000, 5024], a partial last step: 744 us in tiles of 256, 336 in tiles of 128).
     const uint64_t tiles256 = ((g.m + 255) / 256) * ((g.n + 255) / 256);
     const bool fits = p.direct && !(p.tail && is_mx(g.w_kind));
-    if (q && fits && g.m > 64 && g.out_type != ST_OUT_F32 && tiles256 >= 256) p.bm = 256;
+    // The f8f6f4 instructions, whose sums carry some 16 bits, for bf16 outputs alone; fp16 and fp32 ones have fp32 sums
+    // (8192 rows through MXFP8 [12288, 4096] with MXFP8 rows: 476 us to bf16, 818 to fp32).
+    p.f8 = q && g.m > 64 && g.out_type == ST_OUT_BF16;
+    if (p.f8 && fits && tiles256 >= 256) p.bm = 256;
     p.bn = p.bm;
-    p.f8 = q && p.bm > 64 && g.out_type != ST_OUT_F32;
     const uint64_t tiles = ((g.m + p.bm - 1) / p.bm) * ((g.n + p.bn - 1) / p.bn), all = (g.k + ks - 1) / ks;
     // Too few tiles to fill 256 CUs (with two workgroups each, where tiles are small): split K, in whole groups of 128, while
     // each part keeps 8 steps.  The parts' sums pass through memory and take a second launch, which a CU's one large tile does not

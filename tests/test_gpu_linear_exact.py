@@ -69,3 +69,39 @@ def test_mx_scales_at_both_ends(xk, wk, m):
         if xk == "MXFP8" and m > 64:      # the scaled instructions take the value as it is
             got = _run(x, w, out_dtype="bf16").cpu()
             assert torch.equal(got, (v[:, cols].t() * p).to(torch.bfloat16))
+
+
+def _under_residual(xk, wk, m, n, k, out):
+    """A product under a residual that takes its result away, in a 16-bit type: what is left shows the sums' own error.
+    Returns (error, what fp32 sums and the rounding of the rest may be off by, sum |x w|)."""
+    x, w = ref.random_rows(st, xk, m, k, 3), ref.random_weight(st, wk, n, k, 4)
+    a, b = (x.double() if xk in ref.DT else ref.rows_value(x.kind, x.data, x.scale)).to(DEV), ref.weight_value(w).to(DEV)
+    want, s = torch.mm(a, b.t().contiguous()), torch.mm(a.abs(), b.abs().t().contiguous())
+    back = -want.float()
+    left = want + back.double()                          # what rounding `back` left
+    err = (_run(x, w, residual=back, out_dtype=out).double() - left).abs()
+    # cutting what is below 2^-13 of the largest of 16 products: for bf16 from 8-bit rows only
+    cut = ref.f8_tolerance(x, w).to(DEV) * (1 + 2.0 ** -8) if xk not in ref.DT and out == "bf16" else 0.0
+    return err, ref.linear_tolerance(left, s + back.abs().double(), k, ref.DT[out]) + cut, s
+
+
+@pytest.mark.parametrize("xk,wk", DENSE + EIGHT)
+@pytest.mark.parametrize("out", ["bf16", "f16"])
+@pytest.mark.parametrize("m,n,k", [(1, 200, 1056), (40, 200, 4096), (70, 130, 4096), (100, 200, 25600), (4096, 4352, 1056)])
+def test_sums_under_a_residual(xk, wk, out, m, n, k):
+    """fp32 sums for every 16-bit result but bf16 from 8-bit rows, whose scaled instructions cut from the sums no more than
+    2^-13 of the largest of 16 neighbouring products for each of the others."""
+    print(f"sums {xk} {wk} {m} {n} {k} {out}", flush=True)
+    err, tol, s = _under_residual(xk, wk, m, n, k, out)
+    print(f"  off by up to {(err / s).max().item():.2g}, rms {(err / s).square().mean().sqrt().item():.2g} of sum |x w|", flush=True)
+    assert (err <= tol).all()
+
+
+@pytest.mark.parametrize("xk,wk", EIGHT)
+@pytest.mark.parametrize("m,n,k", [(100, 512, 4096), (4096, 4352, 1056)])
+def test_fp16_results_of_8_bit_rows_have_fp32_sums(xk, wk, m, n, k):
+    """The error of K / 32 matrix instructions that add 32 products each in fp32 (8 roundings or cuts of 2^-23 allowed for
+    each, and 32 for joining, scales and epilogue), of which the average, not the worst element, is held: 2^-24 of the sum of
+    magnitudes for each of sqrt(8 K / 32 + 32) steps that err independently, and twice that."""
+    err, _, s = _under_residual(xk, wk, m, n, k, "f16")
+    assert (err / s).square().mean().sqrt() <= 2 * 2.0 ** -24 * math.sqrt(8 * k / 32 + 32)
