@@ -71,6 +71,53 @@ def test_mx_scales_at_both_ends(xk, wk, m):
             assert torch.equal(got, (v[:, cols].t() * p).to(torch.bfloat16))
 
 
+@pytest.mark.parametrize("xk,wk", DENSE + EIGHT)
+@pytest.mark.parametrize("m,n,k", [(1, 70, 25600), (3, 96, 25600), (16, 64, 12288), (48, 130, 25600), (130, 200, 25600), (300, 520, 5120)])
+def test_exact_sums_through_long_and_split_k(xk, wk, m, n, k):
+    """Whole and half numbers through K of many steps, split over workgroups where the output is small, with tensor and
+    row scales of 24 bits: every sum is exact in fp32, so the result is that sum times the scales, each product rounded
+    once; a weight or a partial sum held in fewer bits shows."""
+    print(f"long exact {xk} {wk} {m} {n} {k}", flush=True)
+    g = torch.Generator().manual_seed(k + m)
+    small = torch.tensor([0.0, 1.0, -1.0, 2.0, -2.0, 0.5, -0.5, 1.5])
+    pick = lambda *s: small[torch.randint(0, 8, s, generator=g)]   # noqa: E731
+    two = lambda s: torch.randint(126, 129, tuple(s), generator=g, dtype=torch.uint8)   # noqa: E731
+    w, x = ref.random_weight(st, wk, n, k, 1), ref.random_rows(st, xk, m, k, 2)
+    if wk in ("NVFP4", "MXFP4"):
+        w.data = w.data & 0xBB                          # magnitudes up to 1.5
+    else:
+        w.data = pick(n, k).to(torch.float8_e4m3fn)
+    tail = torch.ones(())                                # what multiplies the finished sum
+    if wk == "FP8_TENSOR":
+        w.scale = tail = torch.tensor(1.0 + 2.0 ** -12 + 2.0 ** -23)
+    elif wk == "NVFP4":
+        w.scale = (2.0 ** (two(w.scale.shape).float() - 127)).to(torch.float8_e4m3fn)
+        w.scale2 = tail = torch.tensor(1.0 + 2.0 ** -11 + 2.0 ** -22)
+    elif wk == "FP8_BLOCK128":
+        w.scale = 2.0 ** (two(w.scale.shape).float() - 127)
+    else:
+        w.scale = two(w.scale.shape).view(torch.float8_e8m0fnu)
+    rows = torch.ones(m, 1)
+    if xk in ref.DT:
+        x = pick(m, k).to(ref.DT[xk])
+    else:
+        x.data = pick(m, k).to(torch.float8_e4m3fn)
+        if xk == "MXFP8":
+            x.scale = two(x.scale.shape).view(torch.float8_e8m0fnu)
+        elif xk == "FP8_GROUP128":
+            x.scale = 2.0 ** (two(x.scale.shape).float() - 127)
+        else:
+            x.scale = 1 + torch.rand(m, generator=g)
+            rows = x.scale[:, None]
+    bare = st.QuantizedWeight("w", wk, (n, k), w.data, w.scale if tail is not w.scale else torch.ones(()),
+                              None if w.scale2 is None else torch.ones(()))
+    plain = x if xk != "FP8_ROW" else st.QuantizedActivation(xk, (m, k), x.data, torch.ones(m))
+    total, s = ref.linear(plain, bare)
+    assert s.max() < 2.0 ** 20                           # in steps of 2^-4 at the least: below 2^24 of them
+    want = total.float() * tail * rows
+    assert torch.equal(_run(x, w, out_dtype="f32").cpu(), want)
+
+
 def _under_residual(xk, wk, m, n, k, out):
     """A product under a residual that takes its result away, in a 16-bit type: what is left shows the sums' own error.
     Returns (error, what fp32 sums and the rounding of the rest may be off by, sum |x w|)."""
