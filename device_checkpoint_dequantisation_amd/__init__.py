@@ -606,9 +606,8 @@ __all__ += ["StreamStateDict", "PrefixViewStateDict", "FilterViewStateDict", "Re
             "load_checkpoint", "shard_files"]
 
 # Operators on quantised weights (ops.py), imported on first use: they need torch, which the rest of the package imports
-# only where it allocates.
+# only where it allocates, and so are not in __all__, whose names a star import fetches at once.
 _OPS = ("QuantizedActivation", "linear", "quantize_activation", "rms_norm")
-__all__ += list(_OPS)
 
 
 def __getattr__(name):

@@ -228,3 +228,16 @@ def test_rows_of_any_layout_are_made_adjacent_whatever_the_batch():
     assert ops._rows(t, 6, "x", "linear")[0].data_ptr() == t.data_ptr()
     with pytest.raises(ValueError, match="stride 1"):
         ops._rows(torch.randn(6, 4).t(), 6, "x", "linear")
+
+
+def test_importing_the_package_leaves_torch_alone():
+    """The header side of the package works without torch: neither an import nor a star import brings it in, and the
+    operators are there on first use."""
+    import subprocess
+    import sys
+    code = ("import sys\nimport device_checkpoint_dequantisation_amd as st\nfrom device_checkpoint_dequantisation_amd import *\n"
+            "assert 'torch' not in sys.modules and SafeTensorIndex is st.SafeTensorIndex\n"
+            "assert st.linear.__module__.endswith('.ops') and 'torch' in sys.modules\n"
+            "from device_checkpoint_dequantisation_amd import QuantizedActivation, quantize_activation, rms_norm\n")
+    done = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0, done.stderr
