@@ -161,7 +161,16 @@ def _overlaps(out, t) -> bool:
         last = sum((s - 1) * st for s, st in zip(x.shape, x.stride()))
         return x.data_ptr(), x.data_ptr() + (last + 1) * x.element_size()
     (a, b), (c, d) = span(out), span(t)
-    return a < d and c < b
+    if not (a < d and c < b):
+        return False
+    if out.dim() == t.dim() == 2 and out.shape[0] > 1 and t.shape[0] > 1:
+        # columns of one buffer: the same pitch p, and rows that start `by` bytes apart modulo p
+        p = out.stride(0) * out.element_size()
+        wide, other = out.shape[1] * out.element_size(), t.shape[1] * t.element_size()
+        if p == t.stride(0) * t.element_size() and out.stride(1) == t.stride(1) == 1:
+            by = (c - a) % p
+            return by < wide or by + other > p
+    return True
 
 
 def linear(x, weight, bias=None, residual=None, activation: str | None = None, out_dtype: str | None = None, out=None,
@@ -228,8 +237,8 @@ def linear(x, weight, bias=None, residual=None, activation: str | None = None, o
         if not ((n <= 1 or o2.stride(1) == 1) and (m <= 1 or o2.stride(0) >= n)):
             raise ValueError(f"{who}: out has strides {out.stride()}")
         same = r2 is not None and r2.data_ptr() == o2.data_ptr() and r2.dtype == o2.dtype and r2.stride() == o2.stride()
-        for t in (xd, xs, weight.data, weight.scale, weight.scale2, bias, None if same else residual):
-            if not (not _overlaps(out, t)):
+        for t in (x2, xs, weight.data, weight.scale, weight.scale2, bias, None if same else r2):
+            if _overlaps(o2, t):
                 raise ValueError(f"{who}: out overlaps an input")
     if m == 0 or n == 0:
         return out

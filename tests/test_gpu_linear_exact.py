@@ -152,3 +152,21 @@ def test_fp16_results_of_8_bit_rows_have_fp32_sums(xk, wk, m, n, k):
     magnitudes for each of sqrt(8 K / 32 + 32) steps that err independently, and twice that."""
     err, _, s = _under_residual(xk, wk, m, n, k, "f16")
     assert (err / s).square().mean().sqrt() <= 2 * 2.0 ** -24 * math.sqrt(8 * k / 32 + 32)
+
+
+@pytest.mark.parametrize("m", [1, 7, 70])
+def test_out_beside_its_input_in_one_buffer(m):
+    """x, residual and out as columns of one buffer: out's are written, the others and what lies between left as they were."""
+    k, n = 128, 64
+    x, w = ref.random_rows(st, "bf16", m, k, 5), ref.to(ref.random_weight(st, "FP8_TENSOR", n, k, 6), DEV)
+    r = torch.randn(m, n, generator=torch.Generator().manual_seed(7)).to(torch.bfloat16).to(DEV)
+    buf = torch.full((m, k + 2 * n + 16), 3.0, dtype=torch.bfloat16, device=DEV)
+    buf[:, :k], buf[:, k + n: k + 2 * n] = x.to(DEV), r
+    before = buf.clone()
+    want = st.linear(x.to(DEV), w, residual=r)
+    st.linear(buf[:, :k], w, residual=buf[:, k + n: k + 2 * n], out=buf[:, k: k + n])
+    assert torch.equal(buf[:, k: k + n], want)
+    buf[:, k: k + n] = 3.0
+    assert torch.equal(buf, before)
+    with pytest.raises(ValueError, match="overlaps"):
+        st.linear(buf[:, :k], w, out=buf[:, k - 1: k - 1 + n])

@@ -241,3 +241,18 @@ def test_importing_the_package_leaves_torch_alone():
             "from device_checkpoint_dequantisation_amd import QuantizedActivation, quantize_activation, rms_norm\n")
     done = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
     assert done.returncode == 0, done.stderr
+
+
+def test_overlap_of_columns_of_one_buffer():
+    """Columns of one buffer lie between each other without overlapping; what shares a byte does."""
+    from device_checkpoint_dequantisation_amd import ops
+    buf = torch.zeros(7, 40)
+    cols = lambda a, b, rows=slice(None): buf[rows, a:b]   # noqa: E731
+    for out, t, want in ((cols(0, 16), cols(16, 40), False), (cols(16, 40), cols(0, 16), False), (cols(0, 16), cols(15, 20), True),
+                         (cols(0, 16), cols(0, 16), True), (cols(10, 20), cols(20, 30, slice(2, 5)), False),
+                         (cols(10, 20, slice(0, 3)), cols(12, 14, slice(3, 7)), False), (cols(30, 40), cols(0, 1), False),
+                         (cols(10, 20), cols(0, 40), True), (cols(0, 16), cols(16, 40).view(torch.int32), False),
+                         (cols(0, 16), buf[3, 4:9], True), (cols(0, 16), buf[3, 20:29], True),      # (a row: by its span)
+                         (cols(0, 16), torch.zeros(7, 16), False), (cols(0, 16), None, False), (cols(0, 16), buf[:0], False)):
+        assert ops._overlaps(out, t) == want, (out.storage_offset(), None if t is None else (t.shape, t.storage_offset()))
+    assert ops._overlaps(cols(0, 20), buf.view(torch.bfloat16)[:, 36:44]) and not ops._overlaps(cols(0, 20), buf.view(torch.bfloat16)[:, 40:44])
