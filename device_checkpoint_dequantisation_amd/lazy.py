@@ -665,6 +665,25 @@ def _stored_bytes(q) -> int:
     return sum(t.numel() * t.element_size() for t in (q.data, q.scale, q.scale2) if t is not None)
 
 
+def _refuse_meta(mod):
+    meta = [n for n, p in mod.named_parameters(recurse=False) if p.is_meta]
+    if meta:
+        raise RuntimeError(f"{type(mod).__name__}: {', '.join(meta)} not loaded (a meta tensor, and its loader is detached); "
+                           "attach a loader, or load it by hand with the loader's materialize()")
+
+
+class _NotLoaded:
+    """The forward_pre_hook that a detached module with meta parameters keeps until it has them: torch computes with a
+    meta weight without a word and returns memory that nobody wrote."""
+
+    def __init__(self, mod):
+        self.handle = mod.register_forward_pre_hook(self)
+
+    def __call__(self, mod, args):
+        _refuse_meta(mod)
+        self.handle.remove()
+
+
 class _Forward:
     """A module's forward through the operators, while ``loader`` is attached; afterwards the module's own.  An
     object and not a closure, so that a deep copy of the module takes the copied loader and module."""
@@ -680,6 +699,8 @@ class _StoredLinear(_Forward):
 
     def __call__(self, input):      # named as nn.Linear.forward names it
         x, mod = input, self.mod
+        if self.loader is None:
+            _refuse_meta(mod)
         if self.loader is None or not mod.weight.is_meta:      # detached, or a weight that was assigned since
             return type(mod).forward(mod, x)
         from . import ops
@@ -764,6 +785,10 @@ class LazyModuleLoader:
                 fwd = self._compute_on_stored(mod, ref.meta) if pname == "weight" else None
                 if fwd is not None:
                     mod.forward = self._forwards[mod] = fwd
+        for mod in self._owned:
+            for h in list(mod._forward_pre_hooks.values()):
+                if isinstance(h, _NotLoaded):
+                    h.handle.remove()
         self._hooks = [mod.register_forward_pre_hook(self._pre_hook) for mod in self._owned]
 
     def _compute_on_stored(self, mod, meta):
@@ -839,7 +864,8 @@ class LazyModuleLoader:
 
     def detach(self):
         """Remove the hooks, and the forwards that compute on stored weights.  Parameters keep their current state; stored
-        weights are let go, so those modules' weight parameters are the meta tensors they were."""
+        weights are let go, so those modules' weight parameters are the meta tensors they were.  A module with meta
+        parameters refuses to run until they are loaded (:meth:`materialize`, another loader) or assigned."""
         for h in self._hooks:
             h.remove()
         self._hooks = []
@@ -855,3 +881,6 @@ class LazyModuleLoader:
                 if not self._resident[mod]:
                     del self._resident[mod]
         self._stored = {}
+        for mod, names in self._owned.items():
+            if any(mod._parameters[p].is_meta for p in names):
+                _NotLoaded(mod)

@@ -133,3 +133,27 @@ def test_more_rows_than_one_launch_takes(d):
             for whole, one in ((y, y1), (q, st.quantize_activation(x[p].contiguous(), kind))):
                 assert torch.equal(whole.data[p].view(torch.uint8), one.data.view(torch.uint8))
                 assert torch.equal(whole.scale[p].view(torch.uint8), one.scale.view(torch.uint8))
+
+
+# ------------------------------------------------------------------------------------------------ layouts
+
+@pytest.mark.parametrize("d", [512, 333])
+def test_one_row_for_all_and_an_input_in_two_places(d):
+    """Rows, residuals and gates broadcast from one row, rows far apart, and x as its own residual and gate."""
+    m = 9
+    g = torch.Generator().manual_seed(9)
+    x, r = (torch.randn(m, d, generator=g).to(torch.bfloat16).to(DEV) for _ in range(2))
+    far = torch.zeros(m, 2 ** 21 + 24, dtype=torch.bfloat16, device=DEV)
+    far[:, 8: 8 + d] = x
+    for kind in (None, "FP8_ROW", "FP8_GROUP128") + (("MXFP8",) if d % 32 == 0 else ()):
+        for a, b in ((x[:1].expand(m, d), r), (x, r[:1].expand(m, d)), (x, x), (far[:, 8: 8 + d], r)):
+            ca, cb = a.contiguous(), b.contiguous().clone()
+            y, h = st.rms_norm(a, residual=b, quantize=kind)
+            z, hz = st.rms_norm(ca, residual=cb, quantize=kind)
+            assert torch.equal(h, hz)
+            pairs = [(y, z)] if kind is None else [(y.data, z.data), (y.scale, z.scale)]
+            if kind is not None:
+                q, p = st.quantize_activation(a, kind, gate=b), st.quantize_activation(ca, kind, gate=cb)
+                pairs += [(q.data, p.data), (q.scale, p.scale)]
+            for s, t in pairs:
+                assert torch.equal(_bits(s), _bits(t))

@@ -174,3 +174,35 @@ def test_inputs_of_any_layout(tmp_path):
         q, p = st.quantize_activation(x, "MXFP8", gate=x), st.quantize_activation(flat, "MXFP8", gate=flat)
         assert torch.equal(q.data.view(torch.uint8), p.data.view(torch.uint8)) and torch.equal(q.scale.view(torch.uint8), p.scale.view(torch.uint8))
     loader.detach()
+
+
+@pytest.mark.parametrize("k", [3, 6])
+def test_a_captured_forward_replays(k, tmp_path):
+    """A resident module's forward captured into a graph, replayed between eager work, new inputs and another module's loads."""
+    sd = st.StreamStateDict(_file(tmp_path, k), DEV)
+    root, lin = _module(k)
+    loader = st.LazyModuleLoader(root, sd, quantized="activations")
+    xs = [torch.randn(5, lin.in_features, generator=torch.Generator().manual_seed(i)).to(torch.bfloat16).to(DEV) for i in range(3)]
+    want = [lin(x) for x in xs]
+    x = xs[0].clone()
+    s = torch.cuda.Stream(DEV)
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        lin(x)
+    torch.cuda.current_stream().wait_stream(s)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        y = lin(x)
+    for i in (0, 1, 2, 1):
+        x.copy_(xs[i])
+        y.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want[i])
+        assert torch.equal(lin(xs[2 - i]), want[2 - i])
+    loader.detach()
+    with pytest.raises(RuntimeError, match="not loaded"):
+        lin(xs[0])
+    loader.materialize(lin)
+    assert torch.equal(lin(xs[0]), torch.nn.functional.linear(xs[0], sd[LINEARS[k][0] + ".weight"]))

@@ -170,3 +170,33 @@ def test_out_beside_its_input_in_one_buffer(m):
     assert torch.equal(buf, before)
     with pytest.raises(ValueError, match="overlaps"):
         st.linear(buf[:, :k], w, out=buf[:, k - 1: k - 1 + n])
+
+
+@pytest.mark.parametrize("xk,wk", DENSE)
+@pytest.mark.parametrize("m", [1, 5, 20, 130])
+def test_rows_far_apart_and_one_row_for_all(xk, wk, m):
+    """Rows of x, residual and out more than 4 MiB apart (past the tiles' 32-bit offsets), and one row read for every row."""
+    n, k = 70, 256
+    x, w = ref.random_rows(st, xk, m, k, 8), ref.to(ref.random_weight(st, wk, n, k, 9), DEV)
+    r = torch.randn(m, n, generator=torch.Generator().manual_seed(10)).to(ref.DT[xk])
+    pitch = 2 ** 21 + 24
+    print(f"far rows {xk} {wk} {m}", flush=True)
+    far = torch.full((m, pitch), 5.0, dtype=ref.DT[xk], device=DEV)
+    far[:, 8: 8 + k], far[:, 1000: 1000 + n] = x.to(DEV), r.to(DEV)
+    want = st.linear(x.to(DEV), w, residual=r.to(DEV))
+    st.linear(far[:, 8: 8 + k], w, residual=far[:, 1000: 1000 + n], out=far[:, 2000: 2000 + n])
+    assert torch.equal(far[:, 2000: 2000 + n], want) and (far[:, 2000 + n:] == 5.0).all() and (far[:, 1000 + n: 2000] == 5.0).all()
+    del far
+    one = st.linear(x[:1].to(DEV).expand(m, k), w, residual=r[:1].to(DEV).expand(m, n))
+    assert torch.equal(one, st.linear(x[:1].repeat(m, 1).to(DEV), w, residual=r[:1].repeat(m, 1).to(DEV)))
+
+
+@pytest.mark.parametrize("m", [1, 9, 100])
+def test_an_input_in_two_places(m):
+    """x as the residual too, and the bias a row of it."""
+    d = 256
+    x, w = ref.random_rows(st, "bf16", m, d, 11), ref.random_weight(st, "MXFP4", d, d, 12)
+    dx = x.to(DEV)
+    got = st.linear(dx, ref.to(w, DEV), bias=dx[0], residual=dx, activation="silu", out_dtype="f32").cpu().double()
+    want, s = ref.linear(x, w, bias=x[0], residual=x, activation="silu")
+    assert ((got - want).abs() <= ref.linear_tolerance(want, s, d, torch.float32)).all()

@@ -157,6 +157,8 @@ def test_a_forward_kept_by_a_wrapper_is_the_modules_own_after_detach():
     lin.forward = lambda t: 2 * inner(t)
     assert torch.equal(lin(x), 2 * ops.linear(x, a["weight"], bias=a["bias"], out_dtype="bf16"))
     loader.detach()
+    with pytest.raises(RuntimeError, match="not loaded"):
+        inner(x)
     loader.materialize(lin)
     assert torch.equal(lin(x), 2 * _decoded(a, x))
 
@@ -244,3 +246,46 @@ def test_inputs_of_any_layout(monkeypatch):
     for x in (_x(64, 5).t(), long.unfold(0, 64, 8), long[::8], long[:64].expand(3, 64), _x(2, 64, 5).transpose(1, 2)):
         for mod in (lin, norm):
             assert torch.equal(mod(x), mod(x.contiguous()))
+
+
+@pytest.mark.parametrize("mode", [None, "weights"])
+def test_a_module_left_without_its_weight_refuses_to_run(mode):
+    """torch computes with a meta weight without a word, and returns memory nobody wrote: a detached module whose weight is not
+    loaded says so instead, until it has one again."""
+    a, b = _checkpoint(1), _checkpoint(2)
+    lin, x = _linear(), _x(5, 64, seed=3)
+    for again in ("by hand", "assigned", "another loader", "another quantized loader"):
+        loader = st.LazyModuleLoader(lin, a, quantized=mode)
+        lin(x)
+        loader.evict_all()
+        loader.detach()
+        for _ in range(2):
+            with pytest.raises(RuntimeError, match="weight.*not loaded"):
+                lin(x)
+        if again == "by hand":
+            loader.materialize(lin)
+            assert torch.equal(lin(x), _decoded(a, x))
+        elif again == "assigned":
+            lin.weight = torch.nn.Parameter(torch.zeros(24, 64, dtype=torch.bfloat16), requires_grad=False)
+            lin.bias = torch.nn.Parameter(a["bias"], requires_grad=False)
+            assert torch.equal(lin(x), a["bias"].expand(5, 24))
+        else:
+            other = st.LazyModuleLoader(lin, b, quantized="weights" if "quantized" in again else None)
+            lin(x)
+            assert len(lin._forward_pre_hooks) == 1
+            other.materialize(lin)
+            other.detach()
+            if other.quantized is None:
+                assert torch.equal(lin(x), _decoded(b, x))
+        if again != "another quantized loader":
+            assert not lin._forward_pre_hooks
+    del lin._forward_pre_hooks[next(iter(lin._forward_pre_hooks))]
+
+
+def test_a_fully_loaded_module_keeps_no_hook_after_detach():
+    a = _checkpoint(1)
+    lin, x = _linear(), _x(5, 64, seed=3)
+    loader = st.LazyModuleLoader(lin, a)
+    lin(x)
+    loader.detach()
+    assert not lin._forward_pre_hooks and torch.equal(lin(x), _decoded(a, x))
