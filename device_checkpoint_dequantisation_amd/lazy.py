@@ -797,6 +797,8 @@ class LazyModuleLoader:
         from . import ops
         if "forward" in mod.__dict__:      # an adapter's
             return None
+        if isinstance(mod, torch.nn.modules.linear.NonDynamicallyQuantizableLinear):      # its owner reads the weight itself
+            return None
         if type(mod).forward is torch.nn.Linear.forward and meta.kind in QUANTIZED_KINDS:
             self._stored[mod] = None
             encode = {w: k for k, ws in ops.PAIRS.items() for w in ws}.get(meta.kind) if self.quantized == "activations" else None

@@ -289,3 +289,20 @@ def test_a_fully_loaded_module_keeps_no_hook_after_detach():
     lin(x)
     loader.detach()
     assert not lin._forward_pre_hooks and torch.equal(lin(x), _decoded(a, x))
+
+
+def test_attention_whose_projection_is_read_by_its_owner():
+    """nn.MultiheadAttention reads its out_proj's weight and never calls that module: it stays a decoded weight."""
+    attn = torch.nn.MultiheadAttention(64, 4, bias=False, batch_first=True, device="meta", dtype=torch.bfloat16)
+    sd = _Memory({"in_proj_weight": _x(192, 64, seed=4), "out_proj.weight": ref.random_weight(st, "FP8_TENSOR", 64, 64, 5)})
+    x = _x(2, 3, 64, seed=6)
+    got = []
+    for mode in (None, "weights", "activations"):
+        loader = st.LazyModuleLoader(attn, sd, quantized=mode)
+        loader.materialize(attn.out_proj)
+        assert not attn.out_proj.weight.is_meta
+        with torch.no_grad():
+            got.append(attn(x, x, x, need_weights=False)[0])
+        loader.evict_all()
+        loader.detach()
+    assert torch.equal(got[0], got[1]) and torch.equal(got[0], got[2]) and got[0].isfinite().all()
