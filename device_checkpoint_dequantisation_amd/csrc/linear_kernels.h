@@ -585,9 +585,9 @@ __global__ __launch_bounds__(64 * F::WAVES) void linear_few(Args a) {
 
 // ------------------------------------------------------------------------- tiles
 
-// What bounds it: 8-bit rows, tiles of 256: the matrix instructions (MXFP8 [12288, 4096] x 8192 rows: 472 us, of which they are busy
+// What bounds it: 8-bit rows, tiles of 256: the matrix instructions (MXFP8 [12288, 4096] x 8192 rows: 476 us, of which they are busy
 // 164; LDS reads take 90, the rest is waiting at the barrier and for LDS at a step's start).  Dense rows, tiles of 128: matrix
-// instructions, decoding and LDS reads count 215, 125 and 220 us of NVFP4 [25600, 5120] x 2048 rows' 546 us and overlap in part.
+// instructions, decoding and LDS reads count 215, 125 and 220 us of NVFP4 [25600, 5120] x 2048 rows' 560-575 us and overlap in part.
 //
 // A tile of BM x BN outputs by WAVES_M x WAVES_N wavefronts; a step of K is 128 bytes of x: 64 elements, or 128
 // of e4m3.  LDS holds rows of 16-byte chunks; chunk c of row r sits at c ^ swizzle(r), so that eight lanes
@@ -1013,7 +1013,7 @@ void launch(const Args& a, const Plan& p, hipStream_t s) {
         if constexpr (is_q(X))
             if (p.f8) launch_tile<Tile<X, WK, 128, 128, 2, 2, true, 2>, false>(a, p, s);
         // Packed fp4 under dense rows: a wavefront takes all rows of the tile, so that each code is decoded once (NVFP4 [25600, 5120]
-        // x 2048 rows: 546 us against 611 with a quadrant each); the 8-bit kinds, cheaper to decode, read less LDS in quadrants.
+        // x 2048 rows: 574 us against 625 with a quadrant each, in turn); the 8-bit kinds, cheaper to decode, read less LDS in quadrants.
         if (!is_q(X) || !p.f8) launch_tile<Tile<X, WK, 128, 128, is_fp4(WK) && !is_q(X) ? 1 : 2, is_fp4(WK) && !is_q(X) ? 4 : 2, false, 2>, false>(a, p, s);
     } else if constexpr (is_q(X)) {
         launch_tile<Tile<X, WK, 256, 256, 2, 4, true, 2>, true>(a, p, s);

@@ -1,4 +1,4 @@
-// Device helpers shared by the kernels that compute on activations (linear.hip, encode.hip).
+// Device helpers shared by the kernels that compute on activations (linear_kernels.h, encode.hip).
 #pragma once
 
 #include <hip/hip_runtime.h>
