@@ -7,17 +7,19 @@
 // the quotient lies on is decided exactly:
 //  * encode without a gate: v, and so amax and s, are exact in fp32.  The fp32 quotient names the middle that is nearest, and the
 //    sign of fma(-middle, s, v), which is exact, says on which side of it v / s lies.
-//  * a gate or a norm: v, amax and the quotient are kept in fp64 (x + residual and the sum of squares too).  For MX, whose scale is a power of two, v
-//    in fp32, good to 2^-21, decides unless it comes within 2^-20 of a middle or amax that near to a power of two's edge;
-//    then the wavefront does its chunk again in fp64 (about one in 100).
+//  * a gate or a norm: v, amax and the quotient are kept in fp64 (x + residual and the sum of squares too).  For MX, whose scale
+//    is a power of two, v in fp32, good to 2^-21, decides unless it comes within 2^-20 of a middle or amax that near to a
+//    power of two's edge; then the wavefront does its chunk again in fp64 (about one in 100).
 // A fp64 quotient is rounded correctly: a middle has 5 bits, s 24 and v 53, so a quotient that is not a middle is not rounded to one.
 // (A gate of 31 makes x * silu(gate) differ from x * gate by 2^-45 of itself: such values do lie that near to middles.)  A norm's own
 // fp64 roundings come to a few 2^-53: its quotients within 2^-49 of a middle count as the middle.
 //
-// Both are bound by memory: every input is read once and stays in registers (chunks of 8 elements per lane, 16-byte
+// Without a gate, and to MXFP8, both are bound by memory: every input is read once and stays in registers (chunks of 8 elements per lane, 16-byte
 // loads) while the row's sums and maxima are taken; groups of 128 and 32 columns are 16 and 4 lanes.  Measured on MI355X: norm of
 // 8192 x 5120 bf16 with residual to MXFP8 68 us (4.3 TB/s), silu-gated 4096 x 25600 bf16 to MXFP8 100-104 us (5.1 TB/s; 143 with
 // expf and an IEEE division, 217 in fp64 throughout), 777 x 12288 fp16 rows to one scale each 16 us (28.6 in fp64).
+// Gates and norms to the other kinds wait for fp64 arithmetic: gated 4096 x 25600 to groups 220-231 us, to one scale per row 276;
+// norm of 8192 x 5120 with residual to groups 83, to one scale per row 81.
 #include <hip/hip_runtime.h>
 
 #include "st_device.h"
@@ -218,7 +220,7 @@ __device__ __forceinline__ void encode_exact(const Args& a, uint64_t row, uint32
     for (int i = 0; i < 8; ++i) amax = __builtin_fmaxf(amax, finite_abs(v[i]));
     const Scale<KIND> s(double(max_over<(KIND == ST_X_MXFP8 ? 4 : 16)>(amax)));
     uint32_t lo, hi;
-    codes_exact(v, KIND == ST_X_MXFP8 ? float(1.0 / s.inv) : as_f32(s.bits), float(s.inv), lo, hi);
+    codes_exact(v, float(s.value()), float(s.inv), lo, hi);
     store_codes<VEC>(a.out + row * a.d, col, a.d, lo, hi);
     store_scale<KIND>(a, row, col, s.bits);
 }

@@ -182,8 +182,8 @@ def linear(x, weight, bias=None, residual=None, activation: str | None = None, o
     [..., N] are bf16, fp16 or fp32; ``activation`` is None, "relu", "silu", "gelu" (erf) or "gelu_tanh".  The result
     has ``out_dtype`` (bf16, f16 or f32; default x's type, bf16 for 8-bit x), or goes to ``out``, which may be
     ``residual`` itself.  The rows of a matrix (and of ``residual``) are read where they are, at any pitch, and have to have
-    adjacent elements; inputs of other shapes are copied where they have not.  The weight's exact values enter (code times scale, not rounded to bf16 first), sums are fp32
-    and the result is rounded once.  The exception: bf16 results of more than 64 8-bit rows come from the scaled matrix
+    adjacent elements; inputs of other shapes are copied where they have not.  The weight's exact values enter (code
+    times scale, not rounded to bf16 first), sums are fp32 and the result is rounded once.  The exception: bf16 results of more than 64 8-bit rows come from the scaled matrix
     instructions, whose sums carry some 16 bits (off by 2e-5 of the results' root mean square on average, a fiftieth of bf16's
     rounding); ``out_dtype`` "f16" or "f32" has fp32 sums."""
     who = "linear"

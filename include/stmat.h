@@ -552,8 +552,9 @@ typedef enum st_activation {
  * and the result is rounded once; only a bf16 result of more than 64 8-bit rows comes from the scaled matrix instructions, which of
  * each 16 neighbouring products cut what is below 2^-13 of the largest (its sums carry some 16 bits: 2e-5 of the results' root
  * mean square on average; ask for an fp16 or fp32 result to have fp32 sums).  The fp32 scales (per tensor, per row, per 128, NVFP4's
- * global one) multiply those sums: a sum of codes that passes fp32's range is infinite whatever its scale.  Pitches are in elements between rows of x, residual and out (the elements of a
- * row are adjacent; a residual pitch of 0 adds one row to every row; ignored for m <= 1).  out may be the
+ * global one) multiply those sums: a sum of x times codes that passes fp32's range is infinite whatever its scale.  Pitches are
+ * in elements between rows of x, residual and out (the elements of a row are adjacent; a pitch of 0 takes one row of x or
+ * residual for every row; ignored for m <= 1).  out may be the
  * residual itself; otherwise out must not overlap an input. */
 typedef struct st_linear_args {
     const void* x;
@@ -578,8 +579,9 @@ typedef struct st_linear_args {
  * output alone is too small to fill the GPU).  Everything but the workspace fields must be set. */
 st_status st_linear_workspace_bytes(const st_linear_args* args, uint64_t* bytes);
 /* Errors: ST_E_ARG (null or misaligned pointers, unknown types, an x type that does not go with the weight kind,
- * too little workspace), ST_E_SHAPE (NVFP4 k % 16, MX k % 32, pitches, size limits; also where m and n take 2^32 threads or more:
- * from n = 2^26 on for one row, 2^27 for up to 16, or 2^24 tiles of 64 x 64 or more outputs), ST_E_HIP (the launch). */
+ * too little workspace), ST_E_SHAPE (NVFP4 k % 16, MX k % 32, pitches, size limits; also where m and n would take
+ * 2^32 threads: n from 2^26 on for one row, from 2^27 on for up to 16, 2^24 tiles of 64 x 64 or more outputs beyond), ST_E_HIP
+ * (the launch). */
 st_status st_linear(const st_linear_args* args, void* stream);
 
 /* Rows x [m, d] (bf16, fp16 or fp32, rows `x_pitch` elements apart) to e4m3 codes [m, d] and scales:
