@@ -605,14 +605,16 @@ __all__ += ["StreamStateDict", "PrefixViewStateDict", "FilterViewStateDict", "Re
             "LazyModuleLoader", "DiskRef", "OutputMeta", "ShardedStateDict", "ShardError", "index_shards",
             "load_checkpoint", "shard_files"]
 
-# Operators on quantised weights (ops.py), imported on first use: they need torch, which the rest of the package imports
+# Operators on quantised data (ops.py, kv_cache.py), imported on first use: they need torch, which the rest of the package imports
 # only where it allocates, and so are not in __all__, whose names a star import fetches at once.
-_OPS = ("QuantizedActivation", "linear", "quantize_activation", "rms_norm")
+_OPS = {"ops": ("QuantizedActivation", "linear", "quantize_activation", "rms_norm"),
+        "kv_cache": ("QuantizedKvCache", "kv_append", "kv_attention")}
 
 
 def __getattr__(name):
-    if name in _OPS:
-        from . import ops
-        value = globals()[name] = getattr(ops, name)
-        return value
+    for module, names in _OPS.items():
+        if name in names:
+            import importlib
+            value = globals()[name] = getattr(importlib.import_module("." + module, __name__), name)
+            return value
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

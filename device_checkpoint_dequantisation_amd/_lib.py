@@ -108,6 +108,21 @@ class RmsNormArgs(C.Structure):
                 [(f, C.c_uint32) for f in ("x_type", "weight_type", "out_type", "kind")])
 
 
+class KvAppendArgs(C.Structure):
+    _fields_ = ([(f, C.c_void_p) for f in ("k_new", "v_new", "k", "v", "k_scale", "v_scale", "table", "lengths", "starts")] +
+                [(f, C.c_uint64) for f in ("pages", "tokens", "seqs", "max_new", "table_blocks", "table_pitch", "k_pitch", "k_head_pitch", "v_pitch",
+                                           "v_head_pitch")] +
+                [(f, C.c_uint32) for f in ("heads", "head_dim", "block", "x_type")])
+
+
+class KvAttentionArgs(C.Structure):
+    _fields_ = ([(f, C.c_void_p) for f in ("q", "out", "k", "v", "k_scale", "v_scale", "table", "lengths", "starts", "workspace")] +
+                [(f, C.c_uint64) for f in ("workspace_bytes", "pages", "tokens", "seqs", "max_new", "table_blocks", "table_pitch", "q_pitch",
+                                           "q_head_pitch", "out_pitch", "out_head_pitch", "window")] + [("scale", C.c_double)] +
+                [(f, C.c_uint32) for f in ("heads", "group", "head_dim", "block", "causal", "q_type")])
+
+
+assert C.sizeof(KvAppendArgs) == 168 and C.sizeof(KvAttentionArgs) == 208
 assert C.sizeof(LinearArgs) == 152 and C.sizeof(EncodeArgs) == 72 and C.sizeof(RmsNormArgs) == 104
 
 # name -> (restype, argtypes); the full list of exported symbols the header declares.
@@ -149,6 +164,9 @@ SIGNATURES = {
     "st_linear": (C.c_int, [C.c_void_p, C.c_void_p]),
     "st_encode": (C.c_int, [C.c_void_p, C.c_void_p]),
     "st_rms_norm": (C.c_int, [C.c_void_p, C.c_void_p]),
+    "st_kv_append": (C.c_int, [C.c_void_p, C.c_void_p]),
+    "st_kv_attention_workspace_bytes": (C.c_int, [C.c_void_p, C.POINTER(C.c_uint64)]),
+    "st_kv_attention": (C.c_int, [C.c_void_p, C.c_void_p]),
     "st_index_out_dtype": (C.c_uint32, [C.c_void_p]),
     "st_stream_plan_build": (C.c_int, [C.c_void_p, C.c_uint64, C.POINTER(C.c_void_p)]),
     "st_stream_plan_select": (C.c_int, [C.c_void_p, C.POINTER(C.c_uint32), C.c_size_t, C.c_uint64, C.c_uint32,

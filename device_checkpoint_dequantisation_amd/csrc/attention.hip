@@ -1,0 +1,531 @@
+// st_kv_attention: attention over pages of e4m3 codes with one power of two for a block of tokens and a head.
+//   s_j = scale * (q . k_j);  o = sum_j e^(s_j - m) v_j / sum_j e^(s_j - m)   over the tokens j a query sees
+// One pass over the tokens with the running maximum m and sum l (in the base-2 exponent: f = scale * log2(e)).
+//
+// Arithmetic.  Key codes are exact in bf16 and fp16, so q meets them as it is, in q's type; the block's power of two multiplies the
+// fp32 score.  The numerators, 2^(s f - m + 6), enter the second product in fp16: m is the largest score until another passes it by 2^8, which
+// leaves them below 2^15 and 30 binades above fp16's smallest step.  Value codes are exact in fp16 too; a block's
+// power of two is taken relative to the largest, 2^E, that the wavefront has met, so that a value is exact unless its block's is 2^15
+// below that (then to 2^-33 of the largest magnitude).  l is summed from the unrounded numerators.  Maxima, sums and results are fp32.
+//
+// Operands come straight from memory to the matrix instructions, no value crosses lanes between the two products.  The first one
+// makes S^T (tokens x queries) from K rows, the second O^T = V^T P^T.  A step has 64 tokens; lane group g (of four) gets scores of tokens
+// 16 g .. 16 g + 15 when row 4 a + i of K tile t is token 16 a + 4 t + i, and those are the tokens whose value codes it loads, 16 adjacent bytes
+// of a V^T row.
+//
+// Rows: the queries of a sequence that read one cache head, (token, query head) in turn; 16 rows are the columns of one instruction.
+#include <hip/hip_runtime.h>
+
+#include "kv_cache.h"
+
+namespace {
+
+using namespace st_kv;
+
+static_assert(sizeof(st_kv_attention_args) == 208, "the ctypes declaration has this size");
+
+constexpr int kWaves = 4, kThreads = 64 * kWaves, kStep = 64;
+
+struct Args {
+    Seqs s;
+    const uint8_t *q, *k, *v, *ks, *vs;
+    uint8_t* out;
+    float* part;                  // [tokens * query heads][splits][D] unfinished results, or null
+    float2* stat;                 // [tokens * query heads][splits] their m and l
+    uint64_t q_pitch, q_head_pitch, out_pitch, out_head_pitch;
+    uint32_t group, causal, window;
+    uint32_t tiles, splits, chunk;   // row tiles of a head, parts of the tokens, steps of a part
+    float f;                      // scale * log2(e)
+};
+
+constexpr float kNone = -__builtin_inff();
+constexpr float kOffset = 6.0f, kSlack = 8.0f;
+
+// The tokens [lo, hi) that row r of a sequence's head sees.
+struct Sees {
+    int32_t lo, hi;
+};
+__device__ __forceinline__ Sees sees(const Args& a, const Span& p, uint32_t row) {
+    Sees s = {0, p.len};
+    if (a.causal) {
+        const int32_t pos = p.pos + int32_t(row / a.group);
+        if (pos < p.len) s.hi = pos + 1 < 0 ? 0 : pos + 1;
+        if (a.window && pos >= int32_t(a.window)) s.lo = pos - int32_t(a.window) + 1;
+    }
+    return s;
+}
+// Steps [first, last) that rows row0 .. rows - 1 of a tile need; both ends grow with the row.
+struct Steps {
+    int32_t first, last;
+};
+__device__ __forceinline__ Steps steps_of(const Args& a, const Span& p, uint32_t row0, uint32_t end) {
+    const int32_t lo = sees(a, p, row0).lo, hi = sees(a, p, end - 1).hi;
+    return hi > lo ? Steps{lo / kStep, (hi + kStep - 1) / kStep} : Steps{0, 0};
+}
+
+__device__ __forceinline__ float max_over_groups(float v) {
+    v = fmaxf(v, __shfl_xor(v, 16));
+    return fmaxf(v, __shfl_xor(v, 32));
+}
+__device__ __forceinline__ float sum_over_groups(float v) {
+    v += __shfl_xor(v, 16);
+    return v + __shfl_xor(v, 32);
+}
+
+// Bytes of c that are a NaN code (0x7F, 0xFF) as 0xFF.
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t c) {
+    const uint32_t z = ~(c & 0x7F7F7F7Fu) & 0x7F7F7F7Fu;           // 0 where the code is NaN
+    const uint32_t t = (z + 0x7F7F7F7Fu) & 0x80808080u;            // 0x80 where it is not
+    return ((t ^ 0x80808080u) >> 7) * 0xFFu;
+}
+
+// What a wavefront knows of its 16 * QT rows.
+template <bool F16, int D, int QT>
+struct Wave {
+    static constexpr int KL = D / 64;      // 16-byte loads of a K row per lane
+    static constexpr int DT = D / 16;      // 16-column tiles of a result
+    u32x4 q[QT][D / 32];
+    float m[QT], l[QT];
+    f32x4 o[QT][DT];
+    int32_t lo[QT], hi[QT];
+    int32_t e = -1;                        // E + 127, -1: no values yet
+    int32_t all_lo, all_hi;                // tokens that every row sees
+
+    __device__ __forceinline__ void start(const Args& a, const Span& p, uint32_t head, uint32_t row0, uint32_t rows) {
+        const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+#pragma unroll
+        for (int j = 0; j < QT; ++j) {
+            const uint32_t row = row0 + 16 * j + r;
+            const bool have = row < rows;
+            const Sees s = sees(a, p, have ? row : rows - 1);
+            lo[j] = s.lo, hi[j] = s.hi;
+            const uint32_t t = row / a.group, h = head * a.group + row % a.group;
+            const uint8_t* pq = a.q + ((uint64_t(p.first) + (have ? t : 0)) * a.q_pitch + (have ? h : 0) * a.q_head_pitch + D / 4 * g) * 2;
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) q[j][c] = have ? u32x4(*reinterpret_cast<const u32x4_any*>(pq + 16 * c)) : u32x4{0, 0, 0, 0};
+            m[j] = kNone, l[j] = 0.0f;
+#pragma unroll
+            for (int d = 0; d < DT; ++d) o[j][d] = f32x4{0, 0, 0, 0};
+        }
+        const uint32_t last = row0 + 16 * QT < rows ? row0 + 16 * QT : rows;
+        all_lo = sees(a, p, last - 1).lo, all_hi = sees(a, p, row0).hi;
+    }
+
+    // One step of tokens from t0.  k, v: its codes as loaded; ks, vs: the scale codes of lane group g's tokens; known: they lie on a
+    // page.
+    __device__ __forceinline__ void step(const Args& a, int32_t t0, const u32x4 (&k)[4][KL], const u32x4 (&v)[DT], uint32_t ks,
+                                         uint32_t vs, bool known) {
+        const int lane = threadIdx.x & 63, g = lane >> 4;
+        f32x4 s[QT][4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+#pragma unroll
+            for (int j = 0; j < QT; ++j) s[j][t] = f32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int i = 0; i < KL; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const u32x4 kv = codes8<F16, ST_KIND_FP8_TENSOR>(k[t][i][2 * h], k[t][i][2 * h + 1], 1.0f);
+#pragma unroll
+                    for (int j = 0; j < QT; ++j) s[j][t] = mfma32<F16>(kv, q[j][2 * i + h], s[j][t]);
+                }
+        }
+        const float f = power_of(ks) * a.f;
+        const bool inside = t0 >= all_lo && t0 + kStep <= all_hi && __all(known);     // every row sees every token
+        const int32_t at = t0 + 16 * g;
+        u32x4 p[QT][2];
+#pragma unroll
+        for (int j = 0; j < QT; ++j) {
+            float mx = kNone;
+            if (inside) {
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) mx = fmaxf(mx, s[j][t][i]);
+                mx *= f;
+            } else {
+                const uint32_t from = uint32_t(at - lo[j]), count = known && hi[j] > lo[j] ? uint32_t(hi[j] - lo[j]) : 0;
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        s[j][t][i] = from + (4 * t + i) < count ? s[j][t][i] * f : kNone;
+                        mx = fmaxf(mx, s[j][t][i]);
+                    }
+            }
+            mx = max_over_groups(mx);
+            if (__any(mx > m[j] + kSlack)) {
+                const float now = fmaxf(m[j], mx), keep = now == kNone ? 1.0f : __builtin_amdgcn_exp2f(m[j] - now);
+                m[j] = now;
+                l[j] *= keep;
+#pragma unroll
+                for (int d = 0; d < DT; ++d) o[j][d] *= keep;
+            }
+            const float base = kOffset - (m[j] == kNone ? 0.0f : m[j]), fj = inside ? f : 1.0f;
+            float sum = 0.0f;
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                float x[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    x[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j][t][i], fj, base));
+                    sum += x[i];
+                }
+                p[j][t >> 1][2 * (t & 1)] = cvt_f16x2(x[0], x[1]);
+                p[j][t >> 1][2 * (t & 1) + 1] = cvt_f16x2(x[2], x[3]);
+            }
+            l[j] += sum;
+        }
+        // the largest power of two so far
+        int32_t now = known ? int32_t(vs == 255 ? 0 : vs) : -1;
+        now = now > e ? now : e;
+        if (__any(now > e)) {
+            int32_t o1 = __shfl_xor(now, 16);
+            now = now > o1 ? now : o1;
+            o1 = __shfl_xor(now, 32);
+            now = now > o1 ? now : o1;
+            now = __builtin_amdgcn_readfirstlane(now);
+            if (e >= 0) {
+#pragma unroll
+                for (int j = 0; j < QT; ++j)
+#pragma unroll
+                    for (int d = 0; d < DT; ++d)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) o[j][d][i] = __builtin_amdgcn_ldexpf(o[j][d][i], e - now);
+            }
+            e = now;
+        }
+        const int32_t by = int32_t(vs) - e + 127;
+        const float vf = as_f32(vs == 255 ? 0x7F800000u : uint32_t(by < 0 ? 0 : by) << 23);
+        if (inside) {
+#pragma unroll
+            for (int d = 0; d < DT; ++d) {
+                const u32x4 v0 = codes8<true, ST_KIND_FP8_TENSOR>(v[d][0], v[d][1], vf), v1 = codes8<true, ST_KIND_FP8_TENSOR>(v[d][2], v[d][3], vf);
+#pragma unroll
+                for (int j = 0; j < QT; ++j) o[j][d] = mfma32<true>(v1, p[j][1], mfma32<true>(v0, p[j][0], o[j][d]));
+            }
+        } else {
+            // Tokens that some rows do not see may hold anything: NaN codes are taken out, and put NaN into the rows that see them.
+            const float vm = vs == 255 ? 1.0f : vf;
+#pragma unroll
+            for (int d = 0; d < DT; ++d) {
+                u32x4 c = v[d], bad;
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    bad[w] = vs == 255 ? 0xFFFFFFFFu : nan_bytes(c[w]);
+                    c[w] &= ~bad[w];
+                }
+                const u32x4 v0 = codes8<true, ST_KIND_FP8_TENSOR>(c[0], c[1], vm), v1 = codes8<true, ST_KIND_FP8_TENSOR>(c[2], c[3], vm);
+#pragma unroll
+                for (int j = 0; j < QT; ++j) o[j][d] = mfma32<true>(v1, p[j][1], mfma32<true>(v0, p[j][0], o[j][d]));
+                if (__any((bad[0] | bad[1] | bad[2] | bad[3]) != 0)) {
+                    // the code of 1 (0x38) where there was NaN, times 1 where the row sees the token
+                    const u32x4 b0 = codes8<true, ST_KIND_FP8_TENSOR>(bad[0] & 0x38383838u, bad[1] & 0x38383838u, 1.0f);
+                    const u32x4 b1 = codes8<true, ST_KIND_FP8_TENSOR>(bad[2] & 0x38383838u, bad[3] & 0x38383838u, 1.0f);
+#pragma unroll
+                    for (int j = 0; j < QT; ++j) {
+                        const uint32_t from = uint32_t(at - lo[j]), count = known && hi[j] > lo[j] ? uint32_t(hi[j] - lo[j]) : 0;
+                        u32x4 y[2];
+#pragma unroll
+                        for (int t = 0; t < 8; ++t)
+                            y[t >> 2][t & 3] = (from + 2 * t < count ? 0x3C00u : 0u) | (from + 2 * t + 1 < count ? 0x3C000000u : 0u);
+                        const f32x4 hit = mfma32<true>(b1, y[1], mfma32<true>(b0, y[0], f32x4{0, 0, 0, 0}));
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (hit[i] > 0.0f) o[j][d][i] = __builtin_nanf("");
+                    }
+                }
+            }
+        }
+    }
+};
+
+// Four consecutive results of one row to the output.
+template <bool F16>
+__device__ __forceinline__ void store_row4(const Args& a, uint64_t i, const float* v) {
+    const uint32_t lo = F16 ? cvt_f16x2(v[0], v[1]) : cvt_bf16x2(v[0], v[1]), hi = F16 ? cvt_f16x2(v[2], v[3]) : cvt_bf16x2(v[2], v[3]);
+    *reinterpret_cast<u64_any*>(a.out + i * 2) = uint64_t(hi) << 32 | lo;
+}
+
+// The wavefronts of a workgroup take the steps of one row tile in turn and join in LDS, in their order.
+template <bool F16, int D, int QT>
+__global__ __launch_bounds__(kThreads, D * QT <= 128 ? 2 : 1) void attend(Args a) {
+    using W = Wave<F16, D, QT>;
+    constexpr int ROWS = 16 * QT, PITCH = D + 4;
+    __shared__ __align__(16) float sum[ROWS][PITCH];
+    __shared__ float top[kWaves][ROWS], den[kWaves][ROWS];
+    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    uint32_t b = blockIdx.x;
+    const uint32_t split = b % a.splits;
+    b /= a.splits;
+    const uint32_t tile = b % a.tiles;
+    b /= a.tiles;
+    const uint32_t head = b % a.s.heads, seq = b / a.s.heads;
+    const Span p = span_of(a.s, seq);
+    const uint32_t rows = uint32_t(p.count) * a.group, row0 = tile * ROWS;
+    if (row0 >= rows) return;
+    const uint32_t end = row0 + ROWS < rows ? row0 + ROWS : rows;
+    Steps st = steps_of(a, p, row0, end);
+    if (a.splits > 1) {
+        st.first += int32_t(split * a.chunk);
+        if (st.first >= st.last) return;
+        st.last = st.first + int32_t(a.chunk) < st.last ? st.first + int32_t(a.chunk) : st.last;
+    }
+    W w;
+    w.start(a, p, head, row0, rows);
+
+    const uint32_t bl = a.s.block_log2, block = 1u << bl;
+    const uint64_t page_bytes = uint64_t(block) * D;
+    u32x4 k[4][W::KL], v[W::DT];
+    uint32_t ks = 0, vs = 0;
+    bool known = false;
+    // the pages of step i's tokens: of the K rows this lane loads, and of its group's
+    auto pages = [&](int32_t i, int32_t& pk, int32_t& pv) {
+        pk = page_of(a.s, seq, (int64_t(i) * kStep + 16 * (r >> 2)) >> bl);
+        pv = page_of(a.s, seq, (int64_t(i) * kStep + 16 * g) >> bl);
+    };
+    auto load_k = [&](int32_t i, int32_t pk) {
+        const uint64_t at = (uint64_t(pk < 0 ? 0 : pk) * a.s.heads + head) * page_bytes;
+        const uint8_t* base = a.k + at + uint64_t(((i * kStep + 16 * (r >> 2)) & (block - 1)) + (r & 3)) * D + D / 4 * g;
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int h = 0; h < W::KL; ++h) k[t][h] = *reinterpret_cast<const u32x4*>(base + t * 4 * D + 16 * h);
+    };
+    auto load_v = [&](int32_t i, int32_t pv) {
+        const uint64_t at = uint64_t(pv < 0 ? 0 : pv) * a.s.heads + head;
+        const uint8_t* base = a.v + at * page_bytes + uint64_t(r) * block + ((i * kStep + 16 * g) & (block - 1));
+#pragma unroll
+        for (int d = 0; d < W::DT; ++d) v[d] = *reinterpret_cast<const u32x4*>(base + uint64_t(d * 16) * block);
+        known = pv >= 0;
+        ks = known ? a.ks[at] : 0, vs = known ? a.vs[at] : 0;
+    };
+    int32_t i = st.first + wave, pk, pv;
+    if (i < st.last) {
+        pages(i, pk, pv);
+        load_k(i, pk);
+        load_v(i, pv);
+        for (; i < st.last; i += kWaves) {
+            w.step(a, i * kStep, k, v, ks, vs, known);
+            if (i + kWaves < st.last) {
+                pages(i + kWaves, pk, pv);
+                load_k(i + kWaves, pk);
+                load_v(i + kWaves, pv);
+            }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < QT; ++j) {
+        w.l[j] = sum_over_groups(w.l[j]);
+        if (g == 0) top[wave][16 * j + r] = w.m[j], den[wave][16 * j + r] = w.l[j];
+    }
+    __syncthreads();
+    float m[QT];
+#pragma unroll
+    for (int j = 0; j < QT; ++j) {
+        m[j] = kNone;
+#pragma unroll
+        for (int o = 0; o < kWaves; ++o) m[j] = fmaxf(m[j], top[o][16 * j + r]);
+        const float keep = w.m[j] == kNone ? 1.0f : __builtin_amdgcn_exp2f(w.m[j] - m[j]);
+#pragma unroll
+        for (int d = 0; d < W::DT; ++d)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) w.o[j][d][x] = __builtin_amdgcn_ldexpf(w.o[j][d][x] * keep, w.e < 0 ? 0 : w.e - 127);
+    }
+#pragma unroll
+    for (int o = 0; o < kWaves; ++o) {
+        if (wave == o) {
+#pragma unroll
+            for (int j = 0; j < QT; ++j)
+#pragma unroll
+                for (int d = 0; d < W::DT; ++d) {
+                    f32x4* at = reinterpret_cast<f32x4*>(&sum[16 * j + r][16 * d + 4 * g]);
+                    *at = o == 0 ? w.o[j][d] : *at + w.o[j][d];
+                }
+        }
+        __syncthreads();
+    }
+    for (uint32_t i4 = threadIdx.x; i4 < (end - row0) * (D / 4); i4 += kThreads) {
+        const uint32_t rr = i4 / (D / 4), d = i4 % (D / 4) * 4, row = row0 + rr;
+        float t = kNone, l = 0.0f;
+#pragma unroll
+        for (int o = 0; o < kWaves; ++o) t = fmaxf(t, top[o][rr]);
+#pragma unroll
+        for (int o = 0; o < kWaves; ++o) l += top[o][rr] == kNone ? den[o][rr] : den[o][rr] * __builtin_amdgcn_exp2f(top[o][rr] - t);
+        f32x4 x = *reinterpret_cast<const f32x4*>(&sum[rr][d]);
+        const uint64_t tok = uint64_t(p.first) + row / a.group, h = head * a.group + row % a.group;
+        if (a.splits > 1) {
+            const uint64_t at = (tok * a.s.heads * a.group + h) * a.splits + split;
+            *reinterpret_cast<f32x4*>(a.part + at * D + d) = x;
+            if (d == 0) a.stat[at] = float2{t, l};
+        } else {
+            float y[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) y[c] = l == 0.0f ? 0.0f : x[c] / l;
+            store_row4<F16>(a, tok * a.out_pitch + h * a.out_head_pitch + d, y);
+        }
+    }
+}
+
+// The parts of each row, in their order; D / 4 lanes have a row.
+template <bool F16, int D, int ROWS>
+__global__ __launch_bounds__(kThreads) void join(Args a) {
+    constexpr uint32_t LANES = D / 4;
+    const uint32_t heads = a.s.heads * a.group, seq = blockIdx.y;
+    const Span p = span_of(a.s, seq);
+    const uint64_t i = uint64_t(blockIdx.x) * (kThreads / LANES) + threadIdx.x / LANES;
+    if (i >= uint64_t(p.count) * heads) return;
+    const uint32_t t = uint32_t(i / heads), h = uint32_t(i % heads), d = threadIdx.x % LANES * 4;
+    const uint32_t rows = uint32_t(p.count) * a.group, row = t * a.group + h % a.group, row0 = row / ROWS * ROWS;
+    const Steps st = steps_of(a, p, row0, row0 + ROWS < rows ? row0 + ROWS : rows);
+    const uint32_t parts = (uint32_t(st.last - st.first) + a.chunk - 1) / a.chunk;
+    const uint64_t at = ((uint64_t(p.first) + t) * heads + h) * a.splits;
+    float m = kNone, l = 0.0f;
+    for (uint32_t o = 0; o < parts; ++o) m = fmaxf(m, a.stat[at + o].x);
+    f32x4 x = {0, 0, 0, 0};
+    for (uint32_t o = 0; o < parts; ++o) {
+        const float2 s = a.stat[at + o];
+        const float keep = s.x == kNone ? 1.0f : __builtin_amdgcn_exp2f(s.x - m);
+        l += s.y * keep;
+        x += *reinterpret_cast<const f32x4*>(a.part + (at + o) * D + d) * keep;
+    }
+    float y[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) y[c] = l == 0.0f ? 0.0f : x[c] / l;
+    store_row4<F16>(a, (uint64_t(p.first) + t) * a.out_pitch + uint64_t(h) * a.out_head_pitch + d, y);
+}
+
+// ------------------------------------------------------------------------- host
+
+const char* kWho = "st_kv_attention";
+
+bool off(const void* p, uint64_t n) { return reinterpret_cast<uintptr_t>(p) % n != 0; }
+
+struct Plan {
+    uint64_t rows;               // of a sequence's head, at most
+    uint32_t qt, tiles, splits, chunk;
+    uint64_t part_bytes, stat_bytes;
+};
+
+st_status check_args(const st_kv_attention_args* g) {
+    if (!g) return st_fail(ST_E_ARG, "%s: null arguments", kWho);
+    if (g->q_type > ST_OUT_F16) return st_fail(ST_E_ARG, "%s: q type %u is not bf16 or fp16", kWho, g->q_type);
+    if (!(g->scale > 0.0 && g->scale < 1e30)) return st_fail(ST_E_ARG, "%s: scale %g is not positive", kWho, g->scale);
+    if (g->causal > 1) return st_fail(ST_E_ARG, "%s: causal is %u", kWho, g->causal);
+    if (g->window && !g->causal) return st_fail(ST_E_ARG, "%s: a window needs causal attention", kWho);
+    if (g->head_dim != 64 && g->head_dim != 128 && g->head_dim != 256)
+        return st_fail(ST_E_SHAPE, "%s: head_dim %u is not 64, 128 or 256", kWho, g->head_dim);
+    if (g->block != 16 && g->block != 32 && g->block != 64 && g->block != 128)
+        return st_fail(ST_E_SHAPE, "%s: block %u is not 16, 32, 64 or 128", kWho, g->block);
+    const uint64_t lim = uint64_t(1) << 31;
+    if (g->tokens >= lim || g->max_new >= lim || g->pages >= lim || g->table_blocks >= lim / 2 / g->block || g->seqs > 65535 ||
+        g->heads > 65535 || g->group > 65535)
+        return st_fail(ST_E_SHAPE, "%s: %llu tokens, %llu sequences, %u heads of %u, %llu pages or %llu blocks a sequence are too many",
+                       kWho, (unsigned long long)g->tokens, (unsigned long long)g->seqs, g->heads, g->group,
+                       (unsigned long long)g->pages, (unsigned long long)g->table_blocks);
+    if (g->tokens == 0 || g->seqs == 0 || g->heads == 0 || g->group == 0) return ST_OK;
+    if (!g->starts && g->tokens % g->seqs)
+        return st_fail(ST_E_SHAPE, "%s: %llu tokens are not %llu equal parts", kWho, (unsigned long long)g->tokens, (unsigned long long)g->seqs);
+    if (g->pages == 0 || g->table_blocks == 0) return st_fail(ST_E_SHAPE, "%s: a cache without pages", kWho);
+    if (!g->q || !g->out || !g->k || !g->v || !g->k_scale || !g->v_scale || !g->table || !g->lengths)
+        return st_fail(ST_E_ARG, "%s: null pointer", kWho);
+    if (g->seqs > 1 && g->table_pitch < g->table_blocks) return st_fail(ST_E_SHAPE, "%s: the table's pitch is shorter than its row", kWho);
+    if (off(g->q, 2) || off(g->out, 2)) return st_fail(ST_E_ARG, "%s: a pointer is not aligned to its element type", kWho);
+    if (off(g->k, 16) || off(g->v, 16)) return st_fail(ST_E_ARG, "%s: the cache is not 16-byte aligned", kWho);
+    if (off(g->table, 4) || off(g->lengths, 4) || off(g->starts, 4)) return st_fail(ST_E_ARG, "%s: a table is not 4-byte aligned", kWho);
+    return ST_OK;
+}
+
+st_status plan_of(const st_kv_attention_args& g, Plan* p) {
+    *p = Plan{};
+    uint64_t count = g.max_new < g.tokens ? g.max_new : g.tokens;
+    if (!g.starts && g.tokens / g.seqs < count) count = g.tokens / g.seqs;
+    p->rows = count * g.group;
+    if (p->rows == 0) return ST_OK;
+    if (p->rows >= uint64_t(1) << 31) return st_fail(ST_E_SHAPE, "%s: %llu queries of a head are too many", kWho, (unsigned long long)p->rows);
+    p->qt = p->rows <= 16 ? 1 : 2;
+    const uint64_t tiles = (p->rows + 16 * p->qt - 1) / (16 * p->qt);
+    const uint64_t groups = tiles * g.seqs * g.heads;
+    // steps that a row tile can have
+    uint64_t tokens = g.table_blocks * g.block;
+    if (g.window && g.window + 16 * p->qt + 2 * kStep < tokens) tokens = g.window + 16 * p->qt + 2 * kStep;
+    const uint64_t steps = (tokens + kStep - 1) / kStep;
+    // Parts of equal length, about eight workgroups a CU, each with four steps for each of its wavefronts at least
+    uint64_t chunk = (groups * steps + 2047) / 2048;
+    chunk = (chunk + kWaves - 1) / kWaves * kWaves;
+    if (chunk < 16) chunk = 16;
+    uint64_t splits = (steps + chunk - 1) / chunk;
+    if (groups >= 2048) splits = 1;
+    if (groups * splits >= uint64_t(1) << 24)
+        return st_fail(ST_E_SHAPE, "%s: %llu workgroups are too many for one launch", kWho, (unsigned long long)(groups * splits));
+    p->tiles = uint32_t(tiles), p->splits = uint32_t(splits), p->chunk = uint32_t(chunk);
+    if (splits > 1) {
+        const uint64_t n = g.tokens * g.heads * g.group * splits;
+        p->part_bytes = n * g.head_dim * 4, p->stat_bytes = n * 8;
+    }
+    return ST_OK;
+}
+
+template <bool F16, int D>
+void launch(const Args& a, const Plan& p, hipStream_t s) {
+    const dim3 grid(p.tiles * a.s.heads * a.s.seqs * p.splits);
+    if (p.qt == 1) hipLaunchKernelGGL((attend<F16, D, 1>), grid, dim3(kThreads), 0, s, a);
+    else hipLaunchKernelGGL((attend<F16, D, 2>), grid, dim3(kThreads), 0, s, a);
+    if (p.splits > 1) {
+        const uint64_t items = p.rows * a.s.heads, per = kThreads / (D / 4);
+        const dim3 jgrid(uint32_t((items + per - 1) / per), a.s.seqs);
+        if (p.qt == 1) hipLaunchKernelGGL((join<F16, D, 16>), jgrid, dim3(kThreads), 0, s, a);
+        else hipLaunchKernelGGL((join<F16, D, 32>), jgrid, dim3(kThreads), 0, s, a);
+    }
+}
+
+}  // namespace
+
+extern "C" st_status st_kv_attention_workspace_bytes(const st_kv_attention_args* g, uint64_t* bytes) {
+    if (!bytes) return st_fail(ST_E_ARG, "st_kv_attention_workspace_bytes: null bytes");
+    *bytes = 0;
+    const st_status r = check_args(g);
+    if (r != ST_OK || g->tokens == 0 || g->seqs == 0 || g->heads == 0 || g->group == 0) return r;
+    Plan p;
+    const st_status f = plan_of(*g, &p);
+    if (f == ST_OK) *bytes = p.part_bytes + p.stat_bytes;
+    return f;
+}
+
+extern "C" st_status st_kv_attention(const st_kv_attention_args* g, void* stream) {
+    const st_status r = check_args(g);
+    if (r != ST_OK || g->tokens == 0 || g->seqs == 0 || g->heads == 0 || g->group == 0) return r;
+    Plan p;
+    const st_status f = plan_of(*g, &p);
+    if (f != ST_OK || p.rows == 0) return f;
+    const uint64_t need = p.part_bytes + p.stat_bytes;
+    if (need) {
+        if (!g->workspace || g->workspace_bytes < need)
+            return st_fail(ST_E_ARG, "%s: %llu bytes of workspace, %llu are needed", kWho,
+                           (unsigned long long)(g->workspace ? g->workspace_bytes : 0), (unsigned long long)need);
+        if (off(g->workspace, 16)) return st_fail(ST_E_ARG, "%s: workspace is not 16-byte aligned", kWho);
+    }
+    Args a = {};
+    a.s = Seqs{g->table, g->lengths, g->starts, g->pages, g->table_blocks, g->table_pitch, uint32_t(g->tokens), uint32_t(g->seqs),
+               uint32_t(g->max_new < g->tokens ? g->max_new : g->tokens), g->heads, stk::ilog2(g->block)};
+    auto b = [](const void* v) { return static_cast<const uint8_t*>(v); };
+    a.q = b(g->q); a.k = b(g->k); a.v = b(g->v); a.ks = b(g->k_scale); a.vs = b(g->v_scale);
+    a.out = static_cast<uint8_t*>(g->out);
+    if (need) {
+        a.part = static_cast<float*>(g->workspace);
+        a.stat = reinterpret_cast<float2*>(static_cast<uint8_t*>(g->workspace) + p.part_bytes);
+    }
+    a.q_pitch = g->q_pitch; a.q_head_pitch = g->q_head_pitch; a.out_pitch = g->out_pitch; a.out_head_pitch = g->out_head_pitch;
+    a.group = g->group; a.causal = g->causal;
+    a.window = uint32_t(g->window < (uint64_t(1) << 31) - 1 ? g->window : 0);      // as long as any sequence: all
+    a.tiles = p.tiles; a.splits = p.splits; a.chunk = p.chunk;
+    a.f = float(g->scale * 1.4426950408889634);
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    const bool h = g->q_type == ST_OUT_F16;
+    if (g->head_dim == 64) h ? launch<true, 64>(a, p, s) : launch<false, 64>(a, p, s);
+    else if (g->head_dim == 128) h ? launch<true, 128>(a, p, s) : launch<false, 128>(a, p, s);
+    else h ? launch<true, 256>(a, p, s) : launch<false, 256>(a, p, s);
+    const hipError_t e = hipGetLastError();
+    return e == hipSuccess ? ST_OK : st_fail(ST_E_HIP, "%s: launch failed: %s", kWho, hipGetErrorString(e));
+}

@@ -629,6 +629,70 @@ st_status st_rms_norm(const st_rms_norm_args* args, void* stream);
 /* Errors of both: ST_E_ARG (null or misaligned pointers, unknown types or kind, eps), ST_E_SHAPE (MX d % 32,
  * pitches, size limits), ST_E_HIP (the launch). */
 
+/* ---- A cache of keys and values in 8 bits ----------------------------------------------------------
+ * Keys and values of earlier tokens (the serving backend's KV cache of "Resident Modal LLM Architecture",
+ * "Current Backend Boundary", in 8 bits instead of bf16), in pages of `block` tokens:
+ *   k        e4m3 [pages, heads, block, head_dim]
+ *   v        e4m3 [pages, heads, head_dim, block]   (a head's tokens are adjacent: the second product's operand)
+ *   k_scale, v_scale   E8M0 [pages, heads]          one power of two for a block of tokens and a head
+ * A value is code * scale.  table [seqs, table_blocks] (rows table_pitch apart) names the page of each block of a sequence's tokens, lengths [seqs]
+ * its tokens, the new ones of this call among them.  New tokens (and queries) of all sequences lie one after the other in
+ * [tokens, ...]: those of sequence s are rows starts[s] .. starts[s + 1] - 1, or, where starts is NULL, the s-th of `seqs` equal
+ * parts; they are the last ones of their sequence.  max_new is at least the most new tokens of a sequence (those behind it
+ * are left out).  table, lengths and starts are read on the device and may change between replays of a captured graph.
+ * Entries that name no page, lengths past the table and rows past `tokens` are never followed: a token on no page is not written
+ * and not attended to. */
+typedef struct st_kv_append_args {
+    const void* k_new;       /* [tokens, heads, head_dim] of x_type, head_dim adjacent */
+    const void* v_new;
+    void* k;
+    void* v;
+    void* k_scale;
+    void* v_scale;
+    const int32_t* table;
+    const int32_t* lengths;
+    const int32_t* starts;   /* [seqs + 1] or NULL */
+    uint64_t pages, tokens, seqs, max_new, table_blocks, table_pitch;
+    uint64_t k_pitch, k_head_pitch, v_pitch, v_head_pitch;   /* elements between tokens and between heads */
+    uint32_t heads, head_dim, block;
+    uint32_t x_type;         /* st_out_dtype */
+} st_kv_append_args;
+/* Write the new tokens.  The scale of a block of tokens and a head is the smallest power of two >= amax / 448 over its finite
+ * values (2^-127 where there is none); a block that already has tokens keeps its scale where that is larger, and where it is not
+ * their codes are rounded to the new one (exact above e4m3's subnormals).  A value that is not finite becomes the NaN code and does
+ * not enter amax.  Tokens of a block behind the sequence's last are left as they are.  No page may be the last one of two sequences.
+ * head_dim: a multiple of 32 up to 256; block: 16, 32, 64 or 128. */
+st_status st_kv_append(const st_kv_append_args* args, void* stream);
+
+typedef struct st_kv_attention_args {
+    const void* q;           /* [tokens, heads * group, head_dim] of q_type; query head h reads cache head h / group */
+    void* out;               /* [tokens, heads * group, head_dim] of q_type */
+    const void* k;
+    const void* v;
+    const void* k_scale;
+    const void* v_scale;
+    const int32_t* table;
+    const int32_t* lengths;
+    const int32_t* starts;
+    void* workspace;         /* st_kv_attention_workspace_bytes bytes, 16-byte aligned, this call's own until it is done */
+    uint64_t workspace_bytes;
+    uint64_t pages, tokens, seqs, max_new, table_blocks, table_pitch;
+    uint64_t q_pitch, q_head_pitch, out_pitch, out_head_pitch;
+    uint64_t window;         /* causal: a query sees this many tokens, itself the last; 0: all */
+    double scale;            /* of the scores, > 0 */
+    uint32_t heads, group, head_dim, block;
+    uint32_t causal;         /* 1: a query sees tokens up to its own; 0: all of its sequence */
+    uint32_t q_type;         /* ST_OUT_BF16 or ST_OUT_F16 */
+} st_kv_attention_args;
+/* out = softmax(scale * q k^T) v over the tokens a query sees; 0 where it sees none.  Scores, maxima, sums and results are kept in
+ * fp32; the softmax's numerators are rounded to fp16 (11 bits) as they meet the values.  Tokens a query does not see have no part in its result,
+ * NaN codes among them.  Rows of `out` that belong to no sequence are left as they are.
+ * head_dim: 64, 128 or 256; block: 16, 32, 64 or 128. */
+st_status st_kv_attention_workspace_bytes(const st_kv_attention_args* args, uint64_t* bytes);
+st_status st_kv_attention(const st_kv_attention_args* args, void* stream);
+/* Errors of these: ST_E_ARG (null or misaligned pointers, unknown types, scale, too little workspace), ST_E_SHAPE (head_dim, block,
+ * pitches, size limits), ST_E_HIP (the launch). */
+
 #ifdef __cplusplus
 }
 #endif
