@@ -605,9 +605,10 @@ __all__ += ["StreamStateDict", "PrefixViewStateDict", "FilterViewStateDict", "Re
             "LazyModuleLoader", "DiskRef", "OutputMeta", "ShardedStateDict", "ShardError", "index_shards",
             "load_checkpoint", "shard_files"]
 
-# Operators on quantised data (ops.py, kv_cache.py), imported on first use: they need torch, which the rest of the package imports
+# Operators on quantised data (ops.py, experts.py, kv_cache.py), imported on first use: they need torch, which the rest of the package imports
 # only where it allocates, and so are not in __all__, whose names a star import fetches at once.
 _OPS = {"ops": ("QuantizedActivation", "linear", "quantize_activation", "rms_norm"),
+        "experts": ("MoeExperts", "moe_route", "moe"),
         "kv_cache": ("QuantizedKvCache", "kv_append", "kv_attention")}
 
 

@@ -122,6 +122,20 @@ class KvAttentionArgs(C.Structure):
                 [(f, C.c_uint32) for f in ("heads", "group", "head_dim", "block", "causal", "q_type")])
 
 
+class MoeRouteArgs(C.Structure):
+    _fields_ = ([(f, C.c_void_p) for f in ("x", "router", "bias", "weights", "ids", "workspace")] +
+                [(f, C.c_uint64) for f in ("workspace_bytes", "t", "k", "x_pitch", "router_pitch")] + [("scaling", C.c_double)] +
+                [(f, C.c_uint32) for f in ("experts", "top", "score", "renormalize", "x_type", "router_type")])
+
+
+class MoeArgs(C.Structure):
+    _fields_ = ([(f, C.c_void_p) for f in ("x", "ids", "weights", "experts_dev", "residual", "out", "workspace")] +
+                [(f, C.c_uint64) for f in ("workspace_bytes", "t", "k", "i", "n", "x_pitch", "residual_pitch", "out_pitch")] +
+                [(f, C.c_uint32) for f in ("experts", "top", "x_type", "up_kind", "down_kind", "activation", "residual_type",
+                                           "out_type")])
+
+
+assert C.sizeof(MoeRouteArgs) == 120 and C.sizeof(MoeArgs) == 152
 assert C.sizeof(KvAppendArgs) == 168 and C.sizeof(KvAttentionArgs) == 208
 assert C.sizeof(LinearArgs) == 152 and C.sizeof(EncodeArgs) == 72 and C.sizeof(RmsNormArgs) == 104
 
@@ -164,6 +178,10 @@ SIGNATURES = {
     "st_linear": (C.c_int, [C.c_void_p, C.c_void_p]),
     "st_encode": (C.c_int, [C.c_void_p, C.c_void_p]),
     "st_rms_norm": (C.c_int, [C.c_void_p, C.c_void_p]),
+    "st_moe_route_workspace_bytes": (C.c_int, [C.c_void_p, C.POINTER(C.c_uint64)]),
+    "st_moe_route": (C.c_int, [C.c_void_p, C.c_void_p]),
+    "st_moe_workspace_bytes": (C.c_int, [C.c_void_p, C.POINTER(C.c_uint64)]),
+    "st_moe": (C.c_int, [C.c_void_p, C.c_void_p]),
     "st_kv_append": (C.c_int, [C.c_void_p, C.c_void_p]),
     "st_kv_attention_workspace_bytes": (C.c_int, [C.c_void_p, C.POINTER(C.c_uint64)]),
     "st_kv_attention": (C.c_int, [C.c_void_p, C.c_void_p]),

@@ -15,7 +15,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libstmat.so")
 ARCH = "gfx950"
 # sources that call the HIP runtime or hold kernels, and host-only sources
-HIP_SOURCES = ("linear_bf16.hip", "linear_f16.hip", "linear_fp8.hip", "materialize.hip", "encode.hip", "attention.hip",
+HIP_SOURCES = ("linear_bf16.hip", "moe_bf16.hip", "moe_f16.hip", "moe_down.hip", "moe_route.hip", "moe.cpp",
+               "linear_f16.hip", "linear_fp8.hip", "materialize.hip", "encode.hip", "attention.hip",
                "kv_append.hip", "linear.cpp",
                "stage.cpp")
 HOST_SOURCES = ("index.cpp", "stream_plan.cpp")

@@ -693,6 +693,62 @@ st_status st_kv_attention(const st_kv_attention_args* args, void* stream);
 /* Errors of these: ST_E_ARG (null or misaligned pointers, unknown types, scale, too little workspace), ST_E_SHAPE (head_dim, block,
  * pitches, size limits), ST_E_HIP (the launch). */
 
+/* ---- Mixtures of experts on quantised weights ------------------------------------------------------
+ * The router and the experts of a mixture whose experts' weights stay as the checkpoint stores them, for few
+ * tokens (the decoding batches of the serving backend that "Resident Modal LLM Architecture", "Current Backend Boundary"
+ * leaves such checkpoints to). */
+typedef enum st_route_score { ST_ROUTE_SOFTMAX = 0, ST_ROUTE_SIGMOID = 1 } st_route_score;
+
+/* z = x router^T in 64 bits;  s = softmax(z) over the experts, or 1 / (1 + e^-z)
+ * ids [t, top]: the experts of the largest z (with a bias, of the largest s + bias), in falling order, equal ones and NaN (which counts
+ * as the least) by their number;  weights [t, top] = s of those, divided by their sum if renormalize, times scaling. */
+typedef struct st_moe_route_args {
+    const void* x;           /* [t, k] of x_type, rows x_pitch elements apart */
+    const void* router;      /* [experts, k] of router_type, rows router_pitch elements apart */
+    const float* bias;       /* [experts] or NULL */
+    float* weights;
+    int32_t* ids;
+    void* workspace;         /* st_moe_route_workspace_bytes bytes, 16-byte aligned, this call's own until it is done */
+    uint64_t workspace_bytes;
+    uint64_t t, k, x_pitch, router_pitch;
+    double scaling;
+    uint32_t experts, top;   /* 1 <= top <= experts <= 1024 */
+    uint32_t score;          /* st_route_score */
+    uint32_t renormalize;    /* 0 or 1 */
+    uint32_t x_type, router_type;   /* st_out_dtype */
+} st_moe_route_args;
+st_status st_moe_route_workspace_bytes(const st_moe_route_args* args, uint64_t* bytes);
+st_status st_moe_route(const st_moe_route_args* args, void* stream);
+
+/* A weight in device memory: codes, scales and NVFP4's global scale, as st_linear_args has them. */
+typedef struct st_moe_weight { const void* w; const void* scale; const void* scale2; } st_moe_weight;
+
+/* out[t] = sum_j weights[t, j] down_e (act(gate_e x_t) * (up_e x_t)) + residual[t],  e = ids[t, j]
+ * experts_dev: device array [experts][3] of st_moe_weight: gate [i, k], up [i, k] (both up_kind) and down [n, i]
+ * (down_kind).  An id that is no expert adds nothing; one that a token has twice counts twice.  As in st_linear the weights' exact
+ * values enter, sums are fp32; gate and up meet in fp32, their product enters the down product with bf16's range and 16 significant
+ * bits, and the result is rounded once. */
+typedef struct st_moe_args {
+    const void* x;           /* [t, k] bf16 or fp16 */
+    const int32_t* ids;      /* [t, top], contiguous */
+    const float* weights;    /* [t, top], contiguous */
+    const st_moe_weight* experts_dev;
+    const void* residual;    /* [t, n] or NULL */
+    void* out;               /* [t, n] */
+    void* workspace;         /* st_moe_workspace_bytes bytes, 16-byte aligned, this call's own until it is done */
+    uint64_t workspace_bytes;
+    uint64_t t, k, i, n;     /* t * top below 2^24, the others below 2^31 */
+    uint64_t x_pitch, residual_pitch, out_pitch;
+    uint32_t experts, top;   /* top <= 32 */
+    uint32_t x_type;         /* ST_X_BF16 or ST_X_F16 */
+    uint32_t up_kind, down_kind;   /* st_kind, ST_KIND_FP8_TENSOR .. ST_KIND_MXFP4 */
+    uint32_t activation;     /* st_activation */
+    uint32_t residual_type, out_type;   /* st_out_dtype */
+} st_moe_args;
+st_status st_moe_workspace_bytes(const st_moe_args* args, uint64_t* bytes);
+st_status st_moe(const st_moe_args* args, void* stream);
+/* Errors as st_linear's. */
+
 #ifdef __cplusplus
 }
 #endif
