@@ -111,24 +111,36 @@ struct Wave {
         all_lo = sees(a, p, last - 1).lo, all_hi = sees(a, p, row0).hi;
     }
 
-    // One step of tokens from t0.  k, v: its codes as loaded; ks, vs: the scale codes of lane group g's tokens; known: they lie on a
-    // page.
-    __device__ __forceinline__ void step(const Args& a, int32_t t0, const u32x4 (&k)[4][KL], const u32x4 (&v)[DT], uint32_t ks,
-                                         uint32_t vs, bool known) {
+    // One step of tokens from t0.  k(t, i), v(d): its codes, 16 bytes of K tile t and of V^T tile d; ks, vs: the scale codes of lane
+    // group g's tokens; known: they lie on a page.  The schedule is cut between tiles, which bounds the registers that decoded
+    // codes take.
+    template <class K, class V>
+    __device__ __forceinline__ void step(const Args& a, int32_t t0, K k, V v, uint32_t ks, uint32_t vs, bool known) {
         const int lane = threadIdx.x & 63, g = lane >> 4;
         f32x4 s[QT][4];
+        u32x4 kn[KL];
+#pragma unroll
+        for (int i = 0; i < KL; ++i) kn[i] = k(0, i);
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
+            u32x4 kc[KL];
+#pragma unroll
+            for (int i = 0; i < KL; ++i) kc[i] = kn[i];
+            if (t + 1 < 4) {
+#pragma unroll
+                for (int i = 0; i < KL; ++i) kn[i] = k(t + 1, i);
+            }
 #pragma unroll
             for (int j = 0; j < QT; ++j) s[j][t] = f32x4{0, 0, 0, 0};
 #pragma unroll
             for (int i = 0; i < KL; ++i)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const u32x4 kv = codes8<F16, ST_KIND_FP8_TENSOR>(k[t][i][2 * h], k[t][i][2 * h + 1], 1.0f);
+                    const u32x4 kv = codes8<F16, ST_KIND_FP8_TENSOR>(kc[i][2 * h], kc[i][2 * h + 1], 1.0f);
 #pragma unroll
                     for (int j = 0; j < QT; ++j) s[j][t] = mfma32<F16>(kv, q[j][2 * i + h], s[j][t]);
                 }
+            __builtin_amdgcn_sched_barrier(0);
         }
         const float f = power_of(ks) * a.f;
         const bool inside = t0 >= all_lo && t0 + kStep <= all_hi && __all(known);     // every row sees every token
@@ -196,43 +208,51 @@ struct Wave {
             e = now;
         }
         const int32_t by = int32_t(vs) - e + 127;
-        const float vf = as_f32(vs == 255 ? 0x7F800000u : uint32_t(by < 0 ? 0 : by) << 23);
-        if (inside) {
+        const float vf = as_f32(vs == 255 ? (inside ? 0x7F800000u : 0x3F800000u) : uint32_t(by < 0 ? 0 : by) << 23);
+        // Tokens that some rows do not see may hold anything: NaN codes are taken out, and put NaN into the rows that see them below.
+        const uint32_t all = !inside && vs == 255 ? 0xFFFFFFFFu : 0;
+        uint32_t found = 0;
+        u32x4 vn = v(0);
 #pragma unroll
-            for (int d = 0; d < DT; ++d) {
-                const u32x4 v0 = codes8<true, ST_KIND_FP8_TENSOR>(v[d][0], v[d][1], vf), v1 = codes8<true, ST_KIND_FP8_TENSOR>(v[d][2], v[d][3], vf);
-#pragma unroll
-                for (int j = 0; j < QT; ++j) o[j][d] = mfma32<true>(v1, p[j][1], mfma32<true>(v0, p[j][0], o[j][d]));
-            }
-        } else {
-            // Tokens that some rows do not see may hold anything: NaN codes are taken out, and put NaN into the rows that see them.
-            const float vm = vs == 255 ? 1.0f : vf;
-#pragma unroll
-            for (int d = 0; d < DT; ++d) {
-                u32x4 c = v[d], bad;
+        for (int d = 0; d < DT; ++d) {
+            u32x4 c = vn;
+            if (d + 1 < DT) vn = v(d + 1);
+            if (!inside) {
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {
-                    bad[w] = vs == 255 ? 0xFFFFFFFFu : nan_bytes(c[w]);
-                    c[w] &= ~bad[w];
+                    const uint32_t bad = nan_bytes(c[w]) | all;
+                    found |= bad;
+                    c[w] &= ~bad;
                 }
-                const u32x4 v0 = codes8<true, ST_KIND_FP8_TENSOR>(c[0], c[1], vm), v1 = codes8<true, ST_KIND_FP8_TENSOR>(c[2], c[3], vm);
+            }
+            const u32x4 v0 = codes8<true, ST_KIND_FP8_TENSOR>(c[0], c[1], vf), v1 = codes8<true, ST_KIND_FP8_TENSOR>(c[2], c[3], vf);
 #pragma unroll
-                for (int j = 0; j < QT; ++j) o[j][d] = mfma32<true>(v1, p[j][1], mfma32<true>(v0, p[j][0], o[j][d]));
-                if (__any((bad[0] | bad[1] | bad[2] | bad[3]) != 0)) {
-                    // the code of 1 (0x38) where there was NaN, times 1 where the row sees the token
-                    const u32x4 b0 = codes8<true, ST_KIND_FP8_TENSOR>(bad[0] & 0x38383838u, bad[1] & 0x38383838u, 1.0f);
-                    const u32x4 b1 = codes8<true, ST_KIND_FP8_TENSOR>(bad[2] & 0x38383838u, bad[3] & 0x38383838u, 1.0f);
+            for (int j = 0; j < QT; ++j) o[j][d] = mfma32<true>(v0, p[j][0], o[j][d]);
 #pragma unroll
-                    for (int j = 0; j < QT; ++j) {
-                        const uint32_t from = uint32_t(at - lo[j]), count = known && hi[j] > lo[j] ? uint32_t(hi[j] - lo[j]) : 0;
-                        u32x4 y[2];
+            for (int j = 0; j < QT; ++j) o[j][d] = mfma32<true>(v1, p[j][1], o[j][d]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        {
+            if (__any(found != 0)) {
+                // the code of 1 (0x38) where there was NaN, times 1 where the row sees the token
 #pragma unroll
-                        for (int t = 0; t < 8; ++t)
-                            y[t >> 2][t & 3] = (from + 2 * t < count ? 0x3C00u : 0u) | (from + 2 * t + 1 < count ? 0x3C000000u : 0u);
+                for (int j = 0; j < QT; ++j) {
+                    const uint32_t from = uint32_t(at - lo[j]), count = known && hi[j] > lo[j] ? uint32_t(hi[j] - lo[j]) : 0;
+                    u32x4 y[2];
+#pragma unroll
+                    for (int t = 0; t < 8; ++t)
+                        y[t >> 2][t & 3] = (from + 2 * t < count ? 0x3C00u : 0u) | (from + 2 * t + 1 < count ? 0x3C000000u : 0u);
+#pragma unroll
+                    for (int d = 0; d < DT; ++d) {
+                        u32x4 b = v(d);
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) b[w] = (nan_bytes(b[w]) | all) & 0x38383838u;
+                        const u32x4 b0 = codes8<true, ST_KIND_FP8_TENSOR>(b[0], b[1], 1.0f), b1 = codes8<true, ST_KIND_FP8_TENSOR>(b[2], b[3], 1.0f);
                         const f32x4 hit = mfma32<true>(b1, y[1], mfma32<true>(b0, y[0], f32x4{0, 0, 0, 0}));
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
                             if (hit[i] > 0.0f) o[j][d][i] = __builtin_nanf("");
+                        __builtin_amdgcn_sched_barrier(0);
                     }
                 }
             }
@@ -307,7 +327,7 @@ __global__ __launch_bounds__(kThreads, D * QT <= 128 ? 2 : 1) void attend(Args a
         load_k(i, pk);
         load_v(i, pv);
         for (; i < st.last; i += kWaves) {
-            w.step(a, i * kStep, k, v, ks, vs, known);
+            w.step(a, i * kStep, [&](int t, int h) { return k[t][h]; }, [&](int d) { return v[d]; }, ks, vs, known);
             if (i + kWaves < st.last) {
                 pages(i + kWaves, pk, pv);
                 load_k(i + kWaves, pk);
@@ -368,27 +388,199 @@ __global__ __launch_bounds__(kThreads, D * QT <= 128 ? 2 : 1) void attend(Args a
     }
 }
 
-// The parts of each row, in their order; D / 4 lanes have a row.
-template <bool F16, int D, int ROWS>
-__global__ __launch_bounds__(kThreads) void join(Args a) {
-    constexpr uint32_t LANES = D / 4;
+// Many rows: four wavefronts of 16 * QT rows each share the codes of a step, which go from memory straight to LDS, kStages - 1 steps ahead.
+// LDS holds rows of 16-byte chunks, K's in the order of the instructions' rows (row 16 t + r: the token that lane r has in K tile
+// t), V^T's as they are; chunk c of a row sits at c ^ swizzle(row), so that 16 lanes reading one chunk of 16 rows touch all banks once.
+constexpr int kStages = 3;
+template <int CHUNKS>
+__device__ __forceinline__ int swizzle(int row) {
+    return CHUNKS == 4 ? (row >> 2) & 3 : CHUNKS == 8 ? (row >> 1) & 7 : row & 15;
+}
+__device__ __forceinline__ void to_lds16(const uint8_t* from, uint8_t* to) {
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)from, (__attribute__((address_space(3))) void*)to, 16, 0, 0);
+}
+// s_waitcnt for vmcnt(n) and lgkmcnt(0), expcnt at its maximum (gfx9 encoding: vmcnt in bits 3:0 and 15:14)
+constexpr int wait_vmem(int n) { return (n & 15) | (n >> 4) << 14 | 7 << 4; }
+
+template <bool F16, int D, int QT>
+__global__ __launch_bounds__(kThreads, D * QT <= 256 ? 2 : 1) void attend_many(Args a) {
+    using W = Wave<F16, D, QT>;
+    constexpr int ROWS = 16 * QT * kWaves, KC = D / 16, KB = kStep * D, STAGE = 2 * KB;
+    constexpr int PER = KB / 16 / kThreads;           // chunks of K, and of V, per thread and step
+    constexpr int PITCH = D + 4;
+    constexpr int OUT = kWaves * 16 * PITCH * 4, LDS = kStages * STAGE > OUT ? kStages * STAGE : OUT;
+    static_assert(PER >= 1, "a chunk for each thread");
+    __shared__ __align__(128) uint8_t lds[LDS];
+    const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    // Workgroup b runs on XCD b mod 8: an XCD takes whole heads, whose codes then stay in its L2, and a head's longest rows first.
+    const uint32_t per_head = a.tiles * a.splits, heads = a.s.heads * a.s.seqs;
+    const uint32_t pair = blockIdx.x / 8 / per_head * 8 + blockIdx.x % 8, in = blockIdx.x / 8 % per_head;
+    if (pair >= heads) return;
+    const uint32_t tile = a.tiles - 1 - in / a.splits, split = in % a.splits;
+    const uint32_t head = pair % a.s.heads, seq = pair / a.s.heads;
+    const Span p = span_of(a.s, seq);
+    const uint32_t rows = uint32_t(p.count) * a.group, row0 = tile * ROWS;
+    if (row0 >= rows) return;
+    const uint32_t end = row0 + ROWS < rows ? row0 + ROWS : rows;
+    Steps st = steps_of(a, p, row0, end);
+    if (a.splits > 1) {
+        st.first += int32_t(split * a.chunk);
+        if (st.first >= st.last) return;
+        st.last = st.first + int32_t(a.chunk) < st.last ? st.first + int32_t(a.chunk) : st.last;
+    }
+    const uint32_t mine = row0 + wave * 16 * QT;
+    const bool work = mine < end;
+    W w;
+    w.start(a, p, head, work ? mine : row0, rows);
+    // tokens that some row of this wavefront sees
+    const uint32_t mine_end = mine + 16 * QT < end ? mine + 16 * QT : end;
+    const int32_t any_lo = work ? sees(a, p, mine).lo : 0, any_hi = work ? sees(a, p, mine_end - 1).hi : 0;
+
+    const uint32_t bl = a.s.block_log2, block = 1u << bl;
+    const uint64_t page_bytes = uint64_t(block) * D;
+    // Lane l keeps the page of the l-th 16 tokens of 16 steps, and its scales; the next 16 steps' are on their way.
+    int32_t page = 0, next_page = 0;
+    uint32_t scales = 0, next_scales = 0;         // ks | vs << 8
+    auto fetch_page = [&](int32_t step) { return page_of(a.s, seq, (int64_t(step) * kStep + 16 * lane) >> bl); };
+    auto fetch_scales = [&](int32_t pg) {
+        const uint64_t at = uint64_t(pg < 0 ? 0 : pg) * a.s.heads + head;
+        return pg < 0 ? 0u : uint32_t(a.ks[at]) | uint32_t(a.vs[at]) << 8;
+    };
+    auto from_lane = [](uint32_t v, int l) { return uint32_t(__builtin_amdgcn_ds_bpermute(l * 4, int(v))); };
+    // this thread's chunks: K row 16 t + kr (t = its turn), V^T column block vg of rows tid / 4 + ...
+    const int kslot = tid % KC, krow = tid / KC, kr = krow % 16, kg = kr >> 2;
+    const int vg = (tid % 4) ^ swizzle<4>(tid / 4);
+    const int32_t pages_at = st.first;
+    auto issue = [&](int32_t step, int buf, int32_t pg, int32_t base) {
+        const int l = (step - base) * 4;
+        const int32_t pk = int32_t(from_lane(uint32_t(pg), l + kg)), pv = int32_t(from_lane(uint32_t(pg), l + vg));
+        const uint8_t* fk = a.k + (uint64_t(pk < 0 ? 0 : pk) * a.s.heads + head) * page_bytes + uint64_t((step * kStep + 16 * kg) & (block - 1)) * D;
+        const uint8_t* fv = a.v + (uint64_t(pv < 0 ? 0 : pv) * a.s.heads + head) * page_bytes + ((step * kStep + 16 * vg) & (block - 1));
+        uint8_t* to = lds + buf * STAGE + wave * 1024;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int row = i * (kThreads / KC) + krow, t = row / 16;
+            to_lds16(fk + (4 * t + (kr & 3)) * D + (kslot ^ swizzle<KC>(row)) * 16, to + i * (kThreads * 16));
+        }
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            to_lds16(fv + uint64_t(i * (kThreads / 4) + tid / 4) * block, to + KB + i * (kThreads * 16));
+    };
+    const int32_t count = st.last - st.first;
+    if (count > 0) {
+        page = fetch_page(st.first);
+        next_page = fetch_page(st.first + 16);
+        scales = fetch_scales(page);
+#pragma unroll
+        for (int i = 0; i < kStages - 1; ++i)
+            if (i < count) issue(st.first + i, i, page, pages_at);
+    }
+    int32_t base = pages_at;
+    int buf = 0;
+    for (int32_t i = 0; i < count; ++i) {
+        const int32_t step = st.first + i;
+        if (step - base == 16) {
+            base = step, page = next_page, scales = next_scales;
+            next_page = fetch_page(base + 16);
+        }
+        if (step - base == 4) next_scales = fetch_scales(next_page);
+        // this step's codes are in LDS and nobody reads the buffer that is filled next
+        if (i + 1 < count) __builtin_amdgcn_s_waitcnt(wait_vmem((kStages - 2) * 2 * PER));
+        else __builtin_amdgcn_s_waitcnt(wait_vmem(0));
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "singlethread");
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "singlethread");
+        if (i + kStages - 1 < count) {
+            const int32_t s2 = step + kStages - 1;
+            const bool on = s2 - base < 16;
+            issue(s2, buf + kStages - 1 < kStages ? buf + kStages - 1 : buf - 1, on ? page : next_page, on ? base : base + 16);
+        }
+        const int32_t t0 = step * kStep;
+        if (t0 < any_hi && t0 + kStep > any_lo) {
+            const uint8_t* sk = lds + buf * STAGE;
+            auto k = [&](int t, int h) {
+                return *reinterpret_cast<const u32x4*>(sk + (16 * t + r) * D + ((W::KL * g + h) ^ swizzle<KC>(16 * t + r)) * 16);
+            };
+            auto v = [&](int d) { return *reinterpret_cast<const u32x4*>(sk + KB + (16 * d + r) * kStep + (g ^ swizzle<4>(16 * d + r)) * 16); };
+            const int l = (step - base) * 4 + g;
+            const bool known = int32_t(from_lane(uint32_t(page), l)) >= 0;
+            const uint32_t sc = from_lane(scales, l);
+            w.step(a, t0, k, v, sc & 0xFF, sc >> 8, known);
+        }
+        buf = buf + 1 < kStages ? buf + 1 : 0;
+    }
+    __syncthreads();
+    float* mem = reinterpret_cast<float*>(lds) + wave * 16 * PITCH;
+#pragma unroll
+    for (int j = 0; j < QT; ++j) {
+        const float l = sum_over_groups(w.l[j]);
+        const float inv = a.splits > 1 ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+        for (int d = 0; d < W::DT; ++d) {
+            f32x4 o;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) o[x] = __builtin_amdgcn_ldexpf(w.o[j][d][x], w.e < 0 ? 0 : w.e - 127) * inv;
+            *reinterpret_cast<f32x4*>(mem + r * PITCH + 16 * d + 4 * g) = o;
+        }
+        const uint32_t first = mine + 16 * j;
+        if (a.splits > 1 && g == 0 && first + r < end) {
+            const uint32_t row = first + r;
+            const uint64_t at = ((uint64_t(p.first) + row / a.group) * a.s.heads * a.group + head * a.group + row % a.group) * a.splits + split;
+            a.stat[at] = float2{w.m[j], l};
+        }
+#pragma unroll 1
+        for (int i4 = lane; i4 < 16 * (D / 4); i4 += 64) {
+            const uint32_t row = first + i4 / (D / 4), d = i4 % (D / 4) * 4;
+            if (row >= end) break;
+            const f32x4 x = *reinterpret_cast<const f32x4*>(mem + i4 / (D / 4) * PITCH + d);
+            const uint64_t tok = uint64_t(p.first) + row / a.group, h = head * a.group + row % a.group;
+            if (a.splits > 1) {
+                *reinterpret_cast<f32x4*>(a.part + ((tok * a.s.heads * a.group + h) * a.splits + split) * D + d) = x;
+            } else {
+                const float y[4] = {x[0], x[1], x[2], x[3]};
+                store_row4<F16>(a, tok * a.out_pitch + h * a.out_head_pitch + d, y);
+            }
+        }
+    }
+}
+
+// The parts of a row: D / 4 lanes hold a result, groups of so many lanes take every so-many-th part, in their order, and join in LDS.
+template <bool F16, int D>
+__global__ __launch_bounds__(kThreads) void join(Args a, uint32_t tile_rows) {
+    constexpr uint32_t LANES = D / 4, GROUPS = kThreads / LANES;
+    __shared__ __align__(16) float sum[GROUPS][D];
+    __shared__ float top[GROUPS], den[GROUPS];
     const uint32_t heads = a.s.heads * a.group, seq = blockIdx.y;
     const Span p = span_of(a.s, seq);
-    const uint64_t i = uint64_t(blockIdx.x) * (kThreads / LANES) + threadIdx.x / LANES;
-    if (i >= uint64_t(p.count) * heads) return;
-    const uint32_t t = uint32_t(i / heads), h = uint32_t(i % heads), d = threadIdx.x % LANES * 4;
-    const uint32_t rows = uint32_t(p.count) * a.group, row = t * a.group + h % a.group, row0 = row / ROWS * ROWS;
-    const Steps st = steps_of(a, p, row0, row0 + ROWS < rows ? row0 + ROWS : rows);
+    const uint32_t t = blockIdx.x / heads, h = blockIdx.x % heads;
+    if (t >= uint32_t(p.count)) return;
+    const uint32_t d = threadIdx.x % LANES * 4, mine = threadIdx.x / LANES;
+    const uint32_t rows = uint32_t(p.count) * a.group, row = t * a.group + h % a.group, row0 = row / tile_rows * tile_rows;
+    const Steps st = steps_of(a, p, row0, row0 + tile_rows < rows ? row0 + tile_rows : rows);
     const uint32_t parts = (uint32_t(st.last - st.first) + a.chunk - 1) / a.chunk;
     const uint64_t at = ((uint64_t(p.first) + t) * heads + h) * a.splits;
     float m = kNone, l = 0.0f;
-    for (uint32_t o = 0; o < parts; ++o) m = fmaxf(m, a.stat[at + o].x);
     f32x4 x = {0, 0, 0, 0};
-    for (uint32_t o = 0; o < parts; ++o) {
+#pragma unroll 4
+    for (uint32_t o = mine; o < parts; o += GROUPS) m = fmaxf(m, a.stat[at + o].x);
+#pragma unroll 4
+    for (uint32_t o = mine; o < parts; o += GROUPS) {
         const float2 s = a.stat[at + o];
         const float keep = s.x == kNone ? 1.0f : __builtin_amdgcn_exp2f(s.x - m);
         l += s.y * keep;
         x += *reinterpret_cast<const f32x4*>(a.part + (at + o) * D + d) * keep;
+    }
+    *reinterpret_cast<f32x4*>(&sum[mine][d]) = x;
+    if (d == 0) top[mine] = m, den[mine] = l;
+    __syncthreads();
+    if (mine != 0) return;
+    for (uint32_t o = 1; o < GROUPS; ++o) m = fmaxf(m, top[o]);
+    l = 0.0f, x = f32x4{0, 0, 0, 0};
+    for (uint32_t o = 0; o < GROUPS; ++o) {
+        const float keep = top[o] == kNone ? 1.0f : __builtin_amdgcn_exp2f(top[o] - m);
+        l += den[o] * keep;
+        x += *reinterpret_cast<const f32x4*>(&sum[o][d]) * keep;
     }
     float y[4];
 #pragma unroll
@@ -404,7 +596,9 @@ bool off(const void* p, uint64_t n) { return reinterpret_cast<uintptr_t>(p) % n 
 
 struct Plan {
     uint64_t rows;               // of a sequence's head, at most
-    uint32_t qt, tiles, splits, chunk;
+    uint32_t qt, tile_rows, tiles, splits, chunk;
+    uint64_t count;              // new tokens of a sequence, at most
+    bool many;
     uint64_t part_bytes, stat_bytes;
 };
 
@@ -444,20 +638,24 @@ st_status plan_of(const st_kv_attention_args& g, Plan* p) {
     p->rows = count * g.group;
     if (p->rows == 0) return ST_OK;
     if (p->rows >= uint64_t(1) << 31) return st_fail(ST_E_SHAPE, "%s: %llu queries of a head are too many", kWho, (unsigned long long)p->rows);
-    p->qt = p->rows <= 16 ? 1 : 2;
-    const uint64_t tiles = (p->rows + 16 * p->qt - 1) / (16 * p->qt);
+    p->count = count;
+    p->many = p->rows > 32;
+    p->qt = p->many || (p->rows > 16 && g.head_dim < 256) ? 2 : 1;       // (two groups of 16 rows of 256 do not fit the registers of `attend`)
+    p->tile_rows = p->many ? 16 * p->qt * kWaves : 16 * p->qt;
+    const uint64_t tiles = (p->rows + p->tile_rows - 1) / p->tile_rows;
     const uint64_t groups = tiles * g.seqs * g.heads;
     // steps that a row tile can have
     uint64_t tokens = g.table_blocks * g.block;
-    if (g.window && g.window + 16 * p->qt + 2 * kStep < tokens) tokens = g.window + 16 * p->qt + 2 * kStep;
+    if (g.window && g.window + p->tile_rows + 2 * kStep < tokens) tokens = g.window + p->tile_rows + 2 * kStep;
     const uint64_t steps = (tokens + kStep - 1) / kStep;
     // Parts of equal length, about eight workgroups a CU, each with four steps for each of its wavefronts at least
-    uint64_t chunk = (groups * steps + 2047) / 2048;
+    const uint64_t want = p->many ? 512 : 2048;
+    uint64_t chunk = (groups * steps + want - 1) / want;
     chunk = (chunk + kWaves - 1) / kWaves * kWaves;
     if (chunk < 16) chunk = 16;
     uint64_t splits = (steps + chunk - 1) / chunk;
-    if (groups >= 2048) splits = 1;
-    if (groups * splits >= uint64_t(1) << 24)
+    if (groups >= want) splits = 1;
+    if ((groups + 8 * tiles) * splits >= uint64_t(1) << 24)
         return st_fail(ST_E_SHAPE, "%s: %llu workgroups are too many for one launch", kWho, (unsigned long long)(groups * splits));
     p->tiles = uint32_t(tiles), p->splits = uint32_t(splits), p->chunk = uint32_t(chunk);
     if (splits > 1) {
@@ -469,15 +667,11 @@ st_status plan_of(const st_kv_attention_args& g, Plan* p) {
 
 template <bool F16, int D>
 void launch(const Args& a, const Plan& p, hipStream_t s) {
-    const dim3 grid(p.tiles * a.s.heads * a.s.seqs * p.splits);
-    if (p.qt == 1) hipLaunchKernelGGL((attend<F16, D, 1>), grid, dim3(kThreads), 0, s, a);
-    else hipLaunchKernelGGL((attend<F16, D, 2>), grid, dim3(kThreads), 0, s, a);
-    if (p.splits > 1) {
-        const uint64_t items = p.rows * a.s.heads, per = kThreads / (D / 4);
-        const dim3 jgrid(uint32_t((items + per - 1) / per), a.s.seqs);
-        if (p.qt == 1) hipLaunchKernelGGL((join<F16, D, 16>), jgrid, dim3(kThreads), 0, s, a);
-        else hipLaunchKernelGGL((join<F16, D, 32>), jgrid, dim3(kThreads), 0, s, a);
-    }
+    const uint32_t heads = a.s.heads * a.s.seqs;
+    if (p.many) hipLaunchKernelGGL((attend_many<F16, D, 2>), dim3((heads + 7) / 8 * 8 * p.tiles * p.splits), dim3(kThreads), 0, s, a);
+    else if (p.qt == 1) hipLaunchKernelGGL((attend<F16, D, 1>), dim3(p.tiles * heads * p.splits), dim3(kThreads), 0, s, a);
+    else if constexpr (D < 256) hipLaunchKernelGGL((attend<F16, D, 2>), dim3(p.tiles * heads * p.splits), dim3(kThreads), 0, s, a);
+    if (p.splits > 1) hipLaunchKernelGGL((join<F16, D>), dim3(uint32_t(p.count) * a.s.heads * a.group, a.s.seqs), dim3(kThreads), 0, s, a, p.tile_rows);
 }
 
 }  // namespace

@@ -19,7 +19,7 @@ from dataclasses import dataclass
 import torch
 
 from ._lib import KvAppendArgs, KvAttentionArgs, check, lib
-from .ops import _E4M3, _E8M0, _TYPE, _launch, _on_device, _overlaps
+from .ops import _E4M3, _E8M0, _TYPE, _launch, _on_device, _overlaps, _span
 
 BLOCKS = (16, 32, 64, 128)         # tokens of a page
 HEAD_DIMS = (64, 128, 256)         # of kv_attention; kv_append takes every multiple of 32 up to 256
@@ -116,8 +116,10 @@ def kv_append(cache: QuantizedKvCache, k, v, table, lengths, starts=None, max_ne
     seqs, most = _check_seqs(table, lengths, starts, max_new, tokens, who)
     if tokens == 0 or seqs == 0 or most == 0 or heads == 0:
         return
-    for t in (k, v):
-        if any(_overlaps(c, t) for c in (cache.k, cache.v, cache.k_scale, cache.v_scale)):
+    (ka, kb), (va, vb) = _span(k), _span(v)
+    for t in (cache.k, cache.v, cache.k_scale, cache.v_scale):
+        a, b = _span(t)
+        if a < kb and ka < b or a < vb and va < b:
             raise ValueError(f"{who}: the cache overlaps an input")
     args = KvAppendArgs(k.data_ptr(), v.data_ptr(), cache.k.data_ptr(), cache.v.data_ptr(), cache.k_scale.data_ptr(),
                         cache.v_scale.data_ptr(), table.data_ptr(), lengths.data_ptr(), None if starts is None else starts.data_ptr(),

@@ -153,14 +153,17 @@ def _check_weight(w, who: str):
     return n, k
 
 
+def _span(t):
+    """First byte and the byte after the last of a tensor with elements."""
+    p = t.data_ptr()
+    last = t.numel() - 1 if t.is_contiguous() else sum((s - 1) * st for s, st in zip(t.shape, t.stride()))
+    return p, p + (last + 1) * t.element_size()
+
+
 def _overlaps(out, t) -> bool:
     if t is None or t.numel() == 0 or out.numel() == 0:
         return False
-
-    def span(x):
-        last = sum((s - 1) * st for s, st in zip(x.shape, x.stride()))
-        return x.data_ptr(), x.data_ptr() + (last + 1) * x.element_size()
-    (a, b), (c, d) = span(out), span(t)
+    (a, b), (c, d) = _span(out), _span(t)
     if not (a < d and c < b):
         return False
     if out.dim() == t.dim() == 2 and out.shape[0] > 1 and t.shape[0] > 1:
