@@ -6,7 +6,8 @@
 // fp32 score.  The numerators, 2^(s f - m + 6), enter the second product in fp16: m is the largest score until another passes it by 2^8, which
 // leaves them below 2^15 and 30 binades above fp16's smallest step.  Value codes are exact in fp16 too; a block's
 // power of two is taken relative to the largest, 2^E, that the wavefront has met, so that a value is exact unless its block's is 2^15
-// below that (then to 2^-33 of the largest magnitude).  l is summed from the unrounded numerators.  Maxima, sums and results are fp32.
+// below that (then to 2^-33 of the largest magnitude).  l sums the numerators as
+// they enter there.  Maxima, sums and results are fp32.
 //
 // Operands come straight from memory to the matrix instructions, no value crosses lanes between the two products.  The first one
 // makes S^T (tokens x queries) from K rows, the second O^T = V^T P^T.  A step has 64 tokens; lane group g (of four) gets scores of tokens
@@ -63,13 +64,18 @@ __device__ __forceinline__ Steps steps_of(const Args& a, const Span& p, uint32_t
     return hi > lo ? Steps{lo / kStep, (hi + kStep - 1) / kStep} : Steps{0, 0};
 }
 
+// Over the four lane groups, by exchanging rows of 16 and halves of 32 lanes on the vector unit.
 __device__ __forceinline__ float max_over_groups(float v) {
-    v = fmaxf(v, __shfl_xor(v, 16));
-    return fmaxf(v, __shfl_xor(v, 32));
+    auto a = __builtin_amdgcn_permlane16_swap(as_u32(v), as_u32(v), false, false);
+    v = fmaxf(as_f32(a[0]), as_f32(a[1]));
+    auto b = __builtin_amdgcn_permlane32_swap(as_u32(v), as_u32(v), false, false);
+    return fmaxf(as_f32(b[0]), as_f32(b[1]));
 }
-__device__ __forceinline__ float sum_over_groups(float v) {
-    v += __shfl_xor(v, 16);
-    return v + __shfl_xor(v, 32);
+
+// v, as something the compiler knows nothing of: what a rarely taken branch computes from it stays in that branch.
+__device__ __forceinline__ uint32_t opaque(uint32_t v) {
+    asm volatile("" : "+v"(v));
+    return v;
 }
 
 // Bytes of c that are a NaN code (0x7F, 0xFF) as 0xFF.
@@ -85,8 +91,10 @@ struct Wave {
     static constexpr int KL = D / 64;      // 16-byte loads of a K row per lane
     static constexpr int DT = D / 16;      // 16-column tiles of a result
     u32x4 q[QT][D / 32];
-    float m[QT], l[QT];
+    float m[QT];
+    f32x4 l[QT];                           // the sum of a row's numerators, four times, in each of its lanes
     f32x4 o[QT][DT];
+    uint32_t nan[QT][(DT + 7) / 8];        // a bit for each result that is NaN whatever o says
     int32_t lo[QT], hi[QT];
     int32_t e = -1;                        // E + 127, -1: no values yet
     int32_t all_lo, all_hi;                // tokens that every row sees
@@ -103,9 +111,9 @@ struct Wave {
             const uint8_t* pq = a.q + ((uint64_t(p.first) + (have ? t : 0)) * a.q_pitch + (have ? h : 0) * a.q_head_pitch + D / 4 * g) * 2;
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) q[j][c] = have ? u32x4(*reinterpret_cast<const u32x4_any*>(pq + 16 * c)) : u32x4{0, 0, 0, 0};
-            m[j] = kNone, l[j] = 0.0f;
+            m[j] = kNone, l[j] = f32x4{0, 0, 0, 0};
 #pragma unroll
-            for (int d = 0; d < DT; ++d) o[j][d] = f32x4{0, 0, 0, 0};
+            for (int d = 0; d < DT; ++d) o[j][d] = f32x4{0, 0, 0, 0}, nan[j][d / 8] = 0;
         }
         const uint32_t last = row0 + 16 * QT < rows ? row0 + 16 * QT : rows;
         all_lo = sees(a, p, last - 1).lo, all_hi = sees(a, p, row0).hi;
@@ -148,23 +156,22 @@ struct Wave {
         u32x4 p[QT][2];
 #pragma unroll
         for (int j = 0; j < QT; ++j) {
+            // tokens of this lane that the row sees; the scores stay as they are, so that neither case copies them
+            const uint32_t from = uint32_t(at - lo[j]), count = known && hi[j] > lo[j] ? uint32_t(hi[j] - lo[j]) : 0;
             float mx = kNone;
             if (inside) {
 #pragma unroll
                 for (int t = 0; t < 4; ++t)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) mx = fmaxf(mx, s[j][t][i]);
-                mx *= f;
             } else {
-                const uint32_t from = uint32_t(at - lo[j]), count = known && hi[j] > lo[j] ? uint32_t(hi[j] - lo[j]) : 0;
+                const uint32_t here = opaque(from);
 #pragma unroll
                 for (int t = 0; t < 4; ++t)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        s[j][t][i] = from + (4 * t + i) < count ? s[j][t][i] * f : kNone;
-                        mx = fmaxf(mx, s[j][t][i]);
-                    }
+                    for (int i = 0; i < 4; ++i) mx = fmaxf(mx, here + (4 * t + i) < count ? s[j][t][i] : kNone);
             }
+            mx *= mx == kNone ? 1.0f : f;
             mx = max_over_groups(mx);
             if (__any(mx > m[j] + kSlack)) {
                 const float now = fmaxf(m[j], mx), keep = now == kNone ? 1.0f : __builtin_amdgcn_exp2f(m[j] - now);
@@ -173,20 +180,30 @@ struct Wave {
 #pragma unroll
                 for (int d = 0; d < DT; ++d) o[j][d] *= keep;
             }
-            const float base = kOffset - (m[j] == kNone ? 0.0f : m[j]), fj = inside ? f : 1.0f;
-            float sum = 0.0f;
+            const float base = kOffset - (m[j] == kNone ? 0.0f : m[j]);
+            if (inside) {
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                float x[4];
+                for (int t = 0; t < 4; ++t) {
+                    float x[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    x[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j][t][i], fj, base));
-                    sum += x[i];
+                    for (int i = 0; i < 4; ++i) x[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j][t][i], f, base));
+                    p[j][t >> 1][2 * (t & 1)] = cvt_f16x2(x[0], x[1]);
+                    p[j][t >> 1][2 * (t & 1) + 1] = cvt_f16x2(x[2], x[3]);
                 }
-                p[j][t >> 1][2 * (t & 1)] = cvt_f16x2(x[0], x[1]);
-                p[j][t >> 1][2 * (t & 1) + 1] = cvt_f16x2(x[2], x[3]);
+            } else {
+                const uint32_t here = opaque(from);
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    float x[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        x[i] = here + (4 * t + i) < count ? __builtin_amdgcn_exp2f(__builtin_fmaf(s[j][t][i], f, base)) : 0.0f;
+                    p[j][t >> 1][2 * (t & 1)] = cvt_f16x2(x[0], x[1]);
+                    p[j][t >> 1][2 * (t & 1) + 1] = cvt_f16x2(x[2], x[3]);
+                }
             }
-            l[j] += sum;
+            const u32x4 ones = {0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u};
+            l[j] = mfma32<true>(ones, p[j][1], mfma32<true>(ones, p[j][0], l[j]));
         }
         // the largest power of two so far
         int32_t now = known ? int32_t(vs == 255 ? 0 : vs) : -1;
@@ -208,55 +225,70 @@ struct Wave {
             e = now;
         }
         const int32_t by = int32_t(vs) - e + 127;
-        const float vf = as_f32(vs == 255 ? (inside ? 0x7F800000u : 0x3F800000u) : uint32_t(by < 0 ? 0 : by) << 23);
-        // Tokens that some rows do not see may hold anything: NaN codes are taken out, and put NaN into the rows that see them below.
-        const uint32_t all = !inside && vs == 255 ? 0xFFFFFFFFu : 0;
+        const float vf = as_f32(vs == 255 ? 0x7F800000u : uint32_t(by < 0 ? 0 : by) << 23);
+        // Tokens that some rows do not see may hold anything.
         uint32_t found = 0;
+        if (!inside) {
+            found = vs == 255;
+#pragma unroll
+            for (int d = 0; d < DT; ++d) {
+                const u32x4 c = v(d);
+                found |= nan_bytes(c[0]) | nan_bytes(c[1]) | nan_bytes(c[2]) | nan_bytes(c[3]);
+            }
+        }
+        const bool dirty = __any(found != 0);
+        const uint32_t all = vs == 255 ? 0xFFFFFFFFu : 0;
+        if (dirty) {
+            // NaN codes are taken out below, and the results of the rows that see them noted here: the code of 1 (0x38) in their place
+            // times 1 where the row sees the token
+#pragma unroll
+            for (int j = 0; j < QT; ++j) {
+                const uint32_t from = uint32_t(at - lo[j]), count = known && hi[j] > lo[j] ? uint32_t(hi[j] - lo[j]) : 0;
+                u32x4 y[2];
+#pragma unroll
+                for (int t = 0; t < 8; ++t)
+                    y[t >> 2][t & 3] = (from + 2 * t < count ? 0x3C00u : 0u) | (from + 2 * t + 1 < count ? 0x3C000000u : 0u);
+#pragma unroll
+                for (int d = 0; d < DT; ++d) {
+                    u32x4 b = v(d);
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) b[w] = (nan_bytes(b[w]) | all) & 0x38383838u;
+                    const u32x4 b0 = codes8<true, ST_KIND_FP8_TENSOR>(b[0], b[1], 1.0f), b1 = codes8<true, ST_KIND_FP8_TENSOR>(b[2], b[3], 1.0f);
+                    const f32x4 hit = mfma32<true>(b1, y[1], mfma32<true>(b0, y[0], f32x4{0, 0, 0, 0}));
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (hit[i] > 0.0f) nan[j][d / 8] |= 1u << (d % 8 * 4 + i);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            }
+        }
+        const float vm = dirty && vs == 255 ? 1.0f : vf;
         u32x4 vn = v(0);
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
             u32x4 c = vn;
             if (d + 1 < DT) vn = v(d + 1);
-            if (!inside) {
+            if (dirty) {
 #pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    const uint32_t bad = nan_bytes(c[w]) | all;
-                    found |= bad;
-                    c[w] &= ~bad;
-                }
+                for (int w = 0; w < 4; ++w) c[w] &= ~(nan_bytes(c[w]) | all);
             }
-            const u32x4 v0 = codes8<true, ST_KIND_FP8_TENSOR>(c[0], c[1], vf), v1 = codes8<true, ST_KIND_FP8_TENSOR>(c[2], c[3], vf);
+            const u32x4 v0 = codes8<true, ST_KIND_FP8_TENSOR>(c[0], c[1], vm), v1 = codes8<true, ST_KIND_FP8_TENSOR>(c[2], c[3], vm);
 #pragma unroll
             for (int j = 0; j < QT; ++j) o[j][d] = mfma32<true>(v0, p[j][0], o[j][d]);
 #pragma unroll
             for (int j = 0; j < QT; ++j) o[j][d] = mfma32<true>(v1, p[j][1], o[j][d]);
             __builtin_amdgcn_sched_barrier(0);
         }
-        {
-            if (__any(found != 0)) {
-                // the code of 1 (0x38) where there was NaN, times 1 where the row sees the token
+    }
+    // o, with 2^E and a factor of the row's
+    __device__ __forceinline__ f32x4 result(int j, int d, float by) const {
+        f32x4 x;
 #pragma unroll
-                for (int j = 0; j < QT; ++j) {
-                    const uint32_t from = uint32_t(at - lo[j]), count = known && hi[j] > lo[j] ? uint32_t(hi[j] - lo[j]) : 0;
-                    u32x4 y[2];
-#pragma unroll
-                    for (int t = 0; t < 8; ++t)
-                        y[t >> 2][t & 3] = (from + 2 * t < count ? 0x3C00u : 0u) | (from + 2 * t + 1 < count ? 0x3C000000u : 0u);
-#pragma unroll
-                    for (int d = 0; d < DT; ++d) {
-                        u32x4 b = v(d);
-#pragma unroll
-                        for (int w = 0; w < 4; ++w) b[w] = (nan_bytes(b[w]) | all) & 0x38383838u;
-                        const u32x4 b0 = codes8<true, ST_KIND_FP8_TENSOR>(b[0], b[1], 1.0f), b1 = codes8<true, ST_KIND_FP8_TENSOR>(b[2], b[3], 1.0f);
-                        const f32x4 hit = mfma32<true>(b1, y[1], mfma32<true>(b0, y[0], f32x4{0, 0, 0, 0}));
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (hit[i] > 0.0f) o[j][d][i] = __builtin_nanf("");
-                        __builtin_amdgcn_sched_barrier(0);
-                    }
-                }
-            }
+        for (int i = 0; i < 4; ++i) {
+            x[i] = __builtin_amdgcn_ldexpf(o[j][d][i] * by, e < 0 ? 0 : e - 127);
+            if (nan[j][d / 8] >> (d % 8 * 4 + i) & 1) x[i] = __builtin_nanf("");
         }
+        return x;
     }
 };
 
@@ -337,8 +369,7 @@ __global__ __launch_bounds__(kThreads, D * QT <= 128 ? 2 : 1) void attend(Args a
     }
 #pragma unroll
     for (int j = 0; j < QT; ++j) {
-        w.l[j] = sum_over_groups(w.l[j]);
-        if (g == 0) top[wave][16 * j + r] = w.m[j], den[wave][16 * j + r] = w.l[j];
+        if (g == 0) top[wave][16 * j + r] = w.m[j], den[wave][16 * j + r] = w.l[j][0];
     }
     __syncthreads();
     float m[QT];
@@ -349,9 +380,7 @@ __global__ __launch_bounds__(kThreads, D * QT <= 128 ? 2 : 1) void attend(Args a
         for (int o = 0; o < kWaves; ++o) m[j] = fmaxf(m[j], top[o][16 * j + r]);
         const float keep = w.m[j] == kNone ? 1.0f : __builtin_amdgcn_exp2f(w.m[j] - m[j]);
 #pragma unroll
-        for (int d = 0; d < W::DT; ++d)
-#pragma unroll
-            for (int x = 0; x < 4; ++x) w.o[j][d][x] = __builtin_amdgcn_ldexpf(w.o[j][d][x] * keep, w.e < 0 ? 0 : w.e - 127);
+        for (int d = 0; d < W::DT; ++d) w.o[j][d] = w.result(j, d, keep);
     }
 #pragma unroll
     for (int o = 0; o < kWaves; ++o) {
@@ -402,6 +431,47 @@ __device__ __forceinline__ void to_lds16(const uint8_t* from, uint8_t* to) {
 // s_waitcnt for vmcnt(n) and lgkmcnt(0), expcnt at its maximum (gfx9 encoding: vmcnt in bits 3:0 and 15:14)
 constexpr int wait_vmem(int n) { return (n & 15) | (n >> 4) << 14 | 7 << 4; }
 
+// The sequence, head and row tile of this workgroup.  Workgroup b runs on XCD b mod 8.  An XCD takes an eighth of the heads, or with 8 / n
+// others every so-many-th tile of one of n heads, so that a head's codes meet in its L2; the longest sequences come first, and of each
+// the tiles with the most tokens.  There is no gap between the tiles of sequences of different size: workgroups without
+// work would come in patterns that leave part of an XCD idle (4 prompts of 682 to 2048 tokens: 511 us without gaps between the longest's tiles, 887 with).
+// All lanes of a wavefront take part, 64 sequences at a time.
+template <int ROWS>
+__device__ __forceinline__ bool place(const Args& a, uint32_t& seq, uint32_t& head, uint32_t& tile) {
+    const uint32_t H = a.s.heads, lane = threadIdx.x & 63, xcd = blockIdx.x % 8;
+    const uint32_t ways = H % 8 == 0 ? 1 : 8 % H == 0 ? 8 / H : 8, groups = 8 / ways, per = H % 8 == 0 ? H / 8 : 8 % H == 0 ? 1 : H;
+    const uint32_t way = xcd / groups;
+    uint32_t at = blockIdx.x / 8 / a.splits;
+    for (uint32_t base = 0; base < a.s.seqs; base += 64) {
+        const uint32_t s = base + lane;
+        uint32_t tiles = 0, len = 0;
+        if (s < a.s.seqs) {
+            const Span p = span_of(a.s, s);
+            const uint32_t all = (uint32_t(p.count) * a.group + ROWS - 1) / ROWS;
+            tiles = all > way ? (all - way + ways - 1) / ways : 0;
+            len = uint32_t(p.len);
+        }
+        uint32_t before = 0, total = 0;
+        const uint32_t n = a.s.seqs - base < 64 ? a.s.seqs - base : 64;
+        for (uint32_t o = 0; o < n; ++o) {
+            const uint32_t t = __builtin_amdgcn_readlane(tiles, o), l = __builtin_amdgcn_readlane(len, o);
+            before += l > len || (l == len && o < lane) ? t : 0;
+            total += t;
+        }
+        if (at < total * per) {
+            const uint64_t hit = __ballot(at >= before * per && at < (before + tiles) * per);
+            const uint32_t o = uint32_t(__builtin_ctzll(hit)), t = __builtin_amdgcn_readlane(tiles, o);
+            at -= __builtin_amdgcn_readlane(before, o) * per;
+            seq = base + o;
+            head = xcd % groups + (per > 1 ? at / t * groups : 0);
+            tile = way + (t - 1 - at % t) * ways;
+            return true;
+        }
+        at -= total * per;
+    }
+    return false;
+}
+
 template <bool F16, int D, int QT>
 __global__ __launch_bounds__(kThreads, D * QT <= 256 ? 2 : 1) void attend_many(Args a) {
     using W = Wave<F16, D, QT>;
@@ -413,12 +483,9 @@ __global__ __launch_bounds__(kThreads, D * QT <= 256 ? 2 : 1) void attend_many(A
     __shared__ __align__(128) uint8_t lds[LDS];
     const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    // Workgroup b runs on XCD b mod 8: an XCD takes whole heads, whose codes then stay in its L2, and a head's longest rows first.
-    const uint32_t per_head = a.tiles * a.splits, heads = a.s.heads * a.s.seqs;
-    const uint32_t pair = blockIdx.x / 8 / per_head * 8 + blockIdx.x % 8, in = blockIdx.x / 8 % per_head;
-    if (pair >= heads) return;
-    const uint32_t tile = a.tiles - 1 - in / a.splits, split = in % a.splits;
-    const uint32_t head = pair % a.s.heads, seq = pair / a.s.heads;
+    uint32_t seq, head, tile;
+    const uint32_t split = blockIdx.x / 8 % a.splits;
+    if (!place<ROWS>(a, seq, head, tile)) return;
     const Span p = span_of(a.s, seq);
     const uint32_t rows = uint32_t(p.count) * a.group, row0 = tile * ROWS;
     if (row0 >= rows) return;
@@ -514,15 +581,10 @@ __global__ __launch_bounds__(kThreads, D * QT <= 256 ? 2 : 1) void attend_many(A
     float* mem = reinterpret_cast<float*>(lds) + wave * 16 * PITCH;
 #pragma unroll
     for (int j = 0; j < QT; ++j) {
-        const float l = sum_over_groups(w.l[j]);
+        const float l = w.l[j][0];
         const float inv = a.splits > 1 ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
-        for (int d = 0; d < W::DT; ++d) {
-            f32x4 o;
-#pragma unroll
-            for (int x = 0; x < 4; ++x) o[x] = __builtin_amdgcn_ldexpf(w.o[j][d][x], w.e < 0 ? 0 : w.e - 127) * inv;
-            *reinterpret_cast<f32x4*>(mem + r * PITCH + 16 * d + 4 * g) = o;
-        }
+        for (int d = 0; d < W::DT; ++d) *reinterpret_cast<f32x4*>(mem + r * PITCH + 16 * d + 4 * g) = w.result(j, d, inv);
         const uint32_t first = mine + 16 * j;
         if (a.splits > 1 && g == 0 && first + r < end) {
             const uint32_t row = first + r;
@@ -599,6 +661,7 @@ struct Plan {
     uint32_t qt, tile_rows, tiles, splits, chunk;
     uint64_t count;              // new tokens of a sequence, at most
     bool many;
+    uint32_t positions;          // workgroups of an XCD, at most
     uint64_t part_bytes, stat_bytes;
 };
 
@@ -655,6 +718,13 @@ st_status plan_of(const st_kv_attention_args& g, Plan* p) {
     if (chunk < 16) chunk = 16;
     uint64_t splits = (steps + chunk - 1) / chunk;
     if (groups >= want) splits = 1;
+    if (p->many) {
+        const uint64_t H = g.heads, ways = H % 8 == 0 ? 1 : 8 % H == 0 ? 8 / H : 8, per = H % 8 == 0 ? H / 8 : 8 % H == 0 ? 1 : H;
+        const uint64_t positions = g.seqs * per * ((tiles + ways - 1) / ways);
+        if (positions * 8 * splits >= uint64_t(1) << 24)
+            return st_fail(ST_E_SHAPE, "%s: %llu workgroups are too many for one launch", kWho, (unsigned long long)(positions * 8 * splits));
+        p->positions = uint32_t(positions);
+    }
     if ((groups + 8 * tiles) * splits >= uint64_t(1) << 24)
         return st_fail(ST_E_SHAPE, "%s: %llu workgroups are too many for one launch", kWho, (unsigned long long)(groups * splits));
     p->tiles = uint32_t(tiles), p->splits = uint32_t(splits), p->chunk = uint32_t(chunk);
@@ -668,7 +738,7 @@ st_status plan_of(const st_kv_attention_args& g, Plan* p) {
 template <bool F16, int D>
 void launch(const Args& a, const Plan& p, hipStream_t s) {
     const uint32_t heads = a.s.heads * a.s.seqs;
-    if (p.many) hipLaunchKernelGGL((attend_many<F16, D, 2>), dim3((heads + 7) / 8 * 8 * p.tiles * p.splits), dim3(kThreads), 0, s, a);
+    if (p.many) hipLaunchKernelGGL((attend_many<F16, D, 2>), dim3(8 * p.positions * p.splits), dim3(kThreads), 0, s, a);
     else if (p.qt == 1) hipLaunchKernelGGL((attend<F16, D, 1>), dim3(p.tiles * heads * p.splits), dim3(kThreads), 0, s, a);
     else if constexpr (D < 256) hipLaunchKernelGGL((attend<F16, D, 2>), dim3(p.tiles * heads * p.splits), dim3(kThreads), 0, s, a);
     if (p.splits > 1) hipLaunchKernelGGL((join<F16, D>), dim3(uint32_t(p.count) * a.s.heads * a.group, a.s.seqs), dim3(kThreads), 0, s, a, p.tile_rows);
