@@ -30,7 +30,7 @@ st_status check_args(const st_moe_args* g) {
     if (g->activation > ST_ACT_GELU_TANH) return st_fail(ST_E_ARG, "%s: unknown activation %u", kWho, g->activation);
     if (g->residual_type > ST_OUT_F32 || g->out_type > ST_OUT_F32) return st_fail(ST_E_ARG, "%s: unknown residual or output type", kWho);
     const uint64_t lim = uint64_t(1) << 31;
-    if (g->k >= lim || g->i >= lim || g->n >= lim || g->experts > 32767 || g->top > kMaxTop || g->t >= lim || g->t * g->top >= uint64_t(1) << 24)
+    if (g->k >= lim || g->i >= lim || g->n >= lim || g->experts > kMaxExperts || g->top > kMaxTop || g->t >= lim || g->t * g->top >= uint64_t(1) << 24)
         return st_fail(ST_E_SHAPE, "%s: t %llu, k %llu, i %llu, n %llu, %u of %u experts are too many", kWho, (unsigned long long)g->t,
                        (unsigned long long)g->k, (unsigned long long)g->i, (unsigned long long)g->n, g->top, g->experts);
     st_status r = check_kind(g->up_kind, g->k, "gate and up");
@@ -49,19 +49,22 @@ st_status check_args(const st_moe_args* g) {
 }
 
 struct Plan {
-    bool few;
-    uint64_t h_pitch, h_bytes, part_bytes;
+    Cut cut;
+    uint64_t h_pitch, h_bytes, part_bytes, sort_bytes;
+    uint64_t total() const { return h_bytes + part_bytes + sort_bytes; }
 };
 
 st_status plan_of(const st_moe_args& g, Plan* p) {
     const uint64_t pairs = g.t * g.top;
-    p->few = g.t <= kFewTokens;
+    p->cut = g.t == 1 ? ONE : pairs > 512 ? MANY : g.t <= 16 ? FEW : g.t <= 64 ? SOME : MANY;
     p->h_pitch = (g.i + 7) / 8 * 8;
     p->h_bytes = (pairs * p->h_pitch * 4 + 15) / 16 * 16;
-    p->part_bytes = p->few ? 0 : pairs * g.n * 4;
+    p->part_bytes = p->cut >= SOME ? pairs * g.n * 4 : 0;
     const uint64_t slots = pairs < g.experts ? pairs : g.experts;
+    p->part_bytes = (p->part_bytes + 15) / 16 * 16;
+    p->sort_bytes = p->cut == ONE ? 0 : (4 + 4 * slots + pairs) * 4;
     // threads of each launch; a grid dimension holds fewer than 2^32, and 65535 workgroups in y (slots is below that)
-    if ((g.i + 15) / 16 * 512 >> 32 || (g.n + 15) / 16 * 512 >> 32 || (!p->few && (g.n + 3) / 4 * g.t >> 32) || slots > 65535)
+    if ((g.i + 3) / 4 * 512 >> 32 || (g.n + 3) / 4 * 512 >> 32 || (p->cut >= SOME && (g.n + 3) / 4 * g.t >> 32) || slots > 65535)
         return st_fail(ST_E_SHAPE, "%s: i %llu, n %llu, t %llu take more threads than one launch holds", kWho, (unsigned long long)g.i,
                        (unsigned long long)g.n, (unsigned long long)g.t);
     return ST_OK;
@@ -76,7 +79,7 @@ extern "C" st_status st_moe_workspace_bytes(const st_moe_args* g, uint64_t* byte
     if (r != ST_OK || empty(*g)) return r;
     Plan p;
     const st_status f = plan_of(*g, &p);
-    if (f == ST_OK) *bytes = p.h_bytes + p.part_bytes;
+    if (f == ST_OK) *bytes = p.total();
     return f;
 }
 
@@ -86,7 +89,7 @@ extern "C" st_status st_moe(const st_moe_args* g, void* stream) {
     Plan p;
     const st_status f = plan_of(*g, &p);
     if (f != ST_OK) return f;
-    const uint64_t need = p.h_bytes + p.part_bytes;
+    const uint64_t need = p.total();
     if (!g->workspace || g->workspace_bytes < need)
         return st_fail(ST_E_ARG, "%s: %llu bytes of workspace, %llu are needed", kWho,
                        (unsigned long long)(g->workspace ? g->workspace_bytes : 0), (unsigned long long)need);
@@ -102,16 +105,17 @@ extern "C" st_status st_moe(const st_moe_args* g, void* stream) {
     a.x_pitch = g->x_pitch; a.res_pitch = g->residual_pitch; a.out_pitch = g->out_pitch; a.h_pitch = p.h_pitch;
     a.t = uint32_t(g->t); a.k = uint32_t(g->k); a.i = uint32_t(g->i); a.n = uint32_t(g->n);
     a.experts = g->experts; a.top = g->top; a.pairs = uint32_t(g->t * g->top);
-    a.by_pair = a.pairs < a.experts;
-    a.slots = a.by_pair ? a.pairs : a.experts;
+    a.slots = p.cut == ONE || a.pairs < a.experts ? a.pairs : a.experts;
+    a.sorted = reinterpret_cast<uint32_t*>(a.h + p.h_bytes + p.part_bytes);
     a.act = g->activation; a.res_type = g->residual_type; a.out_type = g->out_type;
     auto quad = [](const void* v, uint32_t type, uint64_t pitch, uint64_t rows) {
         return !off(v, 4 * size_of(type)) && (rows <= 1 || pitch % 4 == 0);
     };
     a.vec = quad(g->out, g->out_type, g->out_pitch, g->t) && (!g->residual || quad(g->residual, g->residual_type, g->residual_pitch, g->t));
     hipStream_t s = static_cast<hipStream_t>(stream);
-    (g->x_type == ST_X_F16 ? launch_up_f16 : launch_up_bf16)(a, g->up_kind, p.few, s);
-    launch_down(a, g->down_kind, p.few, s);
+    if (p.cut != ONE) launch_sort(a, s);
+    (g->x_type == ST_X_F16 ? launch_up_f16 : launch_up_bf16)(a, g->up_kind, p.cut, s);
+    launch_down(a, g->down_kind, p.cut, s);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return st_fail(ST_E_HIP, "%s: launch failed: %s", kWho, hipGetErrorString(e));
     return ST_OK;

@@ -4,10 +4,12 @@
 // Weights enter as st_linear's do (linear_kernels.h: exact codes times scales, fp32 sums).  h is kept as two bf16 terms, 16 significant bits with
 // bf16's range: one term would add as much again to a bf16 result's own rounding, and more than that to an fp16 one's.
 //
-// Bound by the bytes of the chosen experts' weights; x and h, a few rows, come from L2.  No atomics: every sum has its order.
-//  * few tokens (16): up_few, one workgroup for 16 rows of gate and up of an expert, its wavefronts taking different parts of K; down_few, one
-//    workgroup for 16 or 32 columns of y, its wavefronts taking all experts' parts of K in turn, each instruction's 16 columns being the tokens, so
-//    that the sum over experts is the sum over K and needs no second pass.
+// Bound by the bytes of the chosen experts' weights; x and h, few rows, come from L2.  No atomics on results: every sum has its order.
+//  * one token: up_one, down_one, dot products on the vector unit at the rate the weights arrive; a lane has 16 bytes of a row, and in
+//    down_one the lanes go through all experts' rows as if they were one.
+//  * up to 64: up_few, a workgroup for 16 rows of gate and of up of an expert, its wavefronts taking different parts of K; down_few, a
+//    workgroup for 16 or 32 columns of y, its wavefronts taking all experts' parts of K in turn.  The columns of its instructions are the tokens,
+//    so that the sum over experts is the sum over K and needs no second pass.
 //  * more: tiles of 64 pairs of one expert by 64 rows of gate and of up, or 128 of down; x or h staged through LDS for four wavefronts, weights
 //    straight to their registers; the pairs' results pass through memory and `combine` adds them.
 #pragma once
@@ -20,21 +22,64 @@ namespace {
 
 using namespace st_dev;
 using st_linear_impl::Dense;
-using st_linear_impl::Few;
-using st_linear_impl::Flag;
-using st_linear_impl::load_piece;
+using st_linear_impl::dot2;
+using st_linear_impl::fold;
 using st_linear_impl::load_scales;
 
 // How rows meet the weight: as they are, fp16 split in two bf16 terms, or two terms in memory.
 enum Rows { PLAIN, SPLIT, TWO };
+
+// The 16 bytes at p, of which `avail` belong to a row of `row` bytes, the others 0.  Where the row ends among them they come from a load
+// that ends with the row, shifted.
+__device__ __forceinline__ u32x4 load_end(const uint8_t* p, int32_t avail, uint32_t row) {
+    u32x4 v = {0, 0, 0, 0};
+    if (avail >= 16) {
+        v = *reinterpret_cast<const u32x4_any*>(p);
+    } else if (avail > 0 && row >= 16) {
+        const uint32_t back = 16 - uint32_t(avail), by = back & 3;
+        v = *reinterpret_cast<const u32x4_any*>(p - back);
+        if (back & 4) v = u32x4{v[1], v[2], v[3], 0};
+        if (back & 8) v = u32x4{v[2], v[3], 0, 0};
+        v = u32x4{__builtin_amdgcn_alignbyte(v[1], v[0], by), __builtin_amdgcn_alignbyte(v[2], v[1], by),
+                  __builtin_amdgcn_alignbyte(v[3], v[2], by), __builtin_amdgcn_alignbyte(0, v[3], by)};
+    } else {
+        uint64_t lo = 0, hi = 0;
+#pragma unroll 1
+        for (int i = 0; i < int(avail); ++i) (i < 8 ? lo : hi) |= uint64_t(p[i]) << (8 * (i & 7));
+        v = u32x4{uint32_t(lo), uint32_t(lo >> 32), uint32_t(hi), uint32_t(hi >> 32)};
+    }
+    return v;
+}
+// How a turn ends: within K; at K's end, which cuts no 16 bytes of a weight's row; or anywhere (kernels of their own, since the shifted
+// loads take twice the registers).
+enum Ends { WITHIN, EVEN, ODD };
+// (avail is 32 bits of something the compiler knows nothing of: it would keep each load's own in a register through the loop)
+__device__ __forceinline__ int32_t bytes_left(int64_t v) {
+    int32_t n = v < -1024 ? -1024 : v > 4096 ? 4096 : int32_t(v);
+    asm volatile("" : "+v"(n));
+    return n;
+}
+template <Ends END>
+__device__ __forceinline__ u32x4 load_piece(const uint8_t* p, int32_t avail, uint32_t row) {
+    if constexpr (END == WITHIN) return *reinterpret_cast<const u32x4_any*>(p);
+    else if constexpr (END == EVEN) return avail > 0 ? u32x4(*reinterpret_cast<const u32x4_any*>(p)) : u32x4{0, 0, 0, 0};
+    else return load_end(p, avail, row);
+}
+template <Ends END>
+struct Ending {
+    static constexpr Ends value = END;
+};
 
 // A row's data and scales of one matrix of an expert, in a uniform form.
 struct Matrix {
     const uint8_t *w, *s, *s2;
 };
 __device__ __forceinline__ Matrix matrix_of(const Args& a, uint32_t expert, int which) {
+    // (an address from memory may point anywhere for the compiler, which would take flat loads: these are global memory)
+    typedef const __attribute__((address_space(1))) uint8_t* global;
     const st_moe_weight& m = a.experts_dev[uint64_t(expert) * 3 + which];
-    return Matrix{static_cast<const uint8_t*>(m.w), static_cast<const uint8_t*>(m.scale), static_cast<const uint8_t*>(m.scale2)};
+    auto at = [](const void* p) { return (const uint8_t*)(global)reinterpret_cast<uintptr_t>(p); };
+    return Matrix{at(m.w), at(m.scale), at(m.scale2)};
 }
 template <int WK>
 __device__ __forceinline__ float tensor_scale(const Matrix& m) {
@@ -43,84 +88,106 @@ __device__ __forceinline__ float tensor_scale(const Matrix& m) {
     else return 1.0f;
 }
 
-// A turn of K (Few::SS elements from k0) for NG groups of 16 weight rows: this lane's rows n[i], its row of x at px (and its second
-// term at pl).  acc += the products, with the scales of blocks.  WHOLE: the turn lies within K, else there are zeros behind its end.
-template <int WK, bool F16, Rows R, bool WHOLE, int NG>
-__device__ __forceinline__ void turn(const Matrix (&mat)[NG], const uint32_t (&n)[NG], const uint8_t* px, const uint8_t* pl, bool have,
-                                     uint32_t k0, uint32_t K, f32x4 (&acc)[NG]) {
-    using F = Few<ST_X_BF16, WK>;
-    const int q = (threadIdx.x & 63) >> 4;
-    const uint32_t kq = k0 + F::LK * q, w_row = F::FP4 ? K / 2 : K, ws_row = K / (WK == ST_KIND_NVFP4 ? 16 : 32), groups = (K + 127) / 128;
-    u32x4 w[NG][4], xr[4][F::XL], xl[R == PLAIN ? 1 : 4][F::XL];
-    uint64_t wsc[NG];
+// A turn of K for a wavefront: 256 elements, 64 per lane group.
+template <int WK>
+struct Turn {
+    static constexpr bool FP4 = is_fp4(WK), GROUPED = WK == ST_KIND_FP8_BLOCK128;
+    static constexpr int SS = 256, LK = 64;
+    static constexpr int CHUNKS = FP4 ? 2 : 4, CK = LK / CHUNKS;      // 16-byte chunks of a weight row per lane, elements of one
+    static constexpr int WSB = WK == ST_KIND_NVFP4 ? LK / 16 : is_mx(WK) ? LK / 32 : 0;
+    // Neighbouring chunks belong to one lane, so that its scales are adjacent; with a scale per 128 of K, chunk j of all lanes together is
+    // 64 of K instead, and a scale belongs to whole instructions.
+    static __device__ __forceinline__ uint32_t k_of(uint32_t q, uint32_t j) { return GROUPED ? 64 * j + 16 * q : LK * q + CK * j; }
+};
+
+// The codes and scales of a turn from k0 for NG groups of 16 weight rows; n[i]: this lane's row.  Zeros behind K's end.
+template <int WK, int NG>
+struct Codes {
+    using F = Turn<WK>;
+    u32x4 w[NG][F::CHUNKS];
+    uint32_t sc[NG];
     float gs[NG][2];
+
+    template <Ends END>
+    __device__ __forceinline__ void load(const Matrix (&mat)[NG], const uint32_t (&n)[NG], uint32_t k0, uint32_t K) {
+        const int q = (threadIdx.x & 63) >> 4;
+        const uint32_t w_row = F::FP4 ? K / 2 : K, ws_row = K / (WK == ST_KIND_NVFP4 ? 16 : 32), groups = (K + 127) / 128;
 #pragma unroll
-    for (int i = 0; i < NG; ++i) {
-        const uint8_t* pw = mat[i].w + uint64_t(n[i]) * w_row;
+        for (int i = 0; i < NG; ++i) {
+            const uint32_t to = (k0 + F::k_of(q, 0)) / (F::FP4 ? 2 : 1);
+            const uint8_t* pw = mat[i].w + uint64_t(n[i]) * w_row + to;
+            const int32_t left = END == WITHIN ? 0 : bytes_left(int64_t(w_row) - to);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint32_t k = k0 + F::k_of(q, j), to = F::FP4 ? k / 2 : k;
-            w[i][j] = load_piece<WHOLE>(pw + to, int64_t(w_row) - to);
-        }
-        if constexpr (F::WSB != 0) {
-            const uint32_t to = kq / (WK == ST_KIND_NVFP4 ? 16 : 32);
-            wsc[i] = load_scales<F::WSB, WHOLE>(mat[i].s + uint64_t(n[i]) * ws_row + to, int64_t(ws_row) - to);
-        }
-        if constexpr (F::GROUPED) {
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                const uint32_t kb = k0 / 128 + g < groups ? k0 / 128 + g : groups - 1;
-                gs[i][g] = reinterpret_cast<const float*>(mat[i].s)[uint64_t(n[i] / 128) * groups + kb];
+            for (int j = 0; j < F::CHUNKS; ++j) {
+                constexpr int STEP = F::GROUPED ? 64 : 16;      // bytes between a lane's chunks
+                w[i][j] = load_piece<END>(pw + STEP * j, left - STEP * j, w_row);
             }
-        }
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int h = 0; h < F::XL; ++h) {
-            xr[j][h] = u32x4{0, 0, 0, 0};
-            if constexpr (R != PLAIN) xl[j][h] = u32x4{0, 0, 0, 0};
-        }
-    if (have) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int h = 0; h < F::XL; ++h) {
-                const uint32_t k = k0 + F::k_of(q, j) + 8 * h;
-                xr[j][h] = load_piece<WHOLE>(px + uint64_t(k) * 2, (int64_t(K) - k) * 2);
-                if constexpr (R == TWO) xl[j][h] = load_piece<WHOLE>(pl + uint64_t(k) * 2, (int64_t(K) - k) * 2);
-                if constexpr (R == SPLIT) split_f16(xr[j][h], xr[j][h], xl[j][h]);
+            if constexpr (F::WSB != 0) {
+                const uint32_t to = (k0 + F::LK * q) / (WK == ST_KIND_NVFP4 ? 16 : 32);
+                sc[i] = uint32_t(load_scales<F::WSB, END == WITHIN>(mat[i].s + uint64_t(n[i]) * ws_row + to, int64_t(ws_row) - to));
             }
-    }
+            if constexpr (F::GROUPED) {
 #pragma unroll
-    for (int i = 0; i < NG; ++i) {
-        f32x4 c = acc[i];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (F::GROUPED && (j & 1) == 0) c = f32x4{0, 0, 0, 0};
-#pragma unroll
-            for (int h = 0; h < F::CK / 8; ++h) {
-                u32x4 wv;
-                if constexpr (WK == ST_KIND_NVFP4) {
-                    wv = codes8<F16, WK>(w[i][j][h], 0, scale_of<WK>(uint32_t(wsc[i] >> (8 * (2 * j + h / 2))) & 0xFF));
-                } else if constexpr (F::FP4) {
-                    wv = codes8<F16, WK>(w[i][j][h], 0, scale_of<WK>(uint32_t(wsc[i] >> (8 * j)) & 0xFF));
-                } else {
-                    const float s = F::WSB ? scale_of<WK>(uint32_t(wsc[i] >> (8 * (j / 2))) & 0xFF) : 1.0f;
-                    wv = codes8<F16, WK>(w[i][j][2 * h], w[i][j][2 * h + 1], s);
+                for (int g = 0; g < 2; ++g) {
+                    const uint32_t kb = k0 / 128 + g < groups ? k0 / 128 + g : groups - 1;
+                    gs[i][g] = reinterpret_cast<const float*>(mat[i].s)[uint64_t(n[i] / 128) * groups + kb];
                 }
-                c = mfma32<F16>(wv, xr[j][h], c);
-                if constexpr (R != PLAIN) c = mfma32<F16>(wv, xl[j][h], c);
-            }
-            // a group behind K's end has a sum of 0 and must not meet the last group's scale, which may be infinite
-            if (F::GROUPED && (j & 1) == 1 && (WHOLE || k0 + 64 * (j - 1) < K)) {
-#pragma unroll
-                for (int r = 0; r < 4; ++r) acc[i][r] = __builtin_fmaf(c[r], gs[i][j / 2], acc[i][r]);
             }
         }
-        if constexpr (!F::GROUPED) acc[i] = c;
     }
-}
+    // acc += the products with this lane's row at px (its second term at pl), with the scales of blocks.  Lanes that have no row are given
+    // another's: their columns of the result are not used.
+    // (PARTS of x at a time, which bounds the registers it takes)
+    template <bool F16, Rows R, Ends END, int PARTS>
+    __device__ __forceinline__ void times(const uint8_t* px, const uint8_t* pl, uint32_t k0, uint32_t K, f32x4 (&acc)[NG]) const {
+        const int q = (threadIdx.x & 63) >> 4;
+        constexpr int XL = F::CK / 8;
+        constexpr int HALF = F::CHUNKS / PARTS;
+        static_assert(PARTS == 1 || PARTS == 2, "a group of 128 is half a turn");
+        const uint64_t to = uint64_t(k0 + F::k_of(q, 0)) * 2;
+        const int32_t left = END == WITHIN ? 0 : bytes_left(int64_t(K) * 2 - int64_t(to));
+#pragma unroll
+        for (int half = 0; half < PARTS; ++half) {
+            u32x4 xr[HALF][XL], xl[R == PLAIN ? 1 : HALF][XL];
+#pragma unroll
+            for (int j = 0; j < HALF; ++j)
+#pragma unroll
+                for (int h = 0; h < XL; ++h) {
+                    const int at = 2 * (F::GROUPED ? 64 : F::CK) * (half * HALF + j) + 16 * h;
+                    xr[j][h] = load_piece<END>(px + to + at, left - at, 2 * K);
+                    if constexpr (R == TWO) xl[j][h] = load_piece<END>(pl + to + at, left - at, 2 * K);
+                    if constexpr (R == SPLIT) split_f16(xr[j][h], xr[j][h], xl[j][h]);
+                }
+#pragma unroll
+            for (int i = 0; i < NG; ++i) {
+                f32x4 c = F::GROUPED ? f32x4{0, 0, 0, 0} : acc[i];
+#pragma unroll
+                for (int b = 0; b < HALF; ++b) {
+                    const int j = half * HALF + b;
+#pragma unroll
+                    for (int h = 0; h < XL; ++h) {
+                        u32x4 wv;
+                        if constexpr (WK == ST_KIND_NVFP4) wv = codes8<F16, WK>(w[i][j][h], 0, scale_of<WK>(sc[i] >> (8 * (2 * j + h / 2)) & 0xFF));
+                        else if constexpr (F::FP4) wv = codes8<F16, WK>(w[i][j][h], 0, scale_of<WK>(sc[i] >> (8 * j) & 0xFF));
+                        else wv = codes8<F16, WK>(w[i][j][2 * h], w[i][j][2 * h + 1], F::WSB ? scale_of<WK>(sc[i] >> (8 * (j / 2)) & 0xFF) : 1.0f);
+                        c = mfma32<F16>(wv, xr[b][h], c);
+                        if constexpr (R != PLAIN) c = mfma32<F16>(wv, xl[b][h], c);
+                    }
+                    // a group of 128 behind K's end has a sum of 0 and must not meet the last group's scale, which may be infinite
+                    if (F::GROUPED && (j & 1) == 1) {
+                        if (END == WITHIN || k0 + 64 * (j - 1) < K) {
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) acc[i][r] = __builtin_fmaf(c[r], gs[i][j / 2], acc[i][r]);
+                        }
+                        c = f32x4{0, 0, 0, 0};
+                    }
+                }
+                if constexpr (!F::GROUPED) acc[i] = c;
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+};
 
 // h of columns n..n+3 of pair p, from the sums of gate and up.
 template <int WK>
@@ -162,52 +229,237 @@ __device__ __forceinline__ void store_y(const Args& a, uint32_t t, uint32_t n, f
     }
 }
 
-// The expert of this workgroup's slot, or -1.
-__device__ __forceinline__ int32_t expert_of(const Args& a, uint32_t slot) {
-    const int32_t e = a.by_pair ? a.ids[slot] : int32_t(slot);
-    return e >= 0 && uint32_t(e) < a.experts ? __builtin_amdgcn_readfirstlane(e) : -1;
+// The k-th expert that has pairs and its part of the sorted list; no pairs: there is none.
+struct Entry {
+    uint32_t expert, count;
+    const uint32_t* pairs;
+};
+__device__ __forceinline__ Entry entry_of(const Args& a, uint32_t k) {
+    if (k >= a.sorted[0]) return Entry{0, 0, nullptr};
+    const uint32_t* e = a.sorted + 4 + 4 * k;
+    return Entry{e[0], e[2], a.sorted + 4 + 4 * a.slots + e[1]};
+}
+
+// ------------------------------------------------------------------------- one token
+
+// As linear_one (linear_kernels.h).  A lane's 16 bytes of a weight row hold E elements of K; its part of x stays in registers for R rows.
+template <int WK>
+struct One {
+    static constexpr bool FP4 = is_fp4(WK), GROUPED = WK == ST_KIND_FP8_BLOCK128;
+    static constexpr int E = FP4 ? 32 : 16;
+};
+// One row's 16 bytes and scale codes from element k of K; zeros behind its end.
+template <int WK>
+__device__ __forceinline__ void load_row(const uint8_t* pw, const uint8_t* ps, uint32_t k, uint32_t K, u32x4& w, uint32_t& sc) {
+    using O = One<WK>;
+    const uint32_t at = O::FP4 ? k / 2 : k, row = O::FP4 ? K / 2 : K;
+    w = u32x4{0, 0, 0, 0};
+    sc = 0;
+    if (k + O::E <= K) {
+        w = *reinterpret_cast<const u32x4_any*>(pw + at);
+        if constexpr (WK == ST_KIND_NVFP4) sc = *reinterpret_cast<const u16_any*>(ps + k / 16);
+    } else if (k < K) {
+        w = load_end(pw + at, bytes_left(int64_t(row) - at), row);
+        if constexpr (WK == ST_KIND_NVFP4) sc = ps[k / 16];
+    }
+    if constexpr (is_mx(WK)) sc = k < K ? ps[k / 32] : 0;
+}
+// Its products with E elements of a row in one or two terms, the scales of blocks of 16 and 32 applied.
+template <int WK, bool F16, bool TERMS>
+__device__ __forceinline__ float dot_row(u32x4 w, uint32_t sc, const uint32_t* x, const uint32_t* xl) {
+    using O = One<WK>;
+    float sum = 0.0f;
+#pragma unroll
+    for (int b = 0; b < O::E / 16; ++b) {
+        u32x4 v[2];
+        const float s = is_mx(WK) ? scale_of<WK>(sc) : 1.0f;
+        if constexpr (WK == ST_KIND_NVFP4) {
+            // the codes alone (exact in bf16 and fp16): the block's sum takes the scale
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if constexpr (F16) {
+                    v[h][0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w[2 * b + h], 1.0f, 0));
+                    v[h][1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w[2 * b + h], 1.0f, 1));
+                    v[h][2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w[2 * b + h], 1.0f, 2));
+                    v[h][3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w[2 * b + h], 1.0f, 3));
+                } else {
+                    v[h] = codes8<false, ST_KIND_MXFP4>(w[2 * b + h], 0, 1.0f);
+                }
+            }
+        } else if constexpr (O::FP4) {
+            v[0] = codes8<F16, WK>(w[2 * b], 0, s);
+            v[1] = codes8<F16, WK>(w[2 * b + 1], 0, s);
+        } else {
+            v[0] = codes8<F16, WK>(w.x, w.y, s);
+            v[1] = codes8<F16, WK>(w.z, w.w, s);
+        }
+        float d = WK == ST_KIND_NVFP4 ? 0.0f : sum;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            d = dot2<F16>(v[i / 4][i % 4], x[8 * b + i], d);
+            if constexpr (TERMS) d = dot2<F16>(v[i / 4][i % 4], xl[8 * b + i], d);
+        }
+        if constexpr (WK == ST_KIND_NVFP4) sum = __builtin_fmaf(d, scale_of<WK>(sc >> (8 * b) & 0xFF), sum);
+        else sum = d;
+    }
+    return sum;
+}
+// E elements of a bf16 or fp16 row from element k of K as pairs, zeros behind its end.
+template <int E>
+__device__ __forceinline__ void load_pairs(const uint8_t* p, uint32_t k, uint32_t K, uint32_t* x) {
+#pragma unroll
+    for (int h = 0; h < E / 8; ++h) {
+        const uint32_t at = k + 8 * h;
+        u32x4 c = {0, 0, 0, 0};
+        if (k + E <= K) c = *reinterpret_cast<const u32x4_any*>(p + uint64_t(at) * 2);
+        else if (at < K) c = load_end(p + uint64_t(at) * 2, bytes_left((int64_t(K) - at) * 2), 2 * K);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[4 * h + j] = c[j];
+    }
+}
+
+constexpr int kOneMaxWaves = 8, kOneColumns = 4;
+
+// Columns 4 * blockIdx.x .. + 3 of h of pair blockIdx.y: four rows of gate and four of up.
+template <int X, int WK>
+__global__ __launch_bounds__(64 * kOneMaxWaves) void up_one(Args a) {
+    using O = One<WK>;
+    using D = Dense<X, WK>;
+    constexpr int R = 2 * kOneColumns, PAIRS = O::E / 2;
+    __shared__ __align__(16) float joined[kOneMaxWaves][R];
+    const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
+    const int32_t e = __builtin_amdgcn_readfirstlane(a.ids[blockIdx.y]);
+    if (e < 0 || uint32_t(e) >= a.experts) return;
+    const Matrix mat[2] = {matrix_of(a, e, 0), matrix_of(a, e, 1)};
+    const uint32_t n0 = blockIdx.x * kOneColumns, w_row = O::FP4 ? a.k / 2 : a.k, ws_row = a.k / (WK == ST_KIND_NVFP4 ? 16 : 32);
+    const uint32_t groups = (a.k + 127) / 128;
+    float acc[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) acc[r] = 0.0f;
+    for (uint32_t k0 = wave * 64 * O::E; k0 < a.k; k0 += waves * 64 * O::E) {
+        const uint32_t k = k0 + lane * O::E;
+        u32x4 w[R];
+        uint32_t sc[R];
+        // rows past the last are read as the last one; nothing of them is stored
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const uint32_t n = n0 + r % kOneColumns < a.i ? n0 + r % kOneColumns : a.i - 1;
+            const Matrix& m = mat[r / kOneColumns];
+            load_row<WK>(m.w + uint64_t(n) * w_row, m.s + uint64_t(n) * ws_row, k, a.k, w[r], sc[r]);
+        }
+        uint32_t x[PAIRS], xl[D::SPLIT ? PAIRS : 1];
+        load_pairs<O::E>(a.x, k, a.k, x);
+        if constexpr (D::SPLIT) {
+#pragma unroll
+            for (int h = 0; h < PAIRS / 4; ++h) {
+                u32x4 hi, lo;
+                split_f16(u32x4{x[4 * h], x[4 * h + 1], x[4 * h + 2], x[4 * h + 3]}, hi, lo);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[4 * h + j] = hi[j], xl[4 * h + j] = lo[j];
+            }
+        }
+        float f[2] = {1.0f, 1.0f};          // the lane's fp32 scales, where the kinds have one per 128 of K
+        if constexpr (O::GROUPED) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) f[i] = k < a.k ? reinterpret_cast<const float*>(mat[i].s)[uint64_t(n0 / 128) * groups + k / 128] : 0.0f;
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const float d = dot_row<WK, D::F16, D::SPLIT>(w[r], sc[r], x, xl);
+            acc[r] = O::GROUPED ? __builtin_fmaf(d, f[r / kOneColumns], acc[r]) : acc[r] + d;
+        }
+    }
+    const float v = fold<R>(acc);
+    if (lane < R) joined[wave][lane] = v;
+    __syncthreads();
+    if (threadIdx.x == 0) {                // the slices in their order
+        f32x4 g = {0, 0, 0, 0}, u = {0, 0, 0, 0};
+        for (uint32_t o = 0; o < waves; ++o) {
+            g += *reinterpret_cast<const f32x4*>(joined[o]);
+            u += *reinterpret_cast<const f32x4*>(joined[o] + kOneColumns);
+        }
+        store_h<WK>(a, blockIdx.y, n0, g, u, tensor_scale<WK>(mat[0]), tensor_scale<WK>(mat[1]));
+    }
+}
+
+// Columns 4 * blockIdx.x .. + 3 of y: lane c of all the workgroup's lanes has chunks c, c + threads, ... of the pairs' rows, one after the
+// other; its products take its own pair's weight and scales, and the sum over lanes is the sum over pairs.
+template <int WK>
+__global__ __launch_bounds__(64 * kOneMaxWaves) void down_one(Args a) {
+    using O = One<WK>;
+    constexpr int R = kOneColumns, PAIRS = O::E / 2;
+    __shared__ __align__(16) float joined[kOneMaxWaves][R];
+    const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
+    const uint32_t n0 = blockIdx.x * R, w_row = O::FP4 ? a.i / 2 : a.i, ws_row = a.i / (WK == ST_KIND_NVFP4 ? 16 : 32), groups = (a.i + 127) / 128;
+    const uint32_t chunks = (a.i + O::E - 1) / O::E;
+    const uint64_t plane = uint64_t(a.pairs) * a.h_pitch * 2;
+    float acc[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) acc[r] = 0.0f;
+    for (uint32_t c = threadIdx.x; c < a.pairs * chunks; c += blockDim.x) {
+        const uint32_t p = c / chunks, k = c % chunks * O::E;
+        const int32_t e = a.ids[p];
+        if (e < 0 || uint32_t(e) >= a.experts) continue;
+        const Matrix m = matrix_of(a, e, 2);
+        u32x4 w[R];
+        uint32_t sc[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const uint32_t n = n0 + r < a.n ? n0 + r : a.n - 1;
+            load_row<WK>(m.w + uint64_t(n) * w_row, m.s + uint64_t(n) * ws_row, k, a.i, w[r], sc[r]);
+        }
+        uint32_t x[PAIRS], xl[PAIRS];
+        const uint8_t* ph = a.h + uint64_t(p) * a.h_pitch * 2;
+        load_pairs<O::E>(ph, k, a.i, x);
+        load_pairs<O::E>(ph + plane, k, a.i, xl);
+        float f = a.weights[p] * tensor_scale<WK>(m);
+        if constexpr (O::GROUPED) f *= reinterpret_cast<const float*>(m.s)[uint64_t(n0 / 128) * groups + k / 128];
+#pragma unroll
+        for (int r = 0; r < R; ++r) acc[r] = __builtin_fmaf(dot_row<WK, false, true>(w[r], sc[r], x, xl), f, acc[r]);
+    }
+    const float v = fold<R>(acc);
+    if (lane < R) joined[wave][lane] = v;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        f32x4 t = {0, 0, 0, 0};
+        for (uint32_t o = 0; o < waves; ++o) t += *reinterpret_cast<const f32x4*>(joined[o]);
+        store_y(a, 0, n0, t);
+    }
 }
 
 // ------------------------------------------------------------------------- up to 16 tokens
 
-constexpr int up_waves(int wk) { return is_fp4(wk) ? 4 : 8; }
+constexpr int kUpWaves = 4;
+constexpr uint32_t kFewPairs = 512;
 
-template <int X, int WK>
-__global__ __launch_bounds__(64 * up_waves(WK)) void up_few(Args a) {
-    using F = Few<ST_X_BF16, WK>;
+template <int X, int WK, Ends TAIL>
+__global__ __launch_bounds__(64 * kUpWaves) void up_few(Args a) {
+    using F = Turn<WK>;
     using D = Dense<X, WK>;
     constexpr Rows R = D::SPLIT ? SPLIT : PLAIN;
-    __shared__ __align__(16) float joined[up_waves(WK)][2][256];
-    __shared__ uint16_t list[kFewTokens * kMaxTop];
-    __shared__ uint32_t found;
-    const int lane = threadIdx.x & 63, row = lane & 15, q = lane >> 4;
+    __shared__ __align__(16) float joined[kUpWaves][2][256];
+    const uint32_t lane = threadIdx.x & 63, row = lane & 15, q = lane >> 4;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
-    const uint32_t n0 = blockIdx.x * 16, slot = blockIdx.y;
-    const int32_t e = expert_of(a, slot);
-    if (e < 0) return;
-    if (wave == 0) {
-        uint32_t count = 0;
-        for (uint32_t p = 0; p < a.pairs; p += 64) {
-            const bool mine = p + lane < a.pairs && a.ids[p + lane] == e;
-            const uint64_t m = __ballot(mine);
-            if (mine) list[count + __popcll(m & ((uint64_t(1) << lane) - 1))] = uint16_t(p + lane);
-            count += __popcll(m);
-        }
-        if (lane == 0) found = count;
-    }
-    const Matrix mat[2] = {matrix_of(a, e, 0), matrix_of(a, e, 1)};
-    __syncthreads();
-    const uint32_t count = found;
-    if (count == 0 || (a.by_pair && list[0] != slot)) return;
+    const uint32_t n0 = blockIdx.x * 16;
+    const Entry en = entry_of(a, blockIdx.y);
+    if (en.count == 0) return;
+    const Matrix mat[2] = {matrix_of(a, en.expert, 0), matrix_of(a, en.expert, 1)};
     const uint32_t at = n0 + row < a.i ? n0 + row : a.i - 1, n[2] = {at, at};
-    for (uint32_t c0 = 0; c0 < count; c0 += 16) {
-        const bool have = c0 + row < count;
-        const uint32_t p = list[have ? c0 + row : c0];
+    // 16 pairs at a time; those of an expert that has more meet its weights again, from L2
+    for (uint32_t c0 = 0; c0 < en.count; c0 += 16) {
+        const bool have = c0 + row < en.count;
+        const uint32_t p = en.pairs[have ? c0 + row : c0];
         const uint8_t* px = a.x + uint64_t(p / a.top) * a.x_pitch * 2;
         f32x4 acc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
         for (uint32_t k0 = wave * F::SS; k0 < a.k; k0 += waves * F::SS) {
-            if (k0 + F::SS <= a.k) turn<WK, D::F16, R, true, 2>(mat, n, px, nullptr, have, k0, a.k, acc);
-            else turn<WK, D::F16, R, false, 2>(mat, n, px, nullptr, have, k0, a.k, acc);
+            auto turn = [&](auto ending) {
+                constexpr Ends END = decltype(ending)::value;
+                Codes<WK, 2> codes;
+                codes.template load<END>(mat, n, k0, a.k);
+                codes.template times<D::F16, R, END, 2>(px, nullptr, k0, a.k, acc);
+            };
+            if (k0 + F::SS <= a.k) turn(Ending<WITHIN>{});
+            else turn(Ending<TAIL>{});
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) *reinterpret_cast<f32x4*>(&joined[wave][i][lane * 4]) = acc[i];
@@ -225,18 +477,18 @@ __global__ __launch_bounds__(64 * up_waves(WK)) void up_few(Args a) {
     }
 }
 
-// Entries: each expert that some token has; a second one for tokens that have it twice, and so on.  Row t of an entry is token t's pair, or none.
-constexpr int kDownWaves = 8;
-static_assert(kFewTokens * kMaxTop <= 64 * kDownWaves, "a thread for each pair");
+// Entries: each expert that some token has; a second one for tokens that have it twice, and so on.  An entry's tokens are bits of a mask,
+// their pairs a part of `list` in the tokens' order.
+constexpr int kDownWaves = 16;
+static_assert(kFewPairs <= 64 * kDownWaves, "a thread for each pair");
 
-template <int WK, int NG>
+template <int WK, int NG, Ends TAIL>
 __global__ __launch_bounds__(64 * kDownWaves) void down_few(Args a) {
-    using F = Few<ST_X_BF16, WK>;
-    constexpr uint32_t MAX = kFewTokens * kMaxTop;
-    constexpr uint16_t NONE = 0xFFFF;
+    using F = Turn<WK>;
     __shared__ __align__(16) float joined[kDownWaves][NG][256];
-    __shared__ uint32_t key[MAX];
-    __shared__ uint16_t entry[MAX], expert[MAX], pair[MAX][kFewTokens];
+    __shared__ __align__(16) uint32_t key[64 * kDownWaves];
+    __shared__ uint32_t mask[64 * kDownWaves];
+    __shared__ uint16_t entry[kFewPairs], expert[kFewPairs], list[kFewPairs], base[kFewPairs];
     __shared__ uint32_t leaders[kDownWaves];
     const int lane = threadIdx.x & 63, row = lane & 15, q = lane >> 4;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), p = threadIdx.x;
@@ -251,11 +503,14 @@ __global__ __launch_bounds__(64 * kDownWaves) void down_few(Args a) {
         mine = uint32_t(id) * kMaxTop + again;
     }
     key[p] = mine;
-    for (uint32_t i = p; i < MAX * kFewTokens / 2; i += 64 * kDownWaves) reinterpret_cast<uint32_t*>(pair)[i] = 0xFFFFFFFFu;
+    mask[p] = 0;
     __syncthreads();
     uint32_t first = p;
-    for (uint32_t o = a.pairs; o-- > 0;)
-        if (o < p && key[o] == mine) first = o;
+    for (uint32_t o = 0; valid && o < p; o += 4) {
+        const u32x4 k = *reinterpret_cast<const u32x4*>(&key[o]);
+#pragma unroll
+        for (uint32_t i = 0; i < 4; ++i) first = k[i] == mine && o + i < first ? o + i : first;
+    }
     const bool leads = valid && first == p;
     const uint64_t m = __ballot(leads);
     if (lane == 0) leaders[wave] = __popcll(m);
@@ -272,7 +527,16 @@ __global__ __launch_bounds__(64 * kDownWaves) void down_few(Args a) {
         expert[at] = uint16_t(id);
     }
     __syncthreads();
-    if (valid) pair[entry[first]][p / a.top] = uint16_t(p);
+    const uint32_t t = p / a.top, en0 = valid ? entry[first] : 0;
+    if (valid) atomicOr(&mask[en0], 1u << t);
+    __syncthreads();
+    if (p < entries) {
+        uint32_t b = 0;
+        for (uint32_t o = 0; o < p; ++o) b += __popc(mask[o]);
+        base[p] = uint16_t(b);
+    }
+    __syncthreads();
+    if (valid) list[base[en0] + __popc(mask[en0] & ((1u << t) - 1))] = uint16_t(p);
     __syncthreads();
 
     uint32_t n[NG];
@@ -288,21 +552,28 @@ __global__ __launch_bounds__(64 * kDownWaves) void down_few(Args a) {
     const uint64_t plane = uint64_t(a.pairs) * a.h_pitch * 2;
     for (uint32_t item = wave; item < items; item += kDownWaves) {
         const uint32_t en = item / turns, k0 = item % turns * F::SS;
-        const uint32_t e = __builtin_amdgcn_readfirstlane(expert[en]);
-        const uint16_t pr = pair[en][row];
-        const bool have = pr != NONE;
+        const uint32_t e = __builtin_amdgcn_readfirstlane(expert[en]), has = mask[en];
+        const bool have = has >> row & 1;
+        const uint32_t pr = list[base[en] + (have ? __popc(has & ((1u << row) - 1)) : 0)];
+        const float weight = a.weights[pr];
+        const uint8_t* ph = a.h + uint64_t(pr) * a.h_pitch * 2;
         Matrix mat[NG];
         mat[0] = matrix_of(a, e, 2);
 #pragma unroll
         for (int i = 1; i < NG; ++i) mat[i] = mat[0];
-        const uint8_t* ph = a.h + uint64_t(have ? pr : 0) * a.h_pitch * 2;
         f32x4 acc[NG];
 #pragma unroll
         for (int i = 0; i < NG; ++i) acc[i] = f32x4{0, 0, 0, 0};
-        if (k0 + F::SS <= a.i) turn<WK, false, TWO, true, NG>(mat, n, ph, ph + plane, have, k0, a.i, acc);
-        else turn<WK, false, TWO, false, NG>(mat, n, ph, ph + plane, have, k0, a.i, acc);
+        auto turn = [&](auto ending) {
+            constexpr Ends END = decltype(ending)::value;
+            Codes<WK, NG> codes;
+            codes.template load<END>(mat, n, k0, a.i);
+            codes.template times<false, TWO, END, NG>(ph, ph + plane, k0, a.i, acc);
+        };
+        if (k0 + F::SS <= a.i) turn(Ending<WITHIN>{});
+        else turn(Ending<TAIL>{});
         if (have) {
-            const float f = a.weights[pr] * tensor_scale<WK>(mat[0]);
+            const float f = weight * tensor_scale<WK>(mat[0]);
 #pragma unroll
             for (int i = 0; i < NG; ++i)
 #pragma unroll
@@ -324,64 +595,18 @@ __global__ __launch_bounds__(64 * kDownWaves) void down_few(Args a) {
 
 constexpr int kTileRows = 64, kTileK = 128, kTileThreads = 256;
 
-// The first pairs of expert e from `from` on, at most kTileRows, in their order: list, and their number.  All threads take part; ids are
-// read 16 per thread at a time.
-struct Found {
-    uint32_t list[kTileRows];
-    uint32_t sums[kTileThreads / 64];
-};
-__device__ __forceinline__ uint32_t find(const Args& a, int32_t e, uint32_t from, Found& f) {
-    const uint32_t tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    uint32_t count = 0;
-    for (uint32_t base = from; base < a.pairs && count < kTileRows; base += 16 * kTileThreads) {
-        const uint32_t p0 = base + tid * 16;
-        uint32_t hits = 0;
-        if (p0 + 16 <= a.pairs) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const u32x4 v = *reinterpret_cast<const u32x4_any*>(a.ids + p0 + 4 * c);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) hits |= int32_t(v[i]) == e ? 1u << (4 * c + i) : 0;
-            }
-        } else {
-            for (uint32_t i = 0; i < 16 && p0 + i < a.pairs; ++i) hits |= a.ids[p0 + i] == e ? 1u << i : 0;
-        }
-        uint32_t upto = __popc(hits);          // of the lanes up to this one
-#pragma unroll
-        for (int o = 1; o < 64; o *= 2) {
-            const uint32_t w = __shfl_up(upto, o);
-            upto += lane >= uint32_t(o) ? w : 0;
-        }
-        __syncthreads();                       // the last turn's sums have been read
-        if (lane == 63) f.sums[wave] = upto;
-        __syncthreads();
-        uint32_t at = count + upto - __popc(hits);
-#pragma unroll
-        for (uint32_t o = 0; o < kTileThreads / 64; ++o) {
-            at += o < wave ? f.sums[o] : 0;
-            count += f.sums[o];
-        }
-        while (hits && at < kTileRows) {
-            f.list[at++] = p0 + __builtin_ctz(hits);
-            hits &= hits - 1;
-        }
-    }
-    __syncthreads();
-    return count < kTileRows ? count : kTileRows;
-}
-
 // UP: 64 rows of gate and of up; else 128 rows of down.
-template <int WK, bool F16, Rows R, bool UP>
+template <int WK, bool F16, Rows R, bool UP, Ends TAIL>
 __global__ __launch_bounds__(kTileThreads, 2) void tile(Args a) {
     constexpr bool FP4 = is_fp4(WK), MX = is_mx(WK), GROUPED = WK == ST_KIND_FP8_BLOCK128;
     constexpr int PLANES = R == PLAIN ? 1 : 2, MT = kTileRows / 16, WC = FP4 ? 1 : 2;    // 16-byte chunks of a weight row per lane and step
     constexpr int PER = kTileRows * (kTileK / 8) / kTileThreads;                          // 16-byte chunks of x per thread, step and plane
     __shared__ __align__(16) uint8_t lds[2][PLANES][kTileRows * kTileK * 2];
-    __shared__ Found found;
     const int tid = threadIdx.x, lane = tid & 63, row = lane & 15, q = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int32_t e = expert_of(a, blockIdx.y);
-    if (e < 0) return;
+    const Entry en = entry_of(a, blockIdx.y);
+    if (en.count == 0) return;
+    const uint32_t e = en.expert;
     const uint32_t K = UP ? a.k : a.i, N = UP ? a.i : a.n;
     const uint32_t n0 = UP ? blockIdx.x * 64 + wave * 16 : blockIdx.x * 128 + wave * 32;
     Matrix mat[2];
@@ -396,15 +621,16 @@ __global__ __launch_bounds__(kTileThreads, 2) void tile(Args a) {
     const uint32_t w_row = FP4 ? K / 2 : K, ws_row = K / (WK == ST_KIND_NVFP4 ? 16 : 32), groups = (K + 127) / 128, steps = (K + kTileK - 1) / kTileK;
     const uint64_t plane = uint64_t(a.pairs) * a.h_pitch * 2;
 
-    for (uint32_t from = 0;;) {
-        const uint32_t count = find(a, e, from, found);
-        if (count == 0 || (a.by_pair && from == 0 && found.list[0] != blockIdx.y)) return;
+    for (uint32_t from = 0; from < en.count; from += kTileRows) {
+        const uint32_t count = en.count - from < kTileRows ? en.count - from : kTileRows;
+        const uint32_t* list = en.pairs + from;
+        if (from) __syncthreads();
         const int mt = int(count + 15) / 16;
         // chunk c of row r of a step sits at c ^ (r & 15)
         const uint8_t* src[PER];
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const uint32_t r = (i * kTileThreads + tid) / 16, p = found.list[r < count ? r : 0];
+            const uint32_t r = (i * kTileThreads + tid) / 16, p = list[r < count ? r : 0];
             src[i] = UP ? a.x + uint64_t(p / a.top) * a.x_pitch * 2 : a.h + uint64_t(p) * a.h_pitch * 2;
         }
         const uint32_t c = tid % 16;
@@ -420,7 +646,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void tile(Args a) {
                 for (int j = 0; j < WC; ++j) {
                     const uint32_t k = k0 + (FP4 ? 32 * q : 64 * j + 16 * q), to = FP4 ? k / 2 : k;
                     const uint8_t* p = mat[i].w + uint64_t(n[i]) * w_row + to;
-                    rw[i][j] = whole ? u32x4(*reinterpret_cast<const u32x4_any*>(p)) : load_chunk(p, int64_t(w_row) - to);
+                    rw[i][j] = whole ? load_piece<WITHIN>(p, 16, w_row) : load_piece<TAIL>(p, bytes_left(int64_t(w_row) - to), w_row);
                     if constexpr (WK == ST_KIND_NVFP4) {
                         const uint8_t* ps = mat[i].s + uint64_t(n[i]) * ws_row + k / 16;
                         rs[i][j] = whole ? *reinterpret_cast<const u16_any*>(ps) : load_codes(ps, int64_t(ws_row) - k / 16, 2);
@@ -434,9 +660,9 @@ __global__ __launch_bounds__(kTileThreads, 2) void tile(Args a) {
             for (int i = 0; i < PER; ++i) {
                 if ((i * kTileThreads + tid) / 16 >= uint32_t(16 * mt)) continue;
                 const uint8_t* p = src[i] + (uint64_t(k0) + 8 * c) * 2;
-                const int64_t avail = (int64_t(K) - k0 - 8 * c) * 2;
-                rx[0][i] = whole ? u32x4(*reinterpret_cast<const u32x4_any*>(p)) : load_chunk(p, avail);
-                if constexpr (R == TWO) rx[1][i] = whole ? u32x4(*reinterpret_cast<const u32x4_any*>(p + plane)) : load_chunk(p + plane, avail);
+                const int32_t avail = bytes_left((int64_t(K) - k0 - 8 * c) * 2);
+                rx[0][i] = whole ? load_piece<WITHIN>(p, 16, 2 * K) : load_piece<TAIL>(p, avail, 2 * K);
+                if constexpr (R == TWO) rx[1][i] = whole ? load_piece<WITHIN>(p + plane, 16, 2 * K) : load_piece<TAIL>(p + plane, avail, 2 * K);
             }
         };
         auto commit = [&](int buf) {
@@ -502,7 +728,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void tile(Args a) {
 #pragma unroll
         for (int j = 0; j < MT; ++j) {
             if (uint32_t(16 * j + row) >= count) continue;
-            const uint32_t p = found.list[16 * j + row];
+            const uint32_t p = list[16 * j + row];
             if constexpr (UP) {
                 store_h<WK>(a, p, n0 + 4 * q, acc[0][j], acc[1][j], s0, s1);
             } else {
@@ -518,10 +744,15 @@ __global__ __launch_bounds__(kTileThreads, 2) void tile(Args a) {
                 }
             }
         }
-        if (count < kTileRows) return;
-        from = found.list[kTileRows - 1] + 1;
-        __syncthreads();
     }
+}
+
+// go(kernel's Ends) for rows of K: those of the MX kinds always end on 16 bytes.
+template <int WK, class F>
+void by_end(uint32_t K, F go) {
+    if constexpr (is_mx(WK)) return go(Ending<EVEN>{});
+    else if ((is_fp4(WK) ? K / 2 : K) % 16 == 0) return go(Ending<EVEN>{});
+    else return go(Ending<ODD>{});
 }
 
 }  // namespace

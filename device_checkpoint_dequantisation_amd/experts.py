@@ -33,8 +33,8 @@ class MoeExperts:
         gate, up, down = list(gate), list(up), list(down)
         if not (gate and len(gate) == len(up) == len(down)):
             raise ValueError(f"{who}: {len(gate)} gates, {len(up)} ups and {len(down)} downs; one of each is needed for every expert")
-        if len(gate) > 32767:
-            raise ValueError(f"{who}: {len(gate)} experts; at most 32767 are possible")
+        if len(gate) > 16384:
+            raise ValueError(f"{who}: {len(gate)} experts; at most 16384 are possible")
         self.shape = _check_weight(gate[0], who)
         self.width, self.kind, self.down_kind = _check_weight(down[0], who)[0], gate[0].kind, down[0].kind
         i, k = self.shape
