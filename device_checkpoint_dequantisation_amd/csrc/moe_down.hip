@@ -82,7 +82,7 @@ void launch(const Args& a, Cut cut, hipStream_t s) {
             case FEW: hipLaunchKernelGGL((down_few<WK, NG, END>), grid, block, 0, s, a); break;
             case SOME:
             case MANY: {
-                hipLaunchKernelGGL((tile<WK, false, TWO, false, END>), dim3((a.n + 127) / 128, a.slots), dim3(kTileThreads), 0, s, a);
+                hipLaunchKernelGGL((tile<WK, false, TWO, false, down_k(WK), END>), dim3((a.n + 127) / 128, a.slots), dim3(kTileThreads), 0, s, a);
                 const uint64_t items = uint64_t((a.n + 3) / 4) * a.t;
                 hipLaunchKernelGGL(combine, dim3(uint32_t((items + 255) / 256)), dim3(256), 0, s, a);
             }

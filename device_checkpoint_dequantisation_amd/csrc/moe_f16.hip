@@ -18,7 +18,7 @@ void launch(const Args& a, Cut cut, hipStream_t s) {
             case FEW:
             case SOME: hipLaunchKernelGGL((up_few<ST_X_F16, WK, END>), few, block, 0, s, a); break;
             case MANY:
-                hipLaunchKernelGGL((tile<WK, D::F16, D::SPLIT ? SPLIT : PLAIN, true, END>), dim3((a.i + 63) / 64, a.slots), dim3(kTileThreads), 0, s, a);
+                hipLaunchKernelGGL((tile<WK, D::F16, D::SPLIT ? SPLIT : PLAIN, true, kUpK, END>), dim3((a.i + 63) / 64, a.slots), dim3(kTileThreads), 0, s, a);
                 break;
         }
     });

@@ -593,15 +593,21 @@ __global__ __launch_bounds__(64 * kDownWaves) void down_few(Args a) {
 
 // ------------------------------------------------------------------------- more tokens
 
-constexpr int kTileRows = 64, kTileK = 128, kTileThreads = 256;
+constexpr int kTileRows = 64, kTileThreads = 256, kUpK = 128;
+// Steps of K (40 tokens through MXFP4's down [5120, 1280]: 46 us with 128, 64 with 64; 320 through block FP8's [4096, 1280]: 237 and 223)
+constexpr int down_k(int wk) { return is_fp4(wk) ? 128 : 64; }
 
 // UP: 64 rows of gate and of up; else 128 rows of down.
-template <int WK, bool F16, Rows R, bool UP, Ends TAIL>
-__global__ __launch_bounds__(kTileThreads, 2) void tile(Args a) {
+template <int WK, bool F16, Rows R, bool UP, int TK, Ends TAIL>
+__global__ __launch_bounds__(kTileThreads, R == TWO && TK == 128 ? 2 : 3) void tile(Args a) {
     constexpr bool FP4 = is_fp4(WK), MX = is_mx(WK), GROUPED = WK == ST_KIND_FP8_BLOCK128;
-    constexpr int PLANES = R == PLAIN ? 1 : 2, MT = kTileRows / 16, WC = FP4 ? 1 : 2;    // 16-byte chunks of a weight row per lane and step
-    constexpr int PER = kTileRows * (kTileK / 8) / kTileThreads;                          // 16-byte chunks of x per thread, step and plane
-    __shared__ __align__(16) uint8_t lds[2][PLANES][kTileRows * kTileK * 2];
+    constexpr int PLANES = R == PLAIN ? 1 : 2, MT = kTileRows / 16;
+    constexpr int WC = TK == 128 && !FP4 ? 2 : 1, WB = FP4 ? TK / 8 : 16;     // chunks of a weight row per lane and step, bytes of one
+    constexpr int OPS = TK / 32;                                              // instructions of a step for 16 x 16 results
+    constexpr int XC = TK / 8, PER = kTileRows * XC / kTileThreads;           // 16-byte chunks of a row of x per step; per thread and plane
+    __shared__ __align__(16) uint8_t lds[2][PLANES][kTileRows * TK * 2];
+    // chunk c of row r of a step sits at c ^ swizzle(r): 16 lanes reading one chunk of 16 rows touch all banks once
+    auto place = [](uint32_t r, uint32_t c) { return (r * XC + (c ^ (XC == 16 ? r & 15 : r >> 1 & 7))) * 16; };
     const int tid = threadIdx.x, lane = tid & 63, row = lane & 15, q = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const Entry en = entry_of(a, blockIdx.y);
@@ -618,7 +624,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void tile(Args a) {
         const uint32_t r = n0 + (UP ? 0 : 16 * i) + row;
         n[i] = r < N ? r : N - 1;
     }
-    const uint32_t w_row = FP4 ? K / 2 : K, ws_row = K / (WK == ST_KIND_NVFP4 ? 16 : 32), groups = (K + 127) / 128, steps = (K + kTileK - 1) / kTileK;
+    const uint32_t w_row = FP4 ? K / 2 : K, ws_row = K / (WK == ST_KIND_NVFP4 ? 16 : 32), groups = (K + 127) / 128, steps = (K + TK - 1) / TK;
     const uint64_t plane = uint64_t(a.pairs) * a.h_pitch * 2;
 
     for (uint32_t from = 0; from < en.count; from += kTileRows) {
@@ -626,39 +632,45 @@ __global__ __launch_bounds__(kTileThreads, 2) void tile(Args a) {
         const uint32_t* list = en.pairs + from;
         if (from) __syncthreads();
         const int mt = int(count + 15) / 16;
-        // chunk c of row r of a step sits at c ^ (r & 15)
         const uint8_t* src[PER];
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const uint32_t r = (i * kTileThreads + tid) / 16, p = list[r < count ? r : 0];
+            const uint32_t r = (i * kTileThreads + tid) / XC, p = list[r < count ? r : 0];
             src[i] = UP ? a.x + uint64_t(p / a.top) * a.x_pitch * 2 : a.h + uint64_t(p) * a.h_pitch * 2;
         }
-        const uint32_t c = tid % 16;
+        const uint32_t c = tid % XC;
         u32x4 rx[PLANES][PER], rw[2][WC];
         uint32_t rs[2][WC];
         float rg[2];
         auto load = [&](uint32_t step) {
-            const uint32_t k0 = step * kTileK;
-            const bool whole = k0 + kTileK <= K;
+            const uint32_t k0 = step * TK;
+            const bool whole = k0 + TK <= K;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
 #pragma unroll
                 for (int j = 0; j < WC; ++j) {
-                    const uint32_t k = k0 + (FP4 ? 32 * q : 64 * j + 16 * q), to = FP4 ? k / 2 : k;
+                    const uint32_t k = k0 + (FP4 ? TK / 4 * q : 64 * j + 16 * q), to = FP4 ? k / 2 : k;
                     const uint8_t* p = mat[i].w + uint64_t(n[i]) * w_row + to;
-                    rw[i][j] = whole ? load_piece<WITHIN>(p, 16, w_row) : load_piece<TAIL>(p, bytes_left(int64_t(w_row) - to), w_row);
-                    if constexpr (WK == ST_KIND_NVFP4) {
+                    if constexpr (WB == 8) {           // (rows of packed fp4 end on 8 bytes)
+                        const uint64_t v = k < K ? *reinterpret_cast<const u64_any*>(p) : 0;
+                        rw[i][j] = u32x4{uint32_t(v), uint32_t(v >> 32), 0, 0};
+                    } else {
+                        rw[i][j] = whole ? load_piece<WITHIN>(p, 16, w_row) : load_piece<TAIL>(p, bytes_left(int64_t(w_row) - to), w_row);
+                    }
+                    if constexpr (WK == ST_KIND_NVFP4 && TK == 64) {
+                        rs[i][j] = k < K ? mat[i].s[uint64_t(n[i]) * ws_row + k / 16] : 0;
+                    } else if constexpr (WK == ST_KIND_NVFP4) {
                         const uint8_t* ps = mat[i].s + uint64_t(n[i]) * ws_row + k / 16;
                         rs[i][j] = whole ? *reinterpret_cast<const u16_any*>(ps) : load_codes(ps, int64_t(ws_row) - k / 16, 2);
                     } else if constexpr (MX) {
                         rs[i][j] = k < K ? mat[i].s[uint64_t(n[i]) * ws_row + k / 32] : 0;
                     }
                 }
-                if constexpr (GROUPED) rg[i] = reinterpret_cast<const float*>(mat[i].s)[uint64_t(n[i] / 128) * groups + step];
+                if constexpr (GROUPED) rg[i] = reinterpret_cast<const float*>(mat[i].s)[uint64_t(n[i] / 128) * groups + step * TK / 128];
             }
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
-                if ((i * kTileThreads + tid) / 16 >= uint32_t(16 * mt)) continue;
+                if ((i * kTileThreads + tid) / XC >= uint32_t(16 * mt)) continue;
                 const uint8_t* p = src[i] + (uint64_t(k0) + 8 * c) * 2;
                 const int32_t avail = bytes_left((int64_t(K) - k0 - 8 * c) * 2);
                 rx[0][i] = whole ? load_piece<WITHIN>(p, 16, 2 * K) : load_piece<TAIL>(p, avail, 2 * K);
@@ -668,11 +680,11 @@ __global__ __launch_bounds__(kTileThreads, 2) void tile(Args a) {
         auto commit = [&](int buf) {
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
-                const uint32_t r = (i * kTileThreads + tid) / 16;
+                const uint32_t r = (i * kTileThreads + tid) / XC;
                 if (r >= uint32_t(16 * mt)) continue;
                 if constexpr (R == SPLIT) split_f16(rx[0][i], rx[0][i], rx[1][i]);
 #pragma unroll
-                for (int p = 0; p < PLANES; ++p) *reinterpret_cast<u32x4*>(&lds[buf][p][(r * 16 + (c ^ (r & 15))) * 16]) = rx[p][i];
+                for (int p = 0; p < PLANES; ++p) *reinterpret_cast<u32x4*>(&lds[buf][p][place(r, c)]) = rx[p][i];
             }
         };
         f32x4 acc[2][MT];
@@ -685,14 +697,14 @@ __global__ __launch_bounds__(kTileThreads, 2) void tile(Args a) {
             commit(0);
         }
         for (uint32_t step = 0; step < steps; ++step) {
-            // this step's weights to operands of four instructions, each 32 of K: lane group q's eight elements are chunk at(m) of x
-            u32x4 wv[2][4];
+            // this step's weights to operands, each 32 of K: lane group q's eight elements are chunk `at` of x
+            u32x4 wv[2][OPS];
             float gs[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 gs[i] = GROUPED ? rg[i] : 1.0f;
 #pragma unroll
-                for (int m = 0; m < 4; ++m) {
+                for (int m = 0; m < OPS; ++m) {
                     if constexpr (WK == ST_KIND_NVFP4) wv[i][m] = codes8<F16, WK>(rw[i][0][m], 0, scale_of<WK>(rs[i][0] >> (8 * (m / 2)) & 0xFF));
                     else if constexpr (FP4) wv[i][m] = codes8<F16, WK>(rw[i][0][m], 0, scale_of<WK>(rs[i][0]));
                     else wv[i][m] = codes8<F16, WK>(rw[i][m / 2][2 * (m & 1)], rw[i][m / 2][2 * (m & 1) + 1], MX ? scale_of<WK>(rs[i][m / 2]) : 1.0f);
@@ -708,11 +720,11 @@ __global__ __launch_bounds__(kTileThreads, 2) void tile(Args a) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i) v[i] = GROUPED ? f32x4{0, 0, 0, 0} : acc[i][j];
 #pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    const int at = FP4 ? 4 * q + m : 8 * (m / 2) + 2 * q + (m & 1);
+                for (int m = 0; m < OPS; ++m) {
+                    const int at = FP4 ? OPS * q + m : 8 * (m / 2) + 2 * q + (m & 1);
 #pragma unroll
                     for (int p = 0; p < PLANES; ++p) {
-                        const u32x4 xv = *reinterpret_cast<const u32x4*>(&lds[buf][p][((16 * j + row) * 16 + (at ^ row)) * 16]);
+                        const u32x4 xv = *reinterpret_cast<const u32x4*>(&lds[buf][p][place(16 * j + row, at)]);
 #pragma unroll
                         for (int i = 0; i < 2; ++i) v[i] = mfma32<F16>(wv[i][m], xv, v[i]);
                     }

@@ -3,10 +3,14 @@
 //
 // Which experts are chosen must not depend on the order of a sum, so z is summed in 64 bits (products of 16-bit numbers are exact, the
 // sums good to 2^-50), and everything behind it too.
-//  * logits: a wavefront takes EW experts and TW tokens, eight elements of K per lane at a time, and folds the lanes' sums.
+//  * logits: 16 tokens by 16 experts a workgroup, on the fp64 matrix instructions (16 x 16 x 4, 64 cycles), which take one converted number
+//    per lane and side; the wavefronts have parts of K and join in LDS.  777 tokens, 256 experts of 5120: bound by those instructions
+//    (2 GFLOP at the 68 TFLOP/s that a large fp64 product reaches: 30 us).
 //  * choose: a token's scores in LDS; an expert's place is the number of those ahead of it, counted by one lane each, so that nothing
 //    waits for a chain of maxima.
 #include <hip/hip_runtime.h>
+
+#include <type_traits>
 
 #include "matrix_codes.h"
 
@@ -27,13 +31,14 @@ struct Args {
     uint32_t t, k, experts, top, sigmoid, renormalize;
 };
 
-constexpr int kWaves = 4;
+constexpr int kMaxWaves = 16;
+typedef double f64x4 __attribute__((ext_vector_type(4)));
 
 // Eight elements of type E at element i of a row as fp32, zeros from k on; the row may start at any element.
-template <uint32_t E>
+template <uint32_t E, bool WHOLE>
 __device__ __forceinline__ void load8(const uint8_t* p, uint32_t i, uint32_t k, float* v) {
     constexpr uint32_t S = E == ST_OUT_F32 ? 4 : 2;
-    if (i + 8 <= k) {
+    if (WHOLE || i + 8 <= k) {
         const u32x4 a = *reinterpret_cast<const u32x4_any*>(p + uint64_t(i) * S);
         if constexpr (E == ST_OUT_F32) {
             const u32x4 b = *reinterpret_cast<const u32x4_any*>(p + uint64_t(i) * S + 16);
@@ -56,86 +61,123 @@ __device__ __forceinline__ void load8(const uint8_t* p, uint32_t i, uint32_t k, 
     }
 }
 
-template <uint32_t XE, uint32_t RE, int EW, int TW>
-__global__ __launch_bounds__(64 * kWaves) void logits(Args a) {
-    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const uint32_t e0 = (blockIdx.x * kWaves + wave) * EW, t0 = blockIdx.y * TW;
-    if (e0 >= a.experts) return;
+template <uint32_t XE, uint32_t RE>
+__global__ __launch_bounds__(64 * kMaxWaves) void logits(Args a) {
+    __shared__ double joined[kMaxWaves][256];
+    const uint32_t lane = threadIdx.x & 63, row = lane & 15, g = lane >> 4, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+    const uint32_t e0 = blockIdx.x * 16, t0 = blockIdx.y * 16;
     constexpr uint32_t XS = XE == ST_OUT_F32 ? 4 : 2, RS = RE == ST_OUT_F32 ? 4 : 2;
     // experts and tokens past the last are read as the last one; nothing of them is stored
-    const uint8_t *pr[EW], *px[TW];
+    const uint8_t* pr = a.router + uint64_t(e0 + row < a.experts ? e0 + row : a.experts - 1) * a.router_pitch * RS;
+    const uint8_t* px = a.x + uint64_t(t0 + row < a.t ? t0 + row : a.t - 1) * a.x_pitch * XS;
+    f64x4 acc = {0, 0, 0, 0};
+    // 32 of K a turn: lane group g has eight of them, instruction i takes the i-th of each
+    auto turn = [&](uint32_t k, auto whole) {
+        constexpr bool WHOLE = decltype(whole)::value;
+        float r[8], x[8];
+        load8<RE, WHOLE>(pr, k + 8 * g, a.k, r);
+        load8<XE, WHOLE>(px, k + 8 * g, a.k, x);
 #pragma unroll
-    for (int i = 0; i < EW; ++i) pr[i] = a.router + uint64_t(e0 + i < a.experts ? e0 + i : a.experts - 1) * a.router_pitch * RS;
+        for (int i = 0; i < 8; ++i) acc = __builtin_amdgcn_mfma_f64_16x16x4f64(double(x[i]), double(r[i]), acc, 0, 0, 0);
+    };
+    const uint32_t whole = a.k / 32;
+    uint32_t i = wave;
+    // (four turns' loads together)
+#pragma unroll 4
+    for (; i < whole; i += waves) turn(i * 32, std::true_type{});
+    if (i * 32 < a.k) turn(i * 32, std::false_type{});
 #pragma unroll
-    for (int j = 0; j < TW; ++j) px[j] = a.x + uint64_t(t0 + j < a.t ? t0 + j : a.t - 1) * a.x_pitch * XS;
-    double acc[EW][TW];
-#pragma unroll
-    for (int i = 0; i < EW; ++i)
-#pragma unroll
-        for (int j = 0; j < TW; ++j) acc[i][j] = 0.0;
-    for (uint32_t k = lane * 8; k < a.k; k += 512) {
-        float r[EW][8];
-#pragma unroll
-        for (int i = 0; i < EW; ++i) load8<RE>(pr[i], k, a.k, r[i]);
-#pragma unroll
-        for (int j = 0; j < TW; ++j) {
-            float x[8];
-            load8<XE>(px[j], k, a.k, x);
-#pragma unroll
-            for (int i = 0; i < EW; ++i)
-#pragma unroll
-                for (int c = 0; c < 8; ++c) acc[i][j] = __builtin_fma(double(r[i][c]), double(x[c]), acc[i][j]);
-        }
+    for (int i = 0; i < 4; ++i) joined[wave][i * 64 + lane] = acc[i];
+    __syncthreads();
+    for (uint32_t o = threadIdx.x; o < 256; o += blockDim.x) {
+        double v = joined[0][o];
+        for (uint32_t w = 1; w < waves; ++w) v += joined[w][o];
+        // result i of lane (row, g): token 4 i + g, expert `row`
+        const uint32_t t = t0 + 4 * (o >> 6) + (o >> 4 & 3), e = e0 + (o & 15);
+        if (t < a.t && e < a.experts) a.z[uint64_t(t) * a.experts + e] = v;
     }
-#pragma unroll
-    for (int i = 0; i < EW; ++i)
-#pragma unroll
-        for (int j = 0; j < TW; ++j) {
-            double v = acc[i][j];
-#pragma unroll
-            for (int o = 32; o; o /= 2) v += __shfl_xor(v, o);
-            if (lane == 0 && e0 + i < a.experts && t0 + j < a.t) a.z[uint64_t(t0 + j) * a.experts + e0 + i] = v;
-        }
 }
 
-__device__ __forceinline__ double over_workgroup(double v, bool sum, double* shared) {
+// One token: a wavefront an expert, dot products on the vector unit (128 experts of 4096: 6 us, 15 on the matrix instructions, which would
+// leave 15 of 16 rows empty and give eight workgroups all the router).
+constexpr int kOneWaves = 4;
+template <uint32_t XE, uint32_t RE>
+__global__ __launch_bounds__(64 * kOneWaves) void logits_one(Args a) {
+    const uint32_t lane = threadIdx.x & 63, e = blockIdx.x * kOneWaves + (threadIdx.x >> 6);
+    if (e >= a.experts) return;
+    const uint8_t* pr = a.router + uint64_t(e) * a.router_pitch * (RE == ST_OUT_F32 ? 4 : 2);
+    double acc = 0.0;
+    auto turn = [&](uint32_t k, auto whole) {
+        constexpr bool WHOLE = decltype(whole)::value;
+        float r[8], x[8];
+        load8<RE, WHOLE>(pr, k, a.k, r);
+        load8<XE, WHOLE>(a.x, k, a.k, x);
 #pragma unroll
-    for (int o = 32; o; o /= 2) {
-        const double w = __shfl_xor(v, o);
-        v = sum ? v + w : fmax(v, w);
-    }
-    __syncthreads();
+        for (int c = 0; c < 8; ++c) acc = __builtin_fma(double(r[c]), double(x[c]), acc);
+    };
+    uint32_t k = 0;
+#pragma unroll 4
+    for (; k + 512 <= a.k; k += 512) turn(k + lane * 8, std::true_type{});
+    if (k + lane * 8 < a.k) turn(k + lane * 8, std::false_type{});
+#pragma unroll
+    for (int o = 32; o; o /= 2) acc += __shfl_xor(acc, o);
+    if (lane == 0) a.z[e] = acc;
+}
+
+// The largest of the workgroup's values, NaN if there is one, or their sum; in one order.
+template <bool SUM>
+__device__ __forceinline__ double over_workgroup(double v, double* shared) {
+    auto join = [](double p, double q) { return SUM ? p + q : q > p ? q : q != q ? q : p; };
+#pragma unroll
+    for (int o = 32; o; o /= 2) v = join(v, __shfl_xor(v, o));
+    if (blockDim.x == 64) return v;
     if ((threadIdx.x & 63) == 0) shared[threadIdx.x >> 6] = v;
     __syncthreads();
     v = shared[0];
-    for (uint32_t i = 1; i < blockDim.x >> 6; ++i) v = sum ? v + shared[i] : fmax(v, shared[i]);
+    for (uint32_t i = 1; i < blockDim.x >> 6; ++i) v = join(v, shared[i]);
     return v;
 }
 
+typedef double f64x2 __attribute__((ext_vector_type(2)));
+
 __global__ __launch_bounds__(1024) void choose(Args a) {
-    __shared__ double key[1024], got[1024], shared[16];
+    __shared__ __align__(16) double key[1024], got[1024], shared[2][16];
     const uint32_t e = threadIdx.x;
     const uint64_t t = blockIdx.x;
     const bool in = e < a.experts;
     const double none = -__builtin_inf();
     const double z = in ? a.z[t * a.experts + e] : none;
-    double s, total = 1.0;
+    double s;
     if (a.sigmoid) {
         s = in ? 1.0 / (1.0 + exp(-z)) : 0.0;
     } else {
-        const double most = over_workgroup(z, false, shared);
-        s = in ? exp(z - most) : 0.0;
-        total = over_workgroup(s, true, shared);
-        s /= total;
+        s = in ? exp(z - over_workgroup<false>(z, shared[0])) : 0.0;
+        // (weights that are divided by their own sum need no other)
+        if (a.bias || !a.renormalize) s /= over_workgroup<true>(s, shared[1]);
     }
     double mine = a.bias && in ? s + double(a.bias[e]) : z;
     if (mine != mine) mine = none;
-    key[e] = mine;
+    key[e] = in ? mine : none;
     __syncthreads();
+    // those ahead: larger ones, and equal ones of a smaller number, which all of the wavefronts before this one's are and none behind it
+    // (keys behind the last expert are the least and have the largest numbers)
     uint32_t place = 0;
-    for (uint32_t j = 0; j < a.experts; ++j) {
-        const double other = key[j];
-        place += other > mine || (other == mine && j < e) ? 1 : 0;
+    const uint32_t mine0 = e & ~63u;
+#pragma unroll 4
+    for (uint32_t j = 0; j < mine0; j += 2) {
+        const f64x2 other = *reinterpret_cast<const f64x2*>(&key[j]);
+        place += uint32_t(other.x >= mine) + uint32_t(other.y >= mine);
+    }
+#pragma unroll 4
+    for (uint32_t j = mine0; j < mine0 + 64; j += 2) {
+        const f64x2 other = *reinterpret_cast<const f64x2*>(&key[j]);
+        place += uint32_t(other.x > mine) + (uint32_t(other.x == mine) & uint32_t(j < e));
+        place += uint32_t(other.y > mine) + (uint32_t(other.y == mine) & uint32_t(j + 1 < e));
+    }
+#pragma unroll 4
+    for (uint32_t j = mine0 + 64; j < blockDim.x; j += 2) {
+        const f64x2 other = *reinterpret_cast<const f64x2*>(&key[j]);
+        place += uint32_t(other.x > mine) + uint32_t(other.y > mine);
     }
     if (in && place < a.top) {
         a.ids[t * a.top + place] = int32_t(e);
@@ -177,12 +219,14 @@ st_status check_args(const st_moe_route_args* g) {
 
 template <uint32_t XE, uint32_t RE>
 void launch(const Args& a, hipStream_t s) {
-    auto go = [&](auto kernel, uint32_t ew, uint32_t tw) {
-        const dim3 grid((a.experts + kWaves * ew - 1) / (kWaves * ew), (a.t + tw - 1) / tw);
-        hipLaunchKernelGGL(kernel, grid, dim3(64 * kWaves), 0, s, a);
-    };
-    if (a.t == 1) go(logits<XE, RE, 1, 1>, 1, 1);
-    else go(logits<XE, RE, 4, 4>, 4, 4);
+    if (a.t == 1) {
+        hipLaunchKernelGGL((logits_one<XE, RE>), dim3((a.experts + kOneWaves - 1) / kOneWaves), dim3(64 * kOneWaves), 0, s, a);
+        return;
+    }
+    // few tiles: more wavefronts for each
+    const uint32_t tiles_e = (a.experts + 15) / 16, tiles_t = (a.t + 15) / 16, turns = (a.k + 31) / 32;
+    const uint32_t most = uint64_t(tiles_e) * tiles_t < 256 ? kMaxWaves : 4, waves = turns < 1 ? 1 : turns < most ? turns : most;
+    hipLaunchKernelGGL((logits<XE, RE>), dim3(tiles_e, tiles_t), dim3(64 * waves), 0, s, a);
 }
 template <uint32_t XE>
 void launch_router(const Args& a, uint32_t type, hipStream_t s) {
