@@ -151,7 +151,8 @@ __global__ __launch_bounds__(1024) void choose(Args a) {
     if (a.sigmoid) {
         s = in ? 1.0 / (1.0 + exp(-z)) : 0.0;
     } else {
-        s = in ? exp(z - over_workgroup<false>(z, shared[0])) : 0.0;
+        const double most = over_workgroup<false>(z, shared[0]);      // (all lanes take part)
+        s = in ? exp(z - most) : 0.0;
         // (weights that are divided by their own sum need no other)
         if (a.bias || !a.renormalize) s /= over_workgroup<true>(s, shared[1]);
     }

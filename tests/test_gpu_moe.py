@@ -187,6 +187,23 @@ def test_route(xt, rt, experts, top, k, score):
                 assert ((w.cpu().double() - want).abs() <= want.abs() * (2.0 ** -24 + 2.0 ** -40)).all()
 
 
+@pytest.mark.parametrize("experts,top,k", [(2, 1, 33), (5, 3, 306), (9, 4, 480), (23, 8, 1412), (61, 6, 317), (127, 7, 100), (513, 5, 64)])
+def test_route_any_number_of_experts(experts, top, k):
+    """Wavefronts and workgroups that the experts do not fill, for scores that are far apart."""
+    g = torch.Generator().manual_seed(experts)
+    router, bias = torch.randn(experts, k, generator=g) * 3 / k ** 0.5, 0.1 * torch.randn(experts, generator=g)
+    for m in (1, 17, 300):
+        x = _rows(m, k, "bf16", m)
+        for score in ("softmax", "sigmoid"):
+            for b in (None, bias):
+                for renormalize in (True, False):
+                    print(f"route {experts} {top} {k} {score} rows {m}", flush=True)
+                    w, ids = st.moe_route(x.to(DEV), router.to(DEV), top, score=score, bias=None if b is None else b.to(DEV), renormalize=renormalize)
+                    want, wids = mref.route(x, router, top, score, b, renormalize)
+                    assert torch.equal(ids.cpu(), wids)
+                    assert ((w.cpu().double() - want).abs() <= want.abs() * (2.0 ** -24 + 2.0 ** -40)).all()
+
+
 def test_route_ties_and_nan():
     """Equal scores by their number, NaN last, whatever the sums' order."""
     router = torch.zeros(12, 64)
