@@ -47,14 +47,16 @@ class QuantizedKvCache:
 def _check_cache(c, who: str):
     if not isinstance(c, QuantizedKvCache):
         raise ValueError(f"{who}: the cache is a {type(c).__name__}; a QuantizedKvCache is needed")
-    if not (c.k.dim() == 4 and c.k.dtype == _E4M3 and c.k.is_contiguous()):
-        raise ValueError(f"{who}: the cache's keys are {c.k.dtype} {tuple(c.k.shape)}, strides {c.k.stride()}")
-    pages, heads, block, dim = c.k.shape
-    if not (c.v.dtype == _E4M3 and tuple(c.v.shape) == (pages, heads, dim, block) and c.v.is_contiguous()):
-        raise ValueError(f"{who}: the cache's values are {c.v.dtype} {tuple(c.v.shape)}, strides {c.v.stride()}; "
+    k, v, ks, vs = c.k, c.v, c.k_scale, c.v_scale
+    shape = k.shape
+    if not (len(shape) == 4 and k.dtype == _E4M3 and k.is_contiguous()):
+        raise ValueError(f"{who}: the cache's keys are {k.dtype} {tuple(shape)}, strides {k.stride()}")
+    pages, heads, block, dim = shape
+    if not (v.dtype == _E4M3 and v.shape == (pages, heads, dim, block) and v.is_contiguous()):
+        raise ValueError(f"{who}: the cache's values are {v.dtype} {tuple(v.shape)}, strides {v.stride()}; "
                          f"{(pages, heads, dim, block)} are needed")
-    for s in (c.k_scale, c.v_scale):
-        if not (s.dtype == _E8M0 and tuple(s.shape) == (pages, heads) and s.is_contiguous()):
+    for s in (ks, vs):
+        if not (s.dtype == _E8M0 and s.shape == (pages, heads) and s.is_contiguous()):
             raise ValueError(f"{who}: the cache's scales are {s.dtype} {tuple(s.shape)}, strides {s.stride()}; {(pages, heads)} are needed")
     if block not in BLOCKS:
         raise ValueError(f"{who}: pages of {block} tokens; one of {BLOCKS} is needed")
@@ -63,11 +65,12 @@ def _check_cache(c, who: str):
 
 def _check_seqs(table, lengths, starts, max_new, tokens: int, who: str):
     """(seqs, max_new) of the arguments both operators share."""
-    if not (table.dtype == torch.int32 and table.dim() == 2 and (table.shape[1] <= 1 or table.stride(1) == 1)
-            and (table.shape[0] <= 1 or table.stride(0) >= table.shape[1])):
+    if not (table.dtype == torch.int32 and table.dim() == 2
+            and (table.is_contiguous() or ((table.shape[1] <= 1 or table.stride(1) == 1)
+                                           and (table.shape[0] <= 1 or table.stride(0) >= table.shape[1])))):
         raise ValueError(f"{who}: table {table.dtype} {tuple(table.shape)}, strides {table.stride()}; int32 [sequences, blocks] is needed")
     seqs = table.shape[0]
-    if not (lengths.dtype == torch.int32 and tuple(lengths.shape) == (seqs,) and (seqs <= 1 or lengths.stride(0) == 1)):
+    if not (lengths.dtype == torch.int32 and lengths.shape == (seqs,) and lengths.is_contiguous()):
         raise ValueError(f"{who}: lengths {lengths.dtype} {tuple(lengths.shape)}, strides {lengths.stride()}; int32 [{seqs}] is needed")
     if starts is None:
         if seqs == 0 and tokens or seqs and tokens % seqs:
@@ -75,7 +78,7 @@ def _check_seqs(table, lengths, starts, max_new, tokens: int, who: str):
         if max_new is not None:
             raise ValueError(f"{who}: max_new goes with starts")
         return seqs, tokens // seqs if seqs else 0
-    if not (starts.dtype == torch.int32 and tuple(starts.shape) == (seqs + 1,) and (seqs == 0 or starts.stride(0) == 1)):
+    if not (starts.dtype == torch.int32 and starts.shape == (seqs + 1,) and starts.is_contiguous()):
         raise ValueError(f"{who}: starts {starts.dtype} {tuple(starts.shape)}, strides {starts.stride()}; int32 [{seqs + 1}] is needed")
     if max_new is None:
         return seqs, tokens
@@ -116,15 +119,17 @@ def kv_append(cache: QuantizedKvCache, k, v, table, lengths, starts=None, max_ne
     seqs, most = _check_seqs(table, lengths, starts, max_new, tokens, who)
     if tokens == 0 or seqs == 0 or most == 0 or heads == 0:
         return
+    ck, cv, sk, sv = cache.k.data_ptr(), cache.v.data_ptr(), cache.k_scale.data_ptr(), cache.v_scale.data_ptr()
+    codes, scales = pages * heads * block * dim, pages * heads
     (ka, kb), (va, vb) = _span(k), _span(v)
-    for t in (cache.k, cache.v, cache.k_scale, cache.v_scale):
-        a, b = _span(t)
-        if a < kb and ka < b or a < vb and va < b:
+    for a, n in ((ck, codes), (cv, codes), (sk, scales), (sv, scales)):
+        if a < kb and ka < a + n or a < vb and va < a + n:
             raise ValueError(f"{who}: the cache overlaps an input")
-    args = KvAppendArgs(k.data_ptr(), v.data_ptr(), cache.k.data_ptr(), cache.v.data_ptr(), cache.k_scale.data_ptr(),
-                        cache.v_scale.data_ptr(), table.data_ptr(), lengths.data_ptr(), None if starts is None else starts.data_ptr(),
-                        pages, tokens, seqs, most, table.shape[1], table.stride(0), k.stride(0), k.stride(1), v.stride(0),
-                        v.stride(1), heads, dim, block, _TYPE[k.dtype])
+    k_pitch, k_head, _ = k.stride()
+    v_pitch, v_head, _ = v.stride()
+    args = KvAppendArgs(ka, va, ck, cv, sk, sv, table.data_ptr(), lengths.data_ptr(), None if starts is None else starts.data_ptr(),
+                        pages, tokens, seqs, most, table.shape[1], table.stride(0), k_pitch, k_head, v_pitch, v_head, heads, dim, block,
+                        _TYPE[k.dtype])
     _launch(lib().st_kv_append, args, cache.k.device, stream,
             (k, v, cache.k, cache.v, cache.k_scale, cache.v_scale, table, lengths, starts), who)
 
