@@ -4,9 +4,9 @@
 // Dividing by a power of two is exact, so each code is rounded once (a code that is rounded again changes only below 2^-6 s), and
 // fp32 holds everything.
 //
-// A workgroup has one block of tokens of one head, keys or values: it reads the new tokens twice (amax, codes; the second time
-// from cache) and nobody else writes its codes or its scale.  Keys are stored as they come; values are turned, a lane taking one
-// column's 16 tokens, so that 16 bytes are stored together.
+// A workgroup has one block of tokens of one head, keys or values: nobody else writes its codes or its scale.  It reads the new tokens
+// once and keeps them in registers until their amax is known, up to 32 numbers a lane (64 tokens of 128); larger blocks are read again from
+// cache.  Keys are stored as they come; values are turned, a lane taking two columns' 16 tokens, so that 16 bytes are stored together.
 #include <hip/hip_runtime.h>
 
 #include "kv_cache.h"
@@ -42,6 +42,21 @@ __device__ __forceinline__ void load8(const uint8_t* p, uint64_t i, float* v) {
         for (int k = 0; k < 8; ++k) v[k] = element<E>(p, i + k);
     }
 }
+// Two elements at p + i; VEC: in one load.
+template <uint32_t E, bool VEC>
+__device__ __forceinline__ void load2(const uint8_t* p, uint64_t i, float* v) {
+    if constexpr (VEC && E == ST_OUT_F32) {
+        const dword2 w = *reinterpret_cast<const dword2*>(p + 4 * i);
+        v[0] = as_f32(w.x), v[1] = as_f32(w.y);
+    } else if constexpr (VEC) {
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(p + 2 * i);
+        const f16x2 h = __builtin_bit_cast(f16x2, w);
+        v[0] = E == ST_OUT_BF16 ? as_f32(w << 16) : float(h.x);
+        v[1] = E == ST_OUT_BF16 ? as_f32(w & 0xFFFF0000u) : float(h.y);
+    } else {
+        v[0] = element<E>(p, i), v[1] = element<E>(p, i + 1);
+    }
+}
 __device__ __forceinline__ bool finite(float v) { return __builtin_fabsf(v) <= 3.4028234663852886e38f; }
 
 // a * 2^-e and b * 2^-e to codes in the low two bytes
@@ -75,13 +90,49 @@ __global__ __launch_bounds__(kThreads) void append(Args a) {
     const uint64_t row0 = (uint64_t(p.first) + uint64_t(base + lo - p.pos)) * pitch + uint64_t(head) * a.head_pitch[which];
     uint8_t* codes = a.codes[which] + at * block * D;
 
-    const uint32_t chunks = D / 8, items = (hi - lo) * chunks;
-    float amax = 0.0f;
-    for (uint32_t i = threadIdx.x; i < items; i += kThreads) {
-        float v[8];
-        load8<E, VEC>(x, row0 + uint64_t(i / chunks) * pitch + i % chunks * 8, v);
+    const uint32_t n = hi - lo, chunks = D / 8, items = n * chunks;       // keys: eight numbers of a token
+    const uint32_t first = lo / 16, groups = (hi + 15) / 16 - first, pairs = D / 2, turned = groups * pairs;   // values: two columns of 16 tokens
+    constexpr uint32_t KEEP = 4;
+    const bool once = which == 0 ? items <= KEEP * kThreads : turned <= kThreads;
+    float v[32];
+    auto key = [&](uint32_t i, float* to) { load8<E, VEC>(x, row0 + uint64_t(i / chunks) * pitch + i % chunks * 8, to); };
+    // value 2 t + c of item i: token t of its 16, column c of its two; 0 for tokens that are not new
+    auto value = [&](uint32_t i, float* to) {
+        const uint32_t d = i % pairs * 2, t0 = (first + i / pairs) * 16;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) amax = finite(v[k]) ? fmaxf(amax, __builtin_fabsf(v[k])) : amax;
+        for (uint32_t t = 0; t < 16; ++t) {
+            const bool in = t0 + t >= lo && t0 + t < hi;
+            const uint64_t o = row0 + uint64_t(in ? t0 + t - lo : 0) * pitch + d;
+            load2<E, VEC>(x, o, to + 2 * t);
+            to[2 * t] = in ? to[2 * t] : 0.0f;
+            to[2 * t + 1] = in ? to[2 * t + 1] : 0.0f;
+        }
+    };
+    float amax = 0.0f;
+    auto more = [&](const float* from, int count) {
+#pragma unroll
+        for (int k = 0; k < count; ++k) amax = finite(from[k]) ? fmaxf(amax, __builtin_fabsf(from[k])) : amax;
+    };
+    if (once && which == 0) {
+#pragma unroll
+        for (uint32_t j = 0; j < KEEP; ++j) {
+            const uint32_t i = threadIdx.x + j * kThreads;
+            if (i < items) key(i, v + 8 * j);
+            else
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[8 * j + k] = 0.0f;
+        }
+        more(v, 32);
+    } else if (once) {
+        if (threadIdx.x < turned) {
+            value(threadIdx.x, v);
+            more(v, 32);
+        }
+    } else {
+        for (uint32_t i = threadIdx.x; i < items; i += kThreads) {
+            key(i, v);
+            more(v, 8);
+        }
     }
 #pragma unroll
     for (int o = 32; o; o /= 2) amax = fmaxf(amax, __shfl_xor(amax, o));
@@ -97,11 +148,19 @@ __global__ __launch_bounds__(kThreads) void append(Args a) {
     const int up = e - had;       // >= 0
 
     if (which == 0) {
-        for (uint32_t i = threadIdx.x; i < items; i += kThreads) {
-            float v[8];
-            load8<E, VEC>(x, row0 + uint64_t(i / chunks) * pitch + i % chunks * 8, v);
+        auto put = [&](uint32_t i, const float* from) {
             *reinterpret_cast<dword2*>(codes + uint64_t(lo) * D + i * 8) =
-                dword2{codes2(v[0], v[1], e) | codes2(v[2], v[3], e) << 16, codes2(v[4], v[5], e) | codes2(v[6], v[7], e) << 16};
+                dword2{codes2(from[0], from[1], e) | codes2(from[2], from[3], e) << 16, codes2(from[4], from[5], e) | codes2(from[6], from[7], e) << 16};
+        };
+        if (once) {
+#pragma unroll
+            for (uint32_t j = 0; j < KEEP; ++j)
+                if (threadIdx.x + j * kThreads < items) put(threadIdx.x + j * kThreads, v + 8 * j);
+        } else {
+            for (uint32_t i = threadIdx.x; i < items; i += kThreads) {
+                key(i, v);
+                put(i, v);
+            }
         }
         if (up)
             for (uint32_t i = threadIdx.x; i < lo * chunks; i += kThreads) {
@@ -109,32 +168,47 @@ __global__ __launch_bounds__(kThreads) void append(Args a) {
                 *c = dword2{again4(c->x, up), again4(c->y, up)};
             }
     } else {
-        // 16 tokens of one column: those before lo are there already, those from hi on stay
-        const uint32_t first = up ? 0 : lo / 16, groups = (hi + 15) / 16 - first;
-        for (uint32_t i = threadIdx.x; i < groups * D; i += kThreads) {
-            const uint32_t d = i % D, t0 = (first + i / D) * 16;
-            dword4* c = reinterpret_cast<dword4*>(codes + uint64_t(d) * block + t0);
-            const bool all = t0 >= lo && t0 + 16 <= hi;
-            const dword4 was = all ? dword4{0, 0, 0, 0} : *c;
-            dword4 now;
+        // 16 tokens of a column: those before lo are there already, those from hi on stay
+        auto put = [&](uint32_t i, const float* from) {
+            const uint32_t d = i % pairs * 2, t0 = (first + i / pairs) * 16;
 #pragma unroll
-            for (uint32_t w = 0; w < 4; ++w) {
-                float v[4];
-                uint32_t keep = was[w], fresh = 0;
-                const uint32_t old = up && t0 < lo ? again4(keep, up) : keep;
+            for (uint32_t col = 0; col < 2; ++col) {
+                dword4* c = reinterpret_cast<dword4*>(codes + uint64_t(d + col) * block + t0);
+                const bool all = t0 >= lo && t0 + 16 <= hi;
+                const dword4 was = all ? dword4{0, 0, 0, 0} : *c;
+                dword4 now;
 #pragma unroll
-                for (uint32_t k = 0; k < 4; ++k) {
-                    const uint32_t t = t0 + 4 * w + k;
-                    const bool in = t >= lo && t < hi;
-                    v[k] = in ? element<E>(x, row0 + uint64_t(t - lo) * pitch + d) : 0.0f;
-                    fresh |= in ? 0xFFu << 8 * k : 0;
-                    if (t < lo) keep = (keep & ~(0xFFu << 8 * k)) | (old & 0xFFu << 8 * k);
+                for (uint32_t w = 0; w < 4; ++w) {
+                    uint32_t fresh = 0, old = 0;
+#pragma unroll
+                    for (uint32_t k = 0; k < 4; ++k) {
+                        const uint32_t t = t0 + 4 * w + k;
+                        fresh |= t >= lo && t < hi ? 0xFFu << 8 * k : 0;
+                        old |= t < lo ? 0xFFu << 8 * k : 0;
+                    }
+                    const float* f = from + 8 * w + col;
+                    const uint32_t code = codes2(f[0], f[2], e) | codes2(f[4], f[6], e) << 16;
+                    const uint32_t kept = up && t0 < lo ? (again4(was[w], up) & old) | (was[w] & ~old) : was[w];
+                    now[w] = (code & fresh) | (kept & ~fresh);
                 }
-                const uint32_t n = codes2(v[0], v[1], e) | codes2(v[2], v[3], e) << 16;
-                now[w] = (n & fresh) | (keep & ~fresh);
+                *c = now;
             }
-            *c = now;
+        };
+        if (once) {
+            if (threadIdx.x < turned) put(threadIdx.x, v);
+        } else {
+            for (uint32_t i = threadIdx.x; i < turned; i += kThreads) {
+                value(i, v);
+                put(i, v);
+            }
         }
+        // whole groups of 16 tokens that were there before
+        if (up)
+            for (uint32_t i = threadIdx.x; i < first * D; i += kThreads) {
+                dword4* c = reinterpret_cast<dword4*>(codes + uint64_t(i % D) * block + i / D * 16);
+                const dword4 was = *c;
+                *c = dword4{again4(was[0], up), again4(was[1], up), again4(was[2], up), again4(was[3], up)};
+            }
     }
     if (threadIdx.x == 0) a.scale[which][at] = uint8_t(e + 127);
 }
