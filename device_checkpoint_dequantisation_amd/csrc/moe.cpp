@@ -64,7 +64,7 @@ st_status plan_of(const st_moe_args& g, Plan* p) {
     p->part_bytes = (p->part_bytes + 15) / 16 * 16;
     p->sort_bytes = p->cut == ONE ? 0 : (4 + 4 * slots + pairs) * 4;
     // threads of each launch; a grid dimension holds fewer than 2^32, and 65535 workgroups in y (slots is below that)
-    if ((g.i + 3) / 4 * 512 >> 32 || (g.n + 3) / 4 * 512 >> 32 || (p->cut >= SOME && (g.n + 3) / 4 * g.t >> 32) || slots > 65535)
+    if ((g.i + 1) / 2 * 512 >> 32 || (g.n + 1) / 2 * 512 >> 32 || (p->cut >= SOME && (g.n + 3) / 4 * g.t >> 32) || slots > 65535)
         return st_fail(ST_E_SHAPE, "%s: i %llu, n %llu, t %llu take more threads than one launch holds", kWho, (unsigned long long)g.i,
                        (unsigned long long)g.n, (unsigned long long)g.t);
     return ST_OK;

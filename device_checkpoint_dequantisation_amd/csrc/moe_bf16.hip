@@ -13,7 +13,7 @@ void launch(const Args& a, Cut cut, hipStream_t s) {
         constexpr Ends END = decltype(end)::value;
         switch (cut) {
             case ONE:
-                hipLaunchKernelGGL((up_one<ST_X_BF16, WK>), dim3((a.i + kOneColumns - 1) / kOneColumns, a.slots), dim3(64 * even((chunks + 63) / 64, kOneMaxWaves)), 0, s, a);
+                hipLaunchKernelGGL((up_one<ST_X_BF16, WK>), dim3((a.i + kUpColumns - 1) / kUpColumns, a.slots), dim3(64 * even((chunks + 63) / 64, kOneMaxWaves)), 0, s, a);
                 break;
             case FEW:
             case SOME: hipLaunchKernelGGL((up_few<ST_X_BF16, WK, END>), few, block, 0, s, a); break;

@@ -76,7 +76,7 @@ void launch(const Args& a, Cut cut, hipStream_t s) {
         switch (cut) {
             case ONE: {
                 const uint64_t chunks = (uint64_t(a.i) + One<WK>::E - 1) / One<WK>::E * a.pairs;
-                hipLaunchKernelGGL((down_one<WK>), dim3((a.n + kOneColumns - 1) / kOneColumns), dim3(64 * even((chunks + 63) / 64, kOneMaxWaves)), 0, s, a);
+                hipLaunchKernelGGL((down_one<WK>), dim3((a.n + kDownColumns - 1) / kDownColumns), dim3(64 * even((chunks + 63) / 64, kOneMaxWaves)), 0, s, a);
                 break;
             }
             case FEW: hipLaunchKernelGGL((down_few<WK, NG, END>), grid, block, 0, s, a); break;

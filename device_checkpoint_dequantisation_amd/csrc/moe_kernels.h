@@ -189,18 +189,19 @@ struct Codes {
     }
 };
 
+// h as two terms, each to be rounded to bf16; infinities and NaN stay whole in the first.
+__device__ __forceinline__ void terms_of(float h, float& hi, float& lo) {
+    hi = as_f32(cvt_bf16x2(h, 0.0f) << 16);
+    const float rest = h - hi;
+    lo = rest == rest ? rest : 0.0f;
+}
 // h of columns n..n+3 of pair p, from the sums of gate and up.
 template <int WK>
 __device__ __forceinline__ void store_h(const Args& a, uint32_t p, uint32_t n, f32x4 gate, f32x4 up, float sg, float su) {
     if (n >= a.i) return;
     float hi[4], lo[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float h = activate(gate[i] * sg, a.act) * (up[i] * su);
-        hi[i] = as_f32(cvt_bf16x2(h, 0.0f) << 16);
-        const float rest = h - hi[i];
-        lo[i] = rest == rest ? rest : 0.0f;      // infinities and NaN stay whole in the first term
-    }
+    for (int i = 0; i < 4; ++i) terms_of(activate(gate[i] * sg, a.act) * (up[i] * su), hi[i], lo[i]);
     // (h_pitch is a multiple of 8, so columns behind the last one have room)
     uint8_t* at = a.h + (uint64_t(p) * a.h_pitch + n) * 2;
     *reinterpret_cast<dword2*>(at) = dword2{cvt_bf16x2(hi[0], hi[1]), cvt_bf16x2(hi[2], hi[3])};
@@ -318,20 +319,22 @@ __device__ __forceinline__ void load_pairs(const uint8_t* p, uint32_t k, uint32_
     }
 }
 
-constexpr int kOneMaxWaves = 8, kOneColumns = 4;
+// Columns of a workgroup (packed-fp4 experts [1280, 5120], 8 of them: gate and up 17 us with two, 21 with four, 31 with eight; down 15 us with
+// two, 12 with four).
+constexpr int kOneMaxWaves = 8, kUpColumns = 2, kDownColumns = 4;
 
-// Columns 4 * blockIdx.x .. + 3 of h of pair blockIdx.y: four rows of gate and four of up.
+// kUpColumns columns of h of pair blockIdx.y: their rows of gate and of up.
 template <int X, int WK>
 __global__ __launch_bounds__(64 * kOneMaxWaves) void up_one(Args a) {
     using O = One<WK>;
     using D = Dense<X, WK>;
-    constexpr int R = 2 * kOneColumns, PAIRS = O::E / 2;
+    constexpr int R = 2 * kUpColumns, PAIRS = O::E / 2;
     __shared__ __align__(16) float joined[kOneMaxWaves][R];
     const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
     const int32_t e = __builtin_amdgcn_readfirstlane(a.ids[blockIdx.y]);
     if (e < 0 || uint32_t(e) >= a.experts) return;
     const Matrix mat[2] = {matrix_of(a, e, 0), matrix_of(a, e, 1)};
-    const uint32_t n0 = blockIdx.x * kOneColumns, w_row = O::FP4 ? a.k / 2 : a.k, ws_row = a.k / (WK == ST_KIND_NVFP4 ? 16 : 32);
+    const uint32_t n0 = blockIdx.x * kUpColumns, w_row = O::FP4 ? a.k / 2 : a.k, ws_row = a.k / (WK == ST_KIND_NVFP4 ? 16 : 32);
     const uint32_t groups = (a.k + 127) / 128;
     float acc[R];
 #pragma unroll
@@ -343,8 +346,8 @@ __global__ __launch_bounds__(64 * kOneMaxWaves) void up_one(Args a) {
         // rows past the last are read as the last one; nothing of them is stored
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const uint32_t n = n0 + r % kOneColumns < a.i ? n0 + r % kOneColumns : a.i - 1;
-            const Matrix& m = mat[r / kOneColumns];
+            const uint32_t n = n0 + r % kUpColumns < a.i ? n0 + r % kUpColumns : a.i - 1;
+            const Matrix& m = mat[r / kUpColumns];
             load_row<WK>(m.w + uint64_t(n) * w_row, m.s + uint64_t(n) * ws_row, k, a.k, w[r], sc[r]);
         }
         uint32_t x[PAIRS], xl[D::SPLIT ? PAIRS : 1];
@@ -366,28 +369,29 @@ __global__ __launch_bounds__(64 * kOneMaxWaves) void up_one(Args a) {
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const float d = dot_row<WK, D::F16, D::SPLIT>(w[r], sc[r], x, xl);
-            acc[r] = O::GROUPED ? __builtin_fmaf(d, f[r / kOneColumns], acc[r]) : acc[r] + d;
+            acc[r] = O::GROUPED ? __builtin_fmaf(d, f[r / kUpColumns], acc[r]) : acc[r] + d;
         }
     }
     const float v = fold<R>(acc);
     if (lane < R) joined[wave][lane] = v;
     __syncthreads();
-    if (threadIdx.x == 0) {                // the slices in their order
-        f32x4 g = {0, 0, 0, 0}, u = {0, 0, 0, 0};
-        for (uint32_t o = 0; o < waves; ++o) {
-            g += *reinterpret_cast<const f32x4*>(joined[o]);
-            u += *reinterpret_cast<const f32x4*>(joined[o] + kOneColumns);
-        }
-        store_h<WK>(a, blockIdx.y, n0, g, u, tensor_scale<WK>(mat[0]), tensor_scale<WK>(mat[1]));
+    if (threadIdx.x < kUpColumns && n0 + threadIdx.x < a.i) {      // the slices in their order
+        float g = 0.0f, up = 0.0f;
+        for (uint32_t o = 0; o < waves; ++o) g += joined[o][threadIdx.x], up += joined[o][kUpColumns + threadIdx.x];
+        float hi, lo;
+        terms_of(activate(g * tensor_scale<WK>(mat[0]), a.act) * (up * tensor_scale<WK>(mat[1])), hi, lo);
+        uint16_t* at = reinterpret_cast<uint16_t*>(a.h) + uint64_t(blockIdx.y) * a.h_pitch + n0 + threadIdx.x;
+        at[0] = uint16_t(cvt_bf16x2(hi, 0.0f));
+        at[uint64_t(a.pairs) * a.h_pitch] = uint16_t(cvt_bf16x2(lo, 0.0f));
     }
 }
 
-// Columns 4 * blockIdx.x .. + 3 of y: lane c of all the workgroup's lanes has chunks c, c + threads, ... of the pairs' rows, one after the
+// kDownColumns columns of y: lane c of all the workgroup's lanes has chunks c, c + threads, ... of the pairs' rows, one after the
 // other; its products take its own pair's weight and scales, and the sum over lanes is the sum over pairs.
 template <int WK>
 __global__ __launch_bounds__(64 * kOneMaxWaves) void down_one(Args a) {
     using O = One<WK>;
-    constexpr int R = kOneColumns, PAIRS = O::E / 2;
+    constexpr int R = kDownColumns, PAIRS = O::E / 2;
     __shared__ __align__(16) float joined[kOneMaxWaves][R];
     const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
     const uint32_t n0 = blockIdx.x * R, w_row = O::FP4 ? a.i / 2 : a.i, ws_row = a.i / (WK == ST_KIND_NVFP4 ? 16 : 32), groups = (a.i + 127) / 128;
@@ -420,10 +424,12 @@ __global__ __launch_bounds__(64 * kOneMaxWaves) void down_one(Args a) {
     const float v = fold<R>(acc);
     if (lane < R) joined[wave][lane] = v;
     __syncthreads();
-    if (threadIdx.x == 0) {
-        f32x4 t = {0, 0, 0, 0};
-        for (uint32_t o = 0; o < waves; ++o) t += *reinterpret_cast<const f32x4*>(joined[o]);
-        store_y(a, 0, n0, t);
+    if (threadIdx.x < R && n0 + threadIdx.x < a.n) {
+        const uint32_t n = n0 + threadIdx.x;
+        float y = 0.0f;
+        for (uint32_t o = 0; o < waves; ++o) y += joined[o][threadIdx.x];
+        if (a.res) y += load_as_f32(a.res, a.res_type, n);
+        store_as(a.out, a.out_type, n, y);
     }
 }
 
