@@ -682,6 +682,8 @@ st_status check_args(const st_kv_attention_args* g) {
                        kWho, (unsigned long long)g->tokens, (unsigned long long)g->seqs, g->heads, g->group,
                        (unsigned long long)g->pages, (unsigned long long)g->table_blocks);
     if (g->tokens == 0 || g->seqs == 0 || g->heads == 0 || g->group == 0) return ST_OK;
+    if (g->tokens * g->heads >= (uint64_t(1) << 40) / g->group)
+        return st_fail(ST_E_SHAPE, "%s: %llu tokens of %u times %u heads are too many", kWho, (unsigned long long)g->tokens, g->heads, g->group);
     if (!g->starts && g->tokens % g->seqs)
         return st_fail(ST_E_SHAPE, "%s: %llu tokens are not %llu equal parts", kWho, (unsigned long long)g->tokens, (unsigned long long)g->seqs);
     if (g->pages == 0 || g->table_blocks == 0) return st_fail(ST_E_SHAPE, "%s: a cache without pages", kWho);

@@ -11,12 +11,13 @@ They run on the current stream (or ``stream``), allocate with torch, synchronise
 graph.  They have no backward pass."""
 from __future__ import annotations
 
+import bisect
 import ctypes as C
 
 import torch
 
 from ._lib import MoeArgs, MoeRouteArgs, OUT_DTYPES, check, lib
-from .ops import _ACT, _KIND, _TORCH, _TYPE, ACTIVATIONS, _check_weight, _launch, _on_device, _overlaps, _rows
+from .ops import _ACT, _KIND, _TORCH, _TYPE, ACTIVATIONS, _check_weight, _launch, _on_device, _overlaps, _rows, _span
 
 SCORES = ("softmax", "sigmoid")     # st_route_score codes 0, 1
 MAX_TOP_K = 32                      # of moe
@@ -55,6 +56,20 @@ class MoeExperts:
                         raise ValueError(f"{who}: an fp32 scale is not 4-byte aligned")
                 table.append([w.data.data_ptr(), w.scale.data_ptr(), 0 if w.scale2 is None else w.scale2.data_ptr()])
         self.table = torch.tensor(table, dtype=torch.int64).to(self.device)
+        # what they take: disjoint ranges of bytes in rising order, and a tensor of each allocation
+        held = [t for three in self.weights for w in three for t in (w.data, w.scale, w.scale2) if t is not None and t.numel()]
+        self._spans = []
+        for a, b in sorted(map(_span, held)):
+            if self._spans and a <= self._spans[-1][1]:
+                self._spans[-1] = (self._spans[-1][0], max(b, self._spans[-1][1]))
+            else:
+                self._spans.append((a, b))
+        self._held = list({t.untyped_storage().data_ptr(): t for t in held}.values())
+
+    def _overlaps(self, t) -> bool:
+        a, b = _span(t)
+        i = bisect.bisect_left(self._spans, (b,)) - 1        # the last range that begins before t's end
+        return t.numel() > 0 and i >= 0 and self._spans[i][1] > a
 
     def __len__(self) -> int:
         return len(self.weights)
@@ -151,10 +166,8 @@ def moe(x, experts: MoeExperts, ids, weights, activation: str | None = "silu", r
         if not ((n <= 1 or o2.stride(1) == 1) and (m <= 1 or o2.stride(0) >= n)):
             raise ValueError(f"{who}: out has strides {out.stride()}")
         same = r2 is not None and r2.data_ptr() == o2.data_ptr() and r2.dtype == o2.dtype and r2.stride() == o2.stride()
-        held = [t for three in experts.weights for w in three for t in (w.data, w.scale, w.scale2)]
-        for t in (x2, ids, weights, experts.table, None if same else r2, *held):
-            if _overlaps(o2, t):
-                raise ValueError(f"{who}: out overlaps an input")
+        if experts._overlaps(o2) or any(_overlaps(o2, t) for t in (x2, ids, weights, experts.table, None if same else r2)):
+            raise ValueError(f"{who}: out overlaps an input")
     if m == 0 or n == 0:
         return out
     args = MoeArgs(x2.data_ptr(), ids.data_ptr(), weights.data_ptr(), experts.table.data_ptr(), None if r2 is None else r2.data_ptr(),
@@ -165,6 +178,6 @@ def moe(x, experts: MoeExperts, ids, weights, activation: str | None = "silu", r
     work = x.new_empty(need.value, dtype=torch.uint8)
     args.workspace, args.workspace_bytes = work.data_ptr(), need.value
     # (on another stream the experts' weights are in use there as well)
-    held = () if stream is None else [t for three in experts.weights for w in three for t in (w.data, w.scale, w.scale2)]
+    held = () if stream is None else experts._held
     _launch(lib().st_moe, args, device, stream, (x2, ids, weights, experts.table, r2, o2, work, *held), who)
     return out

@@ -248,6 +248,40 @@ def test_abi_null_and_empty():
     assert L.st_kv_attention(C.byref(a), None) == -1
 
 
+def test_attention_refuses_more_results_than_sizes_hold():
+    """Rows without end (a pitch of 0 takes no memory) must not make the workspace's size wrap around."""
+    a, need = _attention(tokens=(1 << 31) - 2, max_new=1, seqs=2, heads=64, group=65535, starts=P, q_pitch=0, out_pitch=0,
+                         table_blocks=1 << 20, table_pitch=1 << 20), C.c_uint64(7)
+    assert _lib.lib().st_kv_attention_workspace_bytes(C.byref(a), C.byref(need)) == -6 and need.value == 0
+    assert _lib.lib().st_kv_attention(C.byref(a), None) == -6
+
+
+def test_moe_out_among_the_weights(as_gpu):
+    """Experts that are views of one buffer: every place for out that touches one of them is refused, those between are not."""
+    buf, at, lists = torch.zeros(1 << 16, dtype=torch.uint8), 512, ([], [], [])
+    used = torch.zeros(1 << 16, dtype=torch.bool)
+    for e in range(5):
+        for which, shape in enumerate(((32, 64), (32, 64), (16, 32))):
+            w = ref.random_weight(st, "FP8_TENSOR", *shape, 1)
+            n = shape[0] * shape[1]
+            w.data = buf[at:at + n].view(torch.float8_e4m3fn).view(shape)
+            used[at:at + n] = True
+            at += n + 64 * ((3 * e + which) % 4)
+            lists[which].append(w)
+    ex = st.MoeExperts(*lists)
+    x, ids, weights = torch.zeros(2, 64, dtype=torch.bfloat16), torch.zeros(2, 2, dtype=I32), torch.zeros(2, 2)
+    refused = 0
+    for o in range(0, at + 512, 64):
+        out = buf[o:o + 64].view(torch.bfloat16).view(2, 16)
+        if used[o:o + 64].any():
+            refused += 1
+            with pytest.raises(ValueError, match="overlaps"):
+                st.moe(x, ex, ids, weights, out=out)
+        else:
+            st.moe(x, ex, ids, weights, out=out)
+    assert refused == 5 * (2048 + 2048 + 512) // 64
+
+
 def test_reference_append_matches_torch():
     """Scales and codes of whole pages against torch's own conversion."""
     g = torch.Generator().manual_seed(1)
