@@ -607,43 +607,53 @@ __global__ __launch_bounds__(kThreads, D * QT <= 256 ? 2 : 1) void attend_many(A
     }
 }
 
-// The parts of a row: D / 4 lanes hold a result, groups of so many lanes take every so-many-th part, in their order, and join in LDS.
+// The parts of rows: D / 4 lanes hold a result; `ways` such groups of lanes share a row, each taking every so-many-th part, and join in LDS,
+// all in the parts' order.  (A whole workgroup for a row of two parts would take longer than the attention: 32 sequences' 16 drafts, 32
+// heads of 64.)
 template <bool F16, int D>
-__global__ __launch_bounds__(kThreads) void join(Args a, uint32_t tile_rows) {
+__global__ __launch_bounds__(kThreads) void join(Args a, uint32_t tile_rows, uint32_t ways) {
     constexpr uint32_t LANES = D / 4, GROUPS = kThreads / LANES;
     __shared__ __align__(16) float sum[GROUPS][D];
     __shared__ float top[GROUPS], den[GROUPS];
     const uint32_t heads = a.s.heads * a.group, seq = blockIdx.y;
     const Span p = span_of(a.s, seq);
-    const uint32_t t = blockIdx.x / heads, h = blockIdx.x % heads;
-    if (t >= uint32_t(p.count)) return;
-    const uint32_t d = threadIdx.x % LANES * 4, mine = threadIdx.x / LANES;
-    const uint32_t rows = uint32_t(p.count) * a.group, row = t * a.group + h % a.group, row0 = row / tile_rows * tile_rows;
-    const Steps st = steps_of(a, p, row0, row0 + tile_rows < rows ? row0 + tile_rows : rows);
-    const uint32_t parts = (uint32_t(st.last - st.first) + a.chunk - 1) / a.chunk;
+    const uint32_t d = threadIdx.x % LANES * 4, mine = threadIdx.x / LANES, way = mine % ways;
+    const uint64_t item = uint64_t(blockIdx.x) * (GROUPS / ways) + mine / ways;
+    const uint32_t t = uint32_t(item / heads), h = uint32_t(item % heads);
+    const bool have = t < uint32_t(p.count);
     const uint64_t at = ((uint64_t(p.first) + t) * heads + h) * a.splits;
     float m = kNone, l = 0.0f;
     f32x4 x = {0, 0, 0, 0};
+    if (have) {
+        const uint32_t rows = uint32_t(p.count) * a.group, row = t * a.group + h % a.group, row0 = row / tile_rows * tile_rows;
+        const Steps st = steps_of(a, p, row0, row0 + tile_rows < rows ? row0 + tile_rows : rows);
+        const uint32_t parts = (uint32_t(st.last - st.first) + a.chunk - 1) / a.chunk;
+        const uint32_t n = parts > way ? (parts - way + ways - 1) / ways : 0;      // (a loop the compiler can unroll: it would wait for each load)
 #pragma unroll 4
-    for (uint32_t o = mine; o < parts; o += GROUPS) m = fmaxf(m, a.stat[at + o].x);
+        for (uint32_t i = 0; i < n; ++i) m = fmaxf(m, a.stat[at + way + i * ways].x);
 #pragma unroll 4
-    for (uint32_t o = mine; o < parts; o += GROUPS) {
-        const float2 s = a.stat[at + o];
-        const float keep = s.x == kNone ? 1.0f : __builtin_amdgcn_exp2f(s.x - m);
-        l += s.y * keep;
-        x += *reinterpret_cast<const f32x4*>(a.part + (at + o) * D + d) * keep;
+        for (uint32_t i = 0; i < n; ++i) {
+            const uint64_t o = at + way + i * ways;
+            const float2 s = a.stat[o];
+            const float keep = s.x == kNone ? 1.0f : __builtin_amdgcn_exp2f(s.x - m);
+            l += s.y * keep;
+            x += *reinterpret_cast<const f32x4*>(a.part + o * D + d) * keep;
+        }
     }
-    *reinterpret_cast<f32x4*>(&sum[mine][d]) = x;
-    if (d == 0) top[mine] = m, den[mine] = l;
-    __syncthreads();
-    if (mine != 0) return;
-    for (uint32_t o = 1; o < GROUPS; ++o) m = fmaxf(m, top[o]);
-    l = 0.0f, x = f32x4{0, 0, 0, 0};
-    for (uint32_t o = 0; o < GROUPS; ++o) {
-        const float keep = top[o] == kNone ? 1.0f : __builtin_amdgcn_exp2f(top[o] - m);
-        l += den[o] * keep;
-        x += *reinterpret_cast<const f32x4*>(&sum[o][d]) * keep;
+    if (ways > 1) {
+        *reinterpret_cast<f32x4*>(&sum[mine][d]) = x;
+        if (d == 0) top[mine] = m, den[mine] = l;
+        __syncthreads();
+        if (way != 0) return;
+        for (uint32_t o = 1; o < ways; ++o) m = fmaxf(m, top[mine + o]);
+        l = 0.0f, x = f32x4{0, 0, 0, 0};
+        for (uint32_t o = 0; o < ways; ++o) {
+            const float keep = top[mine + o] == kNone ? 1.0f : __builtin_amdgcn_exp2f(top[mine + o] - m);
+            l += den[mine + o] * keep;
+            x += *reinterpret_cast<const f32x4*>(&sum[mine + o][d]) * keep;
+        }
     }
+    if (!have) return;
     float y[4];
 #pragma unroll
     for (int c = 0; c < 4; ++c) y[c] = l == 0.0f ? 0.0f : x[c] / l;
@@ -704,7 +714,10 @@ st_status plan_of(const st_kv_attention_args& g, Plan* p) {
     if (p->rows == 0) return ST_OK;
     if (p->rows >= uint64_t(1) << 31) return st_fail(ST_E_SHAPE, "%s: %llu queries of a head are too many", kWho, (unsigned long long)p->rows);
     p->count = count;
-    p->many = p->rows > 32;
+    // Sharing a step's codes in LDS costs its barriers and fewer, larger workgroups (8192 tokens, 4 sequences, 8 heads, us of `attend` and `attend_many`;
+    // heads of 64: 64 rows 25 and 41, 128 rows 39 and 42, 256 rows 67 and 52; of 128: 32 rows 31 and 51, 64 rows 49 and 53, 128 rows 87 and 56;
+    // of 256: 32 rows 61 and 82, 48 rows 88 and 84, 64 rows 114 and 86).
+    p->many = p->rows * g.head_dim > 8192;
     p->qt = p->many || (p->rows > 16 && g.head_dim < 256) ? 2 : 1;       // (two groups of 16 rows of 256 do not fit the registers of `attend`)
     p->tile_rows = p->many ? 16 * p->qt * kWaves : 16 * p->qt;
     const uint64_t tiles = (p->rows + p->tile_rows - 1) / p->tile_rows;
@@ -713,7 +726,8 @@ st_status plan_of(const st_kv_attention_args& g, Plan* p) {
     uint64_t tokens = g.table_blocks * g.block;
     if (g.window && g.window + p->tile_rows + 2 * kStep < tokens) tokens = g.window + p->tile_rows + 2 * kStep;
     const uint64_t steps = (tokens + kStep - 1) / kStep;
-    // Parts of equal length, about eight workgroups a CU, each with four steps for each of its wavefronts at least
+    // Parts of equal length, about eight workgroups a CU (two of the larger ones), which evens out sequences of different length, each with four
+    // steps for each of its wavefronts at least
     const uint64_t want = p->many ? 512 : 2048;
     uint64_t chunk = (groups * steps + want - 1) / want;
     chunk = (chunk + kWaves - 1) / kWaves * kWaves;
@@ -743,7 +757,14 @@ void launch(const Args& a, const Plan& p, hipStream_t s) {
     if (p.many) hipLaunchKernelGGL((attend_many<F16, D, 2>), dim3(8 * p.positions * p.splits), dim3(kThreads), 0, s, a);
     else if (p.qt == 1) hipLaunchKernelGGL((attend<F16, D, 1>), dim3(p.tiles * heads * p.splits), dim3(kThreads), 0, s, a);
     else if constexpr (D < 256) hipLaunchKernelGGL((attend<F16, D, 2>), dim3(p.tiles * heads * p.splits), dim3(kThreads), 0, s, a);
-    if (p.splits > 1) hipLaunchKernelGGL((join<F16, D>), dim3(uint32_t(p.count) * a.s.heads * a.group, a.s.seqs), dim3(kThreads), 0, s, a, p.tile_rows);
+    if (p.splits > 1) {
+        constexpr uint32_t GROUPS = kThreads / (D / 4);
+        uint32_t ways = 1;             // four parts or more for each
+        while (ways < GROUPS && ways * 4 < p.splits) ways *= 2;
+        const uint32_t per = GROUPS / ways;
+        const uint64_t items = p.count * a.s.heads * a.group;
+        hipLaunchKernelGGL((join<F16, D>), dim3(uint32_t((items + per - 1) / per), a.s.seqs), dim3(kThreads), 0, s, a, p.tile_rows, ways);
+    }
 }
 
 }  // namespace

@@ -31,7 +31,7 @@ template <uint32_t E>
 __device__ __forceinline__ float element(const uint8_t* p, uint64_t i) {
     return load_as_f32(p, E, i);
 }
-// Eight elements at p + i; VEC: p and i are multiples of eight elements.
+// Eight elements at p + i; VEC: p and i are multiples of four elements.
 template <uint32_t E, bool VEC>
 __device__ __forceinline__ void load8(const uint8_t* p, uint64_t i, float* v) {
     if constexpr (VEC) {

@@ -56,11 +56,19 @@ struct Plan {
 
 st_status plan_of(const st_moe_args& g, Plan* p) {
     const uint64_t pairs = g.t * g.top;
-    p->cut = g.t == 1 ? ONE : pairs > 512 ? MANY : g.t <= 16 ? FEW : g.t <= 64 ? SOME : MANY;
+    const uint64_t slots = pairs < g.experts ? pairs : g.experts;
+    // FEW: its down products go through all experts one after the other in every workgroup.  All in us, FEW's and SOME's: 32 pairs of 8 experts
+    // (MXFP4 [1280, 4096]) 35 and 38, 64 of 128 (block FP8) 130 and 141, 64 of 64 (NVFP4 [1280, 5120]) 123 and 131, 128 of these 191 and
+    // 199, 175 and 158, 128 of 128 (MXFP4 [768, 2048]) 84 and 59.
+    // SOME: up_few reads an expert's weights from cache again for every 16 of its pairs, with a workgroup for each 16 of its columns; tiles of 64 are
+    // too few workgroups, or mostly empty.  SOME's and MANY's: block FP8, 128 experts, 4 pairs each 312 and 385, 8 each 440 and 430, 12 each 540
+    // and 504; kinds with scales of short blocks, whose decoding costs more: NVFP4, 64 experts, 8 each 323 and 381, 16 each 473 and 500, 24 each
+    // 626 and 597; MXFP8 [768, 2048], 64 experts, 16 each 186 and 226; MXFP4, 32 experts, 16 each 259 and 302.
+    const uint64_t each = g.up_kind <= ST_KIND_FP8_BLOCK128 ? 6 : 16;
+    p->cut = g.t == 1 ? ONE : g.t <= 16 && pairs <= kFewPairs ? FEW : pairs <= slots * each ? SOME : MANY;
     p->h_pitch = (g.i + 7) / 8 * 8;
     p->h_bytes = (pairs * p->h_pitch * 4 + 15) / 16 * 16;
     p->part_bytes = p->cut >= SOME ? pairs * g.n * 4 : 0;
-    const uint64_t slots = pairs < g.experts ? pairs : g.experts;
     p->part_bytes = (p->part_bytes + 15) / 16 * 16;
     p->sort_bytes = p->cut == ONE ? 0 : (4 + 4 * slots + pairs) * 4;
     // threads of each launch; a grid dimension holds fewer than 2^32, and 65535 workgroups in y (slots is below that)

@@ -22,9 +22,9 @@ struct Args {
     uint32_t vec;                 // four consecutive outputs may be stored (and residuals loaded) together
 };
 
-constexpr uint32_t kMaxTop = 32, kMaxExperts = 16384;
+constexpr uint32_t kMaxTop = 32, kMaxExperts = 16384, kFewPairs = 64;
 
-// How the work is cut (moe_kernels.h): by the tokens, of which FEW are up to 16 and SOME up to 64.
+// How the work is cut (moe_kernels.h): for one token; up_few and down_few; up_few and tiles of down; tiles.
 enum Cut { ONE, FEW, SOME, MANY };
 
 // The fewest wavefronts, at most `most`, that go through n items in as many rounds as `most` would.

@@ -7,11 +7,12 @@
 // Bound by the bytes of the chosen experts' weights; x and h, few rows, come from L2.  No atomics on results: every sum has its order.
 //  * one token: up_one, down_one, dot products on the vector unit at the rate the weights arrive; a lane has 16 bytes of a row, and in
 //    down_one the lanes go through all experts' rows as if they were one.
-//  * up to 64: up_few, a workgroup for 16 rows of gate and of up of an expert, its wavefronts taking different parts of K; down_few, a
-//    workgroup for 16 or 32 columns of y, its wavefronts taking all experts' parts of K in turn.  The columns of its instructions are the tokens,
-//    so that the sum over experts is the sum over K and needs no second pass.
-//  * more: tiles of 64 pairs of one expert by 64 rows of gate and of up, or 128 of down; x or h staged through LDS for four wavefronts, weights
-//    straight to their registers; the pairs' results pass through memory and `combine` adds them.
+//  * few pairs of an expert: up_few, a workgroup for 16 rows of gate and of up of an expert, its wavefronts taking different parts of K.
+//  * up to 16 tokens with few pairs in all: down_few, a workgroup for 16 or 32 columns of y, its wavefronts taking all experts' parts of K in turn.
+//    The columns of its instructions are the tokens, so that the sum over experts is the sum over K and needs no second pass.
+//  * else: tiles of 64 pairs of one expert by 64 rows of gate and of up, or 128 of down; x or h staged through LDS for four wavefronts, weights
+//    straight to their registers; down's results of the pairs pass through memory and `combine` adds them.
+// (moe.cpp has the borders.)
 #pragma once
 
 #include "linear_kernels.h"
@@ -433,10 +434,9 @@ __global__ __launch_bounds__(64 * kOneMaxWaves) void down_one(Args a) {
     }
 }
 
-// ------------------------------------------------------------------------- up to 16 tokens
+// ------------------------------------------------------------------------- few pairs of an expert
 
 constexpr int kUpWaves = 4;
-constexpr uint32_t kFewPairs = 512;
 
 template <int X, int WK, Ends TAIL>
 __global__ __launch_bounds__(64 * kUpWaves) void up_few(Args a) {
@@ -483,67 +483,39 @@ __global__ __launch_bounds__(64 * kUpWaves) void up_few(Args a) {
     }
 }
 
-// Entries: each expert that some token has; a second one for tokens that have it twice, and so on.  An entry's tokens are bits of a mask,
-// their pairs a part of `list` in the tokens' order.
+// Entries: each expert that some token has; a second one for tokens that have it twice, and so on.
 constexpr int kDownWaves = 16;
-static_assert(kFewPairs <= 64 * kDownWaves, "a thread for each pair");
+static_assert(kFewPairs == 64, "a lane for each pair");
 
 template <int WK, int NG, Ends TAIL>
 __global__ __launch_bounds__(64 * kDownWaves) void down_few(Args a) {
     using F = Turn<WK>;
     __shared__ __align__(16) float joined[kDownWaves][NG][256];
-    __shared__ __align__(16) uint32_t key[64 * kDownWaves];
-    __shared__ uint32_t mask[64 * kDownWaves];
-    __shared__ uint16_t entry[kFewPairs], expert[kFewPairs], list[kFewPairs], base[kFewPairs];
-    __shared__ uint32_t leaders[kDownWaves];
+    __shared__ __align__(16) uint8_t pair_of[kFewPairs][16];      // an entry's pair of each token; kFewPairs: none
+    __shared__ uint32_t expert[kFewPairs], number;
     const int lane = threadIdx.x & 63, row = lane & 15, q = lane >> 4;
-    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), p = threadIdx.x;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t n0 = blockIdx.x * (16 * NG);
-
-    const int32_t id = p < a.pairs ? a.ids[p] : -1;
-    const bool valid = id >= 0 && uint32_t(id) < a.experts;
-    uint32_t mine = ~0u;
-    if (valid) {
+    if (wave == 0) {
+        const uint32_t p = lane, j = p % a.top, none = kFewPairs * 0x01010101u;
+        *reinterpret_cast<u32x4*>(pair_of[p]) = u32x4{none, none, none, none};
+        const int32_t id = p < a.pairs ? a.ids[p] : -1;
+        const bool valid = id >= 0 && uint32_t(id) < a.experts;
         uint32_t again = 0;
-        for (uint32_t o = p / a.top * a.top; o < p; ++o) again += a.ids[o] == id ? 1 : 0;
-        mine = uint32_t(id) * kMaxTop + again;
-    }
-    key[p] = mine;
-    mask[p] = 0;
-    __syncthreads();
-    uint32_t first = p;
-    for (uint32_t o = 0; valid && o < p; o += 4) {
-        const u32x4 k = *reinterpret_cast<const u32x4*>(&key[o]);
-#pragma unroll
-        for (uint32_t i = 0; i < 4; ++i) first = k[i] == mine && o + i < first ? o + i : first;
-    }
-    const bool leads = valid && first == p;
-    const uint64_t m = __ballot(leads);
-    if (lane == 0) leaders[wave] = __popcll(m);
-    __syncthreads();
-    uint32_t entries = 0, before = 0;
-#pragma unroll
-    for (uint32_t o = 0; o < kDownWaves; ++o) {
-        before += o < wave ? leaders[o] : 0;
-        entries += leaders[o];
-    }
-    if (leads) {
-        const uint32_t at = before + __popcll(m & ((uint64_t(1) << lane) - 1));
-        entry[p] = uint16_t(at);
-        expert[at] = uint16_t(id);
+        for (uint32_t o = 0; o < a.top; ++o) again += __shfl(id, int(p - j + o)) == id && o < j ? 1 : 0;
+        const uint32_t key = valid ? uint32_t(id) * kMaxTop + again : ~0u;
+        uint32_t first = p;
+        for (uint32_t o = 0; o < a.pairs; ++o) first = uint32_t(__builtin_amdgcn_readlane(int(key), int(o))) == key && o < first ? o : first;
+        const uint64_t leaders = __ballot(valid && first == p);
+        if (valid) {
+            const uint32_t at = __popcll(leaders & ((uint64_t(1) << first) - 1));
+            pair_of[at][p / a.top] = uint8_t(p);
+            expert[at] = uint32_t(id);
+        }
+        if (lane == 0) number = __popcll(leaders);
     }
     __syncthreads();
-    const uint32_t t = p / a.top, en0 = valid ? entry[first] : 0;
-    if (valid) atomicOr(&mask[en0], 1u << t);
-    __syncthreads();
-    if (p < entries) {
-        uint32_t b = 0;
-        for (uint32_t o = 0; o < p; ++o) b += __popc(mask[o]);
-        base[p] = uint16_t(b);
-    }
-    __syncthreads();
-    if (valid) list[base[en0] + __popc(mask[en0] & ((1u << t) - 1))] = uint16_t(p);
-    __syncthreads();
+    const uint32_t entries = number;
 
     uint32_t n[NG];
 #pragma unroll
@@ -558,9 +530,9 @@ __global__ __launch_bounds__(64 * kDownWaves) void down_few(Args a) {
     const uint64_t plane = uint64_t(a.pairs) * a.h_pitch * 2;
     for (uint32_t item = wave; item < items; item += kDownWaves) {
         const uint32_t en = item / turns, k0 = item % turns * F::SS;
-        const uint32_t e = __builtin_amdgcn_readfirstlane(expert[en]), has = mask[en];
-        const bool have = has >> row & 1;
-        const uint32_t pr = list[base[en] + (have ? __popc(has & ((1u << row) - 1)) : 0)];
+        const uint32_t e = __builtin_amdgcn_readfirstlane(expert[en]), of = pair_of[en][row];
+        const bool have = of < kFewPairs;
+        const uint32_t pr = have ? of : 0;          // (lanes without a pair: their columns of the result are not used)
         const float weight = a.weights[pr];
         const uint8_t* ph = a.h + uint64_t(pr) * a.h_pitch * 2;
         Matrix mat[NG];
@@ -597,7 +569,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void down_few(Args a) {
     }
 }
 
-// ------------------------------------------------------------------------- more tokens
+// ------------------------------------------------------------------------- tiles
 
 constexpr int kTileRows = 64, kTileThreads = 256, kUpK = 128;
 // Steps of K (40 tokens through MXFP4's down [5120, 1280]: 46 us with 128, 64 with 64; 320 through block FP8's [4096, 1280]: 237 and 223)
