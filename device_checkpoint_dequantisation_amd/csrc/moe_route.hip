@@ -5,9 +5,10 @@
 // sums good to 2^-50), and everything behind it too.
 //  * logits: 16 tokens by 16 experts a workgroup, on the fp64 matrix instructions (16 x 16 x 4, 64 cycles), which take one converted number
 //    per lane and side; the wavefronts have parts of K and join in LDS.  777 tokens, 256 experts of 5120: bound by those instructions
-//    (2 GFLOP at the 68 TFLOP/s that a large fp64 product reaches: 30 us).
+//    (2 GFLOP at the 68 TFLOP/s that a large fp64 product reaches: 30 us) and by how 784 tiles
+//    go into 256 CUs: 60 us.
 //  * choose: a token's scores in LDS; an expert's place is the number of those ahead of it, counted by one lane each, so that nothing
-//    waits for a chain of maxima.
+//    waits for a chain of maxima.  777 tokens, 256 experts: 10.5 us; one token, 128 experts: 4.8, of which the launch is most.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>

@@ -737,9 +737,9 @@ typedef struct st_moe_args {
     void* out;               /* [t, n] */
     void* workspace;         /* st_moe_workspace_bytes bytes, 16-byte aligned, this call's own until it is done */
     uint64_t workspace_bytes;
-    uint64_t t, k, i, n;     /* t * top below 2^24, the others below 2^31 */
+    uint64_t t, k, i, n;     /* t * top and i and n below 2^24, k below 2^31 */
     uint64_t x_pitch, residual_pitch, out_pitch;
-    uint32_t experts, top;   /* top <= 32 */
+    uint32_t experts, top;   /* at most 16384 and 32 */
     uint32_t x_type;         /* ST_X_BF16 or ST_X_F16 */
     uint32_t up_kind, down_kind;   /* st_kind, ST_KIND_FP8_TENSOR .. ST_KIND_MXFP4 */
     uint32_t activation;     /* st_activation */
