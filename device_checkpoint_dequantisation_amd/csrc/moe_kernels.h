@@ -136,11 +136,11 @@ struct Codes {
             }
         }
     }
-    // acc += the products with this lane's row at px (its second term at pl), with the scales of blocks.  Lanes that have no row are given
-    // another's: their columns of the result are not used.
+    // acc += the products with this lane's row at px (its second term at pl), with the scales of blocks.  Lanes that do not `have` a row load
+    // nothing, their columns are 0 (40 fp16 tokens through MXFP4, 6 pairs an expert: 74 us, 83 when they load another's row).
     // (PARTS of x at a time, which bounds the registers it takes)
     template <bool F16, Rows R, Ends END, int PARTS>
-    __device__ __forceinline__ void times(const uint8_t* px, const uint8_t* pl, uint32_t k0, uint32_t K, f32x4 (&acc)[NG]) const {
+    __device__ __forceinline__ void times(const uint8_t* px, const uint8_t* pl, uint32_t k0, uint32_t K, f32x4 (&acc)[NG], bool have) const {
         const int q = (threadIdx.x & 63) >> 4;
         constexpr int XL = F::CK / 8;
         constexpr int HALF = F::CHUNKS / PARTS;
@@ -154,11 +154,20 @@ struct Codes {
             for (int j = 0; j < HALF; ++j)
 #pragma unroll
                 for (int h = 0; h < XL; ++h) {
-                    const int at = 2 * (F::GROUPED ? 64 : F::CK) * (half * HALF + j) + 16 * h;
-                    xr[j][h] = load_piece<END>(px + to + at, left - at, 2 * K);
-                    if constexpr (R == TWO) xl[j][h] = load_piece<END>(pl + to + at, left - at, 2 * K);
-                    if constexpr (R == SPLIT) split_f16(xr[j][h], xr[j][h], xl[j][h]);
+                    xr[j][h] = u32x4{0, 0, 0, 0};
+                    if constexpr (R != PLAIN) xl[j][h] = u32x4{0, 0, 0, 0};
                 }
+            if (have) {
+#pragma unroll
+                for (int j = 0; j < HALF; ++j)
+#pragma unroll
+                    for (int h = 0; h < XL; ++h) {
+                        const int at = 2 * (F::GROUPED ? 64 : F::CK) * (half * HALF + j) + 16 * h;
+                        xr[j][h] = load_piece<END>(px + to + at, left - at, 2 * K);
+                        if constexpr (R == TWO) xl[j][h] = load_piece<END>(pl + to + at, left - at, 2 * K);
+                        if constexpr (R == SPLIT) split_f16(xr[j][h], xr[j][h], xl[j][h]);
+                    }
+            }
 #pragma unroll
             for (int i = 0; i < NG; ++i) {
                 f32x4 c = F::GROUPED ? f32x4{0, 0, 0, 0} : acc[i];
@@ -437,7 +446,7 @@ __global__ __launch_bounds__(64 * kOneMaxWaves) void down_one(Args a) {
 // ------------------------------------------------------------------------- few pairs of an expert
 
 // Bound by the weights' bytes: 8 tokens of 8 block-FP8 experts of 128 [1280, 4096] (39 to 47 different ones, 10.5 MB each) 83 us, 5 TB/s and more.  With
-// fp16 rows through MXFP4 (40 tokens, 4 of 32 experts [1280, 5120], 24 or 25 different ones of 7 MB) by decoding: each row meets the weights as two bf16 terms, 84 us.
+// fp16 rows through MXFP4 (40 tokens, 4 of 32 experts [1280, 5120], 24 or 25 different ones of 7 MB) by decoding: each row meets the weights as two bf16 terms, 74 us.
 constexpr int kUpWaves = 4;
 
 template <int X, int WK, Ends TAIL>
@@ -464,7 +473,7 @@ __global__ __launch_bounds__(64 * kUpWaves) void up_few(Args a) {
                 constexpr Ends END = decltype(ending)::value;
                 Codes<WK, 2> codes;
                 codes.template load<END>(mat, n, k0, a.k);
-                codes.template times<D::F16, R, END, 2>(px, nullptr, k0, a.k, acc);
+                codes.template times<D::F16, R, END, 2>(px, nullptr, k0, a.k, acc, have);
             };
             if (k0 + F::SS <= a.k) turn(Ending<WITHIN>{});
             else turn(Ending<TAIL>{});
@@ -485,8 +494,8 @@ __global__ __launch_bounds__(64 * kUpWaves) void up_few(Args a) {
     }
 }
 
-// 8 tokens of 8 experts of 128 (block FP8 [4096, 1280], 39 to 47 different ones, 5.2 MB each): 72 us, 3 TB/s, one workgroup of 16 wavefronts a CU, each
-// of whose turns waits for its codes and for two terms of h.
+// 8 tokens of 8 experts of 128 (block FP8 [4096, 1280], 39 to 47 different ones, 5.2 MB each): 70 us, 3 TB/s and more.  Not for want of loads in flight (two
+// turns' codes at once: the same); the two terms of h are four times the codes' bytes through the CU's cache.
 // Entries: each expert that some token has; a second one for tokens that have it twice, and so on.
 constexpr int kDownWaves = 16;
 static_assert(kFewPairs == 64, "a lane for each pair");
@@ -536,7 +545,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void down_few(Args a) {
         const uint32_t en = item / turns, k0 = item % turns * F::SS;
         const uint32_t e = __builtin_amdgcn_readfirstlane(expert[en]), of = pair_of[en][row];
         const bool have = of < kFewPairs;
-        const uint32_t pr = have ? of : 0;          // (lanes without a pair: their columns of the result are not used)
+        const uint32_t pr = have ? of : 0;
         const float weight = a.weights[pr];
         const uint8_t* ph = a.h + uint64_t(pr) * a.h_pitch * 2;
         Matrix mat[NG];
@@ -550,7 +559,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void down_few(Args a) {
             constexpr Ends END = decltype(ending)::value;
             Codes<WK, NG> codes;
             codes.template load<END>(mat, n, k0, a.i);
-            codes.template times<false, TWO, END, NG>(ph, ph + plane, k0, a.i, acc);
+            codes.template times<false, TWO, END, NG>(ph, ph + plane, k0, a.i, acc, have);
         };
         if (k0 + F::SS <= a.i) turn(Ending<WITHIN>{});
         else turn(Ending<TAIL>{});
