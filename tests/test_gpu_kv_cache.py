@@ -182,6 +182,20 @@ def test_long(dim, heads, group):
     _attend(q, cache, table, lengths, starts, window=5000)
 
 
+@pytest.mark.parametrize("dim,heads,group,count", [(64, 1, 1, 3), (64, 3, 3, 11), (128, 2, 2, 5), (128, 1, 5, 30), (256, 1, 3, 2), (256, 2, 1, 40)])
+@pytest.mark.parametrize("longest", [1100, 2300, 5000, 17000])
+def test_parts(dim, heads, group, count, longest):
+    """Two parts to many, of sequences that have all of them, some, one and none."""
+    lengths, counts = [longest, 0, longest // 2, 40], [count, 2, 1, count]
+    q, cache, table, starts = _case(heads, group, dim, 64, lengths, counts, "bf16", gap=1)
+    print(f"attention parts {dim} {heads} {group} {count} {longest}", flush=True)
+    out = torch.full(q.shape, 7.0, dtype=q.dtype, device=DEV)
+    got = st.kv_attention(q.to(DEV), kv.to(cache, DEV), _i32(table), _i32(lengths), starts=_i32(starts), out=out)
+    want, tol = kv.attention(q, cache, table, lengths, starts)
+    kv.check(got[1:-1], want[1:-1], tol[1:-1])
+    assert (out[0] == 7).all() and (out[-1] == 7).all()
+
+
 def test_rows_that_see_nothing():
     """More queries than tokens, sequences of no tokens, tokens on no page."""
     lengths, counts = [3, 0, 40], [7, 2, 5]

@@ -115,6 +115,32 @@ def test_many_experts_few_rows():
         _check(_rows(m, 64, "f16", m), lists, ex, ids, torch.rand(m, top, generator=torch.Generator().manual_seed(1)), out_dtype="f32")
 
 
+@pytest.mark.parametrize("kind", KINDS)
+def test_pairs_of_one_wavefront(kind):
+    """Up to 16 tokens and 64 pairs, all of them used, with experts that a token has many times."""
+    lists = mref.random_experts(st, kind, kind, 6, 96, 288, 72, 12)
+    ex = _gpu(lists)
+    for m, top in ((2, 32), (16, 4), (9, 7), (3, 21), (16, 1)):
+        print(f"moe one wavefront {kind} {m} {top}", flush=True)
+        g = torch.Generator().manual_seed(100 * m + top)
+        w = torch.rand(m, top, generator=g)
+        for ids in (torch.randint(-1, 7, (m, top), generator=g, dtype=torch.int32), torch.full((m, top), 3, dtype=torch.int32),
+                    torch.arange(m * top, dtype=torch.int32).view(m, top) % 6):
+            _check(_rows(m, 288, "bf16", m), lists, ex, ids.contiguous(), w, out_dtype="f32")
+
+
+@pytest.mark.parametrize("kind,dt", [("FP8_BLOCK128", "bf16"), ("NVFP4", "f16"), ("MXFP8", "f16")])
+def test_few_pairs_on_average(kind, dt):
+    """Many experts, most of whose pairs are one's: it has them in many turns of 16."""
+    lists = mref.random_experts(st, kind, kind, 40, 64, 288, 40, 13)
+    ex = _gpu(lists)
+    for m, top in ((30, 4), (17, 8), (70, 3)):
+        print(f"moe one busy {kind} {m} {top}", flush=True)
+        ids = torch.full((m, top), 31, dtype=torch.int32)
+        ids[1::3, 0] = torch.arange(len(ids[1::3]), dtype=torch.int32) % 40
+        _check(_rows(m, 288, dt, m), lists, ex, ids, torch.rand(m, top, generator=torch.Generator().manual_seed(m)), out_dtype="f32")
+
+
 def test_nan_stays_with_its_rows():
     """NaN and infinities in one row, in one expert's weights, in a weight of a slot: nobody else's result changes."""
     for m in (8, 60):
