@@ -141,7 +141,7 @@ def kv_attention(q, cache: QuantizedKvCache, table, lengths, starts=None, max_ne
 
     ``table``, ``lengths``, ``starts`` and ``max_new`` are those of :func:`kv_append`.  ``causal``: the queries are the last tokens of
     their sequence and each sees the tokens up to its own, with a ``window`` the last ``window`` of them; not causal: each sees all
-    ``lengths[s]`` tokens, such as an encoder's, and a sequence may have more queries than tokens.  A query that sees no token gives 0.
+    ``lengths[s]`` tokens, such as an encoder's, and a sequence may have more queries than tokens.  A query that sees no token, or only scores of minus infinity, gives 0.
     Tokens that a query does not see, and what pages hold behind a sequence's end, have no part in its result.
     Rows that belong to no sequence (before ``starts[0]``, from ``starts[-1]`` on, behind ``max_new``) stay as they are in ``out`` and are
     0 without one.  Scores and sums are fp32; the softmax's numerators enter the second product with fp16's 11 bits, fp16 queries with values
