@@ -5,7 +5,7 @@
 // Arithmetic.  Key codes are exact in bf16 and fp16, so q meets them as it is, in q's type; the block's power of two multiplies the
 // fp32 score.  The numerators, 2^(s f - m + 6), enter the second product in fp16: m is the largest score until another passes it by 2^8, which
 // leaves them below 2^15 and 30 binades above fp16's smallest step.  Value codes are exact in fp16 too; a block's
-// power of two is taken relative to the largest, 2^E, that the wavefront has met, so that a value is exact unless its block's is 2^15
+// power of two is taken relative to the largest, 2^E, of those that a row of the wavefront has seen, so that a value is exact unless its block's is 2^15
 // below that (then to 2^-33 of the largest magnitude).  l sums the numerators as
 // they enter there.  Maxima, sums and results are fp32.
 //
@@ -98,6 +98,7 @@ struct Wave {
     int32_t lo[QT], hi[QT];
     int32_t e = -1;                        // E + 127, -1: no values yet
     int32_t all_lo, all_hi;                // tokens that every row sees
+    int32_t any_lo, any_hi;                // tokens that some row sees
 
     __device__ __forceinline__ void start(const Args& a, const Span& p, uint32_t head, uint32_t row0, uint32_t rows) {
         const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
@@ -116,7 +117,8 @@ struct Wave {
             for (int d = 0; d < DT; ++d) o[j][d] = f32x4{0, 0, 0, 0}, nan[j][d / 8] = 0;
         }
         const uint32_t last = row0 + 16 * QT < rows ? row0 + 16 * QT : rows;
-        all_lo = sees(a, p, last - 1).lo, all_hi = sees(a, p, row0).hi;
+        const Sees s0 = sees(a, p, row0), s1 = sees(a, p, last - 1);
+        all_lo = s1.lo, all_hi = s0.hi, any_lo = s0.lo, any_hi = s1.hi;
     }
 
     // One step of tokens from t0.  k(t, i), v(d): its codes, 16 bytes of K tile t and of V^T tile d; ks, vs: the scale codes of lane
@@ -207,8 +209,9 @@ struct Wave {
         }
         // the largest power of two so far
         int32_t now = known ? int32_t(vs == 255 ? 0 : vs) : -1;
-        now = now > e ? now : e;
         if (__any(now > e)) {
+            // of lane groups whose 16 tokens some row sees: the others' pages (behind a sequence's end, ahead of a window) may have any
+            now = at < any_hi && at + 16 > any_lo && now > e ? now : e;
             int32_t o1 = __shfl_xor(now, 16);
             now = now > o1 ? now : o1;
             o1 = __shfl_xor(now, 32);
@@ -224,8 +227,10 @@ struct Wave {
             }
             e = now;
         }
-        const int32_t by = int32_t(vs) - e + 127;
-        const float vf = as_f32(vs == 255 ? 0x7F800000u : uint32_t(by < 0 ? 0 : by) << 23);
+        // (a factor above 1 is one of a page that nobody sees, whose numerators are 0: it must be finite)
+        int32_t by = int32_t(vs) - e + 127;
+        by = by < 0 ? 0 : by > 127 ? 127 : by;
+        const float vf = as_f32(vs == 255 ? 0x7F800000u : uint32_t(by) << 23);
         // Tokens that some rows do not see may hold anything.
         uint32_t found = 0;
         if (!inside) {
@@ -507,9 +512,6 @@ __global__ __launch_bounds__(kThreads, D * QT <= 256 ? 2 : 1) void attend_many(A
     const bool work = mine < end;
     W w;
     w.start(a, p, head, work ? mine : row0, rows);
-    // tokens that some row of this wavefront sees
-    const uint32_t mine_end = mine + 16 * QT < end ? mine + 16 * QT : end;
-    const int32_t any_lo = work ? sees(a, p, mine).lo : 0, any_hi = work ? sees(a, p, mine_end - 1).hi : 0;
 
     const uint32_t bl = a.s.block_log2, block = 1u << bl;
     const uint64_t page_bytes = uint64_t(block) * D;
@@ -571,7 +573,7 @@ __global__ __launch_bounds__(kThreads, D * QT <= 256 ? 2 : 1) void attend_many(A
             issue(s2, buf + kStages - 1 < kStages ? buf + kStages - 1 : buf - 1, on ? page : next_page, on ? base : base + 16);
         }
         const int32_t t0 = step * kStep;
-        if (t0 < any_hi && t0 + kStep > any_lo) {
+        if (work && t0 < w.any_hi && t0 + kStep > w.any_lo) {
             const uint8_t* sk = lds + buf * STAGE;
             auto k = [&](int t, int h) {
                 return *reinterpret_cast<const u32x4*>(sk + (16 * t + r) * D + ((W::KL * g + h) ^ swizzle<KC>(16 * t + r)) * 16);
