@@ -27,12 +27,19 @@ static_assert(sizeof(st_kv_attention_args) == 208, "the ctypes declaration has t
 
 constexpr int kWaves = 4, kThreads = 64 * kWaves, kStep = 64;
 
+// An unfinished result is a sum of numerators times values, in units of 2^(e - 127): its m and l, and e (-1 where l is 0).  A sum in
+// units of 1 would pass fp32's range for values above 2^64, whose mean does not.
+struct Part {
+    float m, l;
+    int32_t e;
+};
+
 struct Args {
     Seqs s;
     const uint8_t *q, *k, *v, *ks, *vs;
     uint8_t* out;
     float* part;                  // [tokens * query heads][splits][D] unfinished results, or null
-    float2* stat;                 // [tokens * query heads][splits] their m and l
+    Part* stat;                   // [tokens * query heads][splits]
     uint64_t q_pitch, q_head_pitch, out_pitch, out_head_pitch;
     uint32_t group, causal, window;
     uint32_t tiles, splits, chunk;   // row tiles of a head, parts of the tokens, steps of a part
@@ -285,12 +292,14 @@ struct Wave {
             __builtin_amdgcn_sched_barrier(0);
         }
     }
-    // o, with 2^E and a factor of the row's
-    __device__ __forceinline__ f32x4 result(int j, int d, float by) const {
+    // The exponent of a row's units.
+    __device__ __forceinline__ int32_t units(int j) const { return l[j][0] == 0.0f ? -1 : e; }
+    // o times a factor of the row's and 2^up
+    __device__ __forceinline__ f32x4 result(int j, int d, float by, int32_t up) const {
         f32x4 x;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            x[i] = __builtin_amdgcn_ldexpf(o[j][d][i] * by, e < 0 ? 0 : e - 127);
+            x[i] = __builtin_amdgcn_ldexpf(o[j][d][i] * by, up);
             if (nan[j][d / 8] >> (d % 8 * 4 + i) & 1) x[i] = __builtin_nanf("");
         }
         return x;
@@ -314,6 +323,7 @@ __global__ __launch_bounds__(kThreads, D * QT <= 128 ? 2 : 1) void attend(Args a
     constexpr int ROWS = 16 * QT, PITCH = D + 4;
     __shared__ __align__(16) float sum[ROWS][PITCH];
     __shared__ float top[kWaves][ROWS], den[kWaves][ROWS];
+    __shared__ int32_t unit[kWaves][ROWS];
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     uint32_t b = blockIdx.x;
@@ -377,18 +387,22 @@ __global__ __launch_bounds__(kThreads, D * QT <= 128 ? 2 : 1) void attend(Args a
     }
 #pragma unroll
     for (int j = 0; j < QT; ++j) {
-        if (g == 0) top[wave][16 * j + r] = w.m[j], den[wave][16 * j + r] = w.l[j][0];
+        if (g == 0) top[wave][16 * j + r] = w.m[j], den[wave][16 * j + r] = w.l[j][0], unit[wave][16 * j + r] = w.units(j);
     }
     __syncthreads();
     float m[QT];
 #pragma unroll
     for (int j = 0; j < QT; ++j) {
         m[j] = kNone;
+        int32_t e = -1;
 #pragma unroll
-        for (int o = 0; o < kWaves; ++o) m[j] = fmaxf(m[j], top[o][16 * j + r]);
+        for (int o = 0; o < kWaves; ++o) {
+            m[j] = fmaxf(m[j], top[o][16 * j + r]);
+            e = unit[o][16 * j + r] > e ? unit[o][16 * j + r] : e;
+        }
         const float keep = w.m[j] == kNone ? 1.0f : __builtin_amdgcn_exp2f(w.m[j] - m[j]);
 #pragma unroll
-        for (int d = 0; d < W::DT; ++d) w.o[j][d] = w.result(j, d, keep);
+        for (int d = 0; d < W::DT; ++d) w.o[j][d] = w.result(j, d, keep, w.units(j) - e);
     }
 #pragma unroll
     for (int o = 0; o < kWaves; ++o) {
@@ -406,8 +420,9 @@ __global__ __launch_bounds__(kThreads, D * QT <= 128 ? 2 : 1) void attend(Args a
     for (uint32_t i4 = threadIdx.x; i4 < (end - row0) * (D / 4); i4 += kThreads) {
         const uint32_t rr = i4 / (D / 4), d = i4 % (D / 4) * 4, row = row0 + rr;
         float t = kNone, l = 0.0f;
+        int32_t e = -1;
 #pragma unroll
-        for (int o = 0; o < kWaves; ++o) t = fmaxf(t, top[o][rr]);
+        for (int o = 0; o < kWaves; ++o) t = fmaxf(t, top[o][rr]), e = unit[o][rr] > e ? unit[o][rr] : e;
 #pragma unroll
         for (int o = 0; o < kWaves; ++o) l += top[o][rr] == kNone ? den[o][rr] : den[o][rr] * __builtin_amdgcn_exp2f(top[o][rr] - t);
         f32x4 x = *reinterpret_cast<const f32x4*>(&sum[rr][d]);
@@ -415,11 +430,11 @@ __global__ __launch_bounds__(kThreads, D * QT <= 128 ? 2 : 1) void attend(Args a
         if (a.splits > 1) {
             const uint64_t at = (tok * a.s.heads * a.group + h) * a.splits + split;
             *reinterpret_cast<f32x4*>(a.part + at * D + d) = x;
-            if (d == 0) a.stat[at] = float2{t, l};
+            if (d == 0) a.stat[at] = Part{t, l, e};
         } else {
             float y[4];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) y[c] = l == 0.0f ? 0.0f : x[c] / l;
+            for (int c = 0; c < 4; ++c) y[c] = l == 0.0f ? 0.0f : __builtin_amdgcn_ldexpf(x[c] / l, e - 127);
             store_row4<F16>(a, tok * a.out_pitch + h * a.out_head_pitch + d, y);
         }
     }
@@ -592,13 +607,14 @@ __global__ __launch_bounds__(kThreads, D * QT <= 256 ? 2 : 1) void attend_many(A
     for (int j = 0; j < QT; ++j) {
         const float l = w.l[j][0];
         const float inv = a.splits > 1 ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
+        const int32_t e = w.units(j), up = a.splits > 1 || e < 0 ? 0 : e - 127;
 #pragma unroll
-        for (int d = 0; d < W::DT; ++d) *reinterpret_cast<f32x4*>(mem + r * PITCH + 16 * d + 4 * g) = w.result(j, d, inv);
+        for (int d = 0; d < W::DT; ++d) *reinterpret_cast<f32x4*>(mem + r * PITCH + 16 * d + 4 * g) = w.result(j, d, inv, up);
         const uint32_t first = mine + 16 * j;
         if (a.splits > 1 && g == 0 && first + r < end) {
             const uint32_t row = first + r;
             const uint64_t at = ((uint64_t(p.first) + row / a.group) * a.s.heads * a.group + head * a.group + row % a.group) * a.splits + split;
-            a.stat[at] = float2{w.m[j], l};
+            a.stat[at] = Part{w.m[j], l, e};
         }
 #pragma unroll 1
         for (int i4 = lane; i4 < 16 * (D / 4); i4 += 64) {
@@ -624,6 +640,7 @@ __global__ __launch_bounds__(kThreads) void join(Args a, uint32_t tile_rows, uin
     constexpr uint32_t LANES = D / 4, GROUPS = kThreads / LANES;
     __shared__ __align__(16) float sum[GROUPS][D];
     __shared__ float top[GROUPS], den[GROUPS];
+    __shared__ int32_t unit[GROUPS];
     const uint32_t heads = a.s.heads * a.group, seq = blockIdx.y;
     const Span p = span_of(a.s, seq);
     const uint32_t d = threadIdx.x % LANES * 4, mine = threadIdx.x / LANES, way = mine % ways;
@@ -632,40 +649,49 @@ __global__ __launch_bounds__(kThreads) void join(Args a, uint32_t tile_rows, uin
     const bool have = t < uint32_t(p.count);
     const uint64_t at = ((uint64_t(p.first) + t) * heads + h) * a.splits;
     float m = kNone, l = 0.0f;
+    int32_t e = -1;
     f32x4 x = {0, 0, 0, 0};
+    auto scaled = [](f32x4 v, float by, int32_t up) {
+        v *= by;
+        return f32x4{__builtin_amdgcn_ldexpf(v[0], up), __builtin_amdgcn_ldexpf(v[1], up), __builtin_amdgcn_ldexpf(v[2], up), __builtin_amdgcn_ldexpf(v[3], up)};
+    };
     if (have) {
         const uint32_t rows = uint32_t(p.count) * a.group, row = t * a.group + h % a.group, row0 = row / tile_rows * tile_rows;
         const Steps st = steps_of(a, p, row0, row0 + tile_rows < rows ? row0 + tile_rows : rows);
         const uint32_t parts = (uint32_t(st.last - st.first) + a.chunk - 1) / a.chunk;
         const uint32_t n = parts > way ? (parts - way + ways - 1) / ways : 0;      // (a loop the compiler can unroll: it would wait for each load)
 #pragma unroll 4
-        for (uint32_t i = 0; i < n; ++i) m = fmaxf(m, a.stat[at + way + i * ways].x);
+        for (uint32_t i = 0; i < n; ++i) {
+            const Part s = a.stat[at + way + i * ways];
+            m = fmaxf(m, s.m);
+            e = s.e > e ? s.e : e;
+        }
 #pragma unroll 4
         for (uint32_t i = 0; i < n; ++i) {
             const uint64_t o = at + way + i * ways;
-            const float2 s = a.stat[o];
-            const float keep = s.x == kNone ? 1.0f : __builtin_amdgcn_exp2f(s.x - m);
-            l += s.y * keep;
-            x += *reinterpret_cast<const f32x4*>(a.part + o * D + d) * keep;
+            const Part s = a.stat[o];
+            const float keep = s.m == kNone ? 1.0f : __builtin_amdgcn_exp2f(s.m - m);
+            l += s.l * keep;
+            x += scaled(*reinterpret_cast<const f32x4*>(a.part + o * D + d), keep, s.e - e);
         }
     }
     if (ways > 1) {
         *reinterpret_cast<f32x4*>(&sum[mine][d]) = x;
-        if (d == 0) top[mine] = m, den[mine] = l;
+        if (d == 0) top[mine] = m, den[mine] = l, unit[mine] = e;
         __syncthreads();
         if (way != 0) return;
-        for (uint32_t o = 1; o < ways; ++o) m = fmaxf(m, top[mine + o]);
+        for (uint32_t o = 1; o < ways; ++o) m = fmaxf(m, top[mine + o]), e = unit[mine + o] > e ? unit[mine + o] : e;
         l = 0.0f, x = f32x4{0, 0, 0, 0};
         for (uint32_t o = 0; o < ways; ++o) {
             const float keep = top[mine + o] == kNone ? 1.0f : __builtin_amdgcn_exp2f(top[mine + o] - m);
             l += den[mine + o] * keep;
-            x += *reinterpret_cast<const f32x4*>(&sum[mine + o][d]) * keep;
+            x += scaled(*reinterpret_cast<const f32x4*>(&sum[mine + o][d]), keep, unit[mine + o] - e);
         }
     }
     if (!have) return;
     float y[4];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) y[c] = l == 0.0f ? 0.0f : x[c] / l;
+    for (int c = 0; c < 4; ++c) y[c] = l == 0.0f ? 0.0f : __builtin_amdgcn_ldexpf(x[c] / l, e - 127);
     store_row4<F16>(a, (uint64_t(p.first) + t) * a.out_pitch + uint64_t(h) * a.out_head_pitch + d, y);
 }
 
@@ -755,7 +781,7 @@ st_status plan_of(const st_kv_attention_args& g, Plan* p) {
     p->tiles = uint32_t(tiles), p->splits = uint32_t(splits), p->chunk = uint32_t(chunk);
     if (splits > 1) {
         const uint64_t n = g.tokens * g.heads * g.group * splits;
-        p->part_bytes = n * g.head_dim * 4, p->stat_bytes = n * 8;
+        p->part_bytes = n * g.head_dim * 4, p->stat_bytes = n * sizeof(Part);
     }
     return ST_OK;
 }
@@ -810,7 +836,7 @@ extern "C" st_status st_kv_attention(const st_kv_attention_args* g, void* stream
     a.out = static_cast<uint8_t*>(g->out);
     if (need) {
         a.part = static_cast<float*>(g->workspace);
-        a.stat = reinterpret_cast<float2*>(static_cast<uint8_t*>(g->workspace) + p.part_bytes);
+        a.stat = reinterpret_cast<Part*>(static_cast<uint8_t*>(g->workspace) + p.part_bytes);
     }
     a.q_pitch = g->q_pitch; a.q_head_pitch = g->q_head_pitch; a.out_pitch = g->out_pitch; a.out_head_pitch = g->out_head_pitch;
     a.group = g->group; a.causal = g->causal;

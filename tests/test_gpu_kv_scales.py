@@ -67,3 +67,26 @@ def test_scales_of_pages_nobody_sees(dim, heads, group, count, block, how):
                     kv.raw(other.k_scale)[own[s][b]] = code
         got = _run(q, other, own, lengths, starts, **kw)
         assert torch.equal(got, want), f"scale code {code}: {int((got != want).sum())} of {got.numel()} results differ"
+
+
+def _far_apart(dim, heads, group, block, n, count, codes, seed, dt="bf16", **kw):
+    """One sequence of n tokens whose pages take their values' scale codes from `codes` in turn."""
+    width = -(-n // block)
+    cache = kv.random_cache(st, width, heads, dim, block, seed)
+    cache.v_scale = torch.tensor([[codes[b % len(codes)]] * heads for b in range(width)], dtype=torch.uint8).view(E8M0)
+    q = _queries(count, heads * group, dim, dt, seed + 1)
+    table = [list(range(width))]
+    got = _run(q, cache, table, [n], [0, count], **kw)
+    want, tol = kv.attention(q, cache, table, [n], [0, count], **kw)
+    kv.check(got, want, tol)
+
+
+@pytest.mark.parametrize("dim,heads,group,count", FEW_MANY)
+@pytest.mark.parametrize("n", [90, 5000])
+def test_values_near_the_largest_number(dim, heads, group, count, n):
+    """Values up to 448 * 2^119: sums of their products pass fp32's range, the results, which are their means, do not; and values near
+    the smallest."""
+    print(f"attention largest values {dim} {group} x {count} of {n}", flush=True)
+    for code in (246, 20, 3):
+        _far_apart(dim, heads, group, 64, n, count, (code,), 11)
+        _far_apart(dim, heads, group, 64, n, count, (code, code - 1, code - 3), 12)
