@@ -6,8 +6,9 @@
 // fp32 score.  The numerators, 2^(s f - m + 6), enter the second product in fp16: m is the largest score until another passes it by 2^8, which
 // leaves them below 2^15 and 30 binades above fp16's smallest step.  Value codes are exact in fp16 too; a block's
 // power of two is taken relative to the largest, 2^E, of those that a row of the wavefront has seen, so that a value is exact unless its block's is 2^15
-// below that (then to 2^-33 of the largest magnitude).  l sums the numerators as
-// they enter there.  Maxima, sums and results are fp32.
+// below that, then good to 2^-25 of 2^E.  Where 2^E may be more than 2^8 above the largest that some row of the wavefront sees itself
+// (queries at either end of a window, or of a sequence), rows are taken one by one (attend_row), so that values always count to 2^-17 of the largest power
+// of two that a query sees.  l sums the numerators as they enter there.  Maxima, sums and results are fp32.
 //
 // Operands come straight from memory to the matrix instructions, no value crosses lanes between the two products.  The first one
 // makes S^T (tokens x queries) from K rows, the second O^T = V^T P^T.  A step has 64 tokens; lane group g (of four) gets scores of tokens
@@ -48,6 +49,9 @@ struct Args {
 
 constexpr float kNone = -__builtin_inff();
 constexpr float kOffset = 6.0f, kSlack = 8.0f;
+// Binades below the common power of two in which every value code is exact in fp16; those by which it may be above what a row sees itself (a value is
+// good to 2^-25 of the former, then 2^-17 of the latter); and see settle.
+constexpr int32_t kNear = 15, kAbove = 8, kRoom = 5;
 
 // The tokens [lo, hi) that row r of a sequence's head sees.
 struct Sees {
@@ -79,10 +83,30 @@ __device__ __forceinline__ float max_over_groups(float v) {
     return fmaxf(as_f32(b[0]), as_f32(b[1]));
 }
 
+__device__ __forceinline__ int32_t max_over_groups(int32_t v) {
+    auto a = __builtin_amdgcn_permlane16_swap(uint32_t(v), uint32_t(v), false, false);
+    v = int32_t(a[0]) > int32_t(a[1]) ? int32_t(a[0]) : int32_t(a[1]);
+    auto b = __builtin_amdgcn_permlane32_swap(uint32_t(v), uint32_t(v), false, false);
+    return __builtin_amdgcn_readfirstlane(int32_t(b[0]) > int32_t(b[1]) ? int32_t(b[0]) : int32_t(b[1]));
+}
+
 // v, as something the compiler knows nothing of: what a rarely taken branch computes from it stays in that branch.
 __device__ __forceinline__ uint32_t opaque(uint32_t v) {
     asm volatile("" : "+v"(v));
     return v;
+}
+
+__device__ __forceinline__ uint32_t opaque_uniform(uint32_t v) {
+    asm volatile("" : "+s"(v));
+    return v;
+}
+// The kernel's arguments (its only ones) read again: a rarely taken branch that uses these keeps none of the others in registers through a loop
+// ahead of it.
+__device__ __forceinline__ Args arguments_again() {
+    typedef const __attribute__((address_space(4))) Args* constant;
+    uint64_t p = reinterpret_cast<uint64_t>(__builtin_amdgcn_kernarg_segment_ptr());
+    asm volatile("" : "+s"(p));
+    return *(const Args*)reinterpret_cast<constant>(p);
 }
 
 // Bytes of c that are a NaN code (0x7F, 0xFF) as 0xFF.
@@ -104,6 +128,8 @@ struct Wave {
     uint32_t nan[QT][(DT + 7) / 8];        // a bit for each result that is NaN whatever o says
     int32_t lo[QT], hi[QT];
     int32_t e = -1;                        // E + 127, -1: no values yet
+    int32_t every = -1, low = 256;         // the largest page that every row has seen, a bound below those that some row has (256: none),
+    int32_t span = 0;                      // and how far the one is above the other
     int32_t all_lo, all_hi;                // tokens that every row sees
     int32_t any_lo, any_hi;                // tokens that some row sees
 
@@ -127,6 +153,46 @@ struct Wave {
         const Sees s0 = sees(a, p, row0), s1 = sees(a, p, last - 1);
         all_lo = s1.lo, all_hi = s0.hi, any_lo = s0.lo, any_hi = s1.hi;
     }
+
+    // The common power of two, of lane groups whose 16 tokens some row sees: the pages of others (behind a sequence's end, ahead of a window) may
+    // have any.  And what tells whether it serves all rows.
+    template <class V>
+    __device__ __forceinline__ void settle(int32_t at, uint32_t vs, V v, bool known) {
+        const bool none = vs == 255;
+        const int32_t now = !none ? int32_t(vs) : e < 0 ? 0 : e;
+        const bool some = known && at < any_hi && at + 16 > any_lo, all = some && all_lo < all_hi && at < all_hi && at + 16 > all_lo;
+        const int32_t most = max_over_groups(some && now > e ? now : e);
+        every = max_over_groups(all && now > every ? now : every);
+        bool below = some && !none && now < low;
+        if (__any(below)) {
+            if (__any(below && now == 0)) {         // pages of zeros, which have the smallest power of two, lose nothing
+                uint32_t any = 0;
+#pragma unroll
+                for (int d = 0; d < DT; ++d) {
+                    const u32x4 c = v(d);
+                    any |= c[0] | c[1] | c[2] | c[3];
+                }
+                below = below && (__ballot(any & 0x7F7F7F7Fu) >> (at & 48) & 0xFFFF) != 0;
+            }
+            // (with some room, so that pages of ordinary data do not come here one after the other)
+            const int32_t least = -max_over_groups(below ? -now : -256);
+            if (least < 256) low = least - kRoom;
+        }
+        span = every > low ? every - low : 0;
+        if (most > e) {
+            if (e >= 0) {
+#pragma unroll
+                for (int j = 0; j < QT; ++j)
+#pragma unroll
+                    for (int d = 0; d < DT; ++d)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) o[j][d][i] = __builtin_amdgcn_ldexpf(o[j][d][i], e - most);
+            }
+            e = most;
+        }
+    }
+    // Some row may have seen only pages far below the common power of two, and some page's codes are not exact beside it.
+    __device__ __forceinline__ bool apart() const { return low < e - kNear && every < e - kAbove; }
 
     // One step of tokens from t0.  k(t, i), v(d): its codes, 16 bytes of K tile t and of V^T tile d; ks, vs: the scale codes of lane
     // group g's tokens; known: they lie on a page.  The schedule is cut between tiles, which bounds the registers that decoded
@@ -214,26 +280,7 @@ struct Wave {
             const u32x4 ones = {0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u};
             l[j] = mfma32<true>(ones, p[j][1], mfma32<true>(ones, p[j][0], l[j]));
         }
-        // the largest power of two so far
-        int32_t now = known ? int32_t(vs == 255 ? 0 : vs) : -1;
-        if (__any(now > e)) {
-            // of lane groups whose 16 tokens some row sees: the others' pages (behind a sequence's end, ahead of a window) may have any
-            now = at < any_hi && at + 16 > any_lo && now > e ? now : e;
-            int32_t o1 = __shfl_xor(now, 16);
-            now = now > o1 ? now : o1;
-            o1 = __shfl_xor(now, 32);
-            now = now > o1 ? now : o1;
-            now = __builtin_amdgcn_readfirstlane(now);
-            if (e >= 0) {
-#pragma unroll
-                for (int j = 0; j < QT; ++j)
-#pragma unroll
-                    for (int d = 0; d < DT; ++d)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) o[j][d][i] = __builtin_amdgcn_ldexpf(o[j][d][i], e - now);
-            }
-            e = now;
-        }
+        if (__any(known && vs - uint32_t(low) > uint32_t(span))) settle(at, vs, v, known);
         // (a factor above 1 is one of a page that nobody sees, whose numerators are 0: it must be finite)
         int32_t by = int32_t(vs) - e + 127;
         by = by < 0 ? 0 : by > 127 ? 127 : by;
@@ -313,6 +360,133 @@ __device__ __forceinline__ void store_row4(const Args& a, uint64_t i, const floa
     *reinterpret_cast<u64_any*>(a.out + i * 2) = uint64_t(hi) << 32 | lo;
 }
 
+// What a workgroup has: rows row0 .. end - 1 of a sequence's head, over the steps st.
+struct Tile {
+    uint32_t seq, head, row0, end, rows, split;
+    Span p;
+    Steps st;
+};
+// The rest of t from its sequence, head, row0 and split; false: nothing to do.
+__device__ __forceinline__ bool complete(const Args& a, uint32_t tile_rows, Tile& t) {
+    t.p = span_of(a.s, t.seq);
+    t.rows = uint32_t(t.p.count) * a.group;
+    if (t.row0 >= t.rows) return false;
+    t.end = t.row0 + tile_rows < t.rows ? t.row0 + tile_rows : t.rows;
+    t.st = steps_of(a, t.p, t.row0, t.end);
+    if (a.splits > 1) {
+        t.st.first += int32_t(t.split * a.chunk);
+        if (t.st.first >= t.st.last) return false;
+        t.st.last = t.st.first + int32_t(a.chunk) < t.st.last ? t.st.first + int32_t(a.chunk) : t.st.last;
+    }
+    return true;
+}
+__device__ __forceinline__ bool tile_of(const Args& a, uint32_t tile_rows, uint32_t block, Tile& t) {
+    t.split = block % a.splits;
+    block /= a.splits;
+    t.row0 = block % a.tiles * tile_rows;
+    block /= a.tiles;
+    t.head = block % a.s.heads, t.seq = block / a.s.heads;
+    return complete(a, tile_rows, t);
+}
+
+// One row of a tile by one wavefront, its own numerators and powers of two in fp32: for rows that a power of two in common does not
+// serve (Wave::apart()).  A lane has one token's score, then D / 64 results.  Simple rather than fast, since pages of one sequence and head do not differ
+// like that in earnest: 4 prompts' chunks of up to 2048 tokens, 32 heads of 128, through windows of 300 take 1.96 ms where each page's values are 2^12
+// below those of the one before, 0.10 where they are not.
+template <bool F16, int D>
+__device__ __forceinline__ void attend_row(const Args& a, const Tile& tile, uint32_t row) {
+    const Span& p = tile.p;
+    const uint32_t seq = tile.seq, head = tile.head, split = tile.split;
+    const Steps st = tile.st;
+    constexpr int COLS = D / 64;
+    const int lane = threadIdx.x & 63;
+    const uint32_t bl = a.s.block_log2, block = 1u << bl;
+    const uint64_t page_bytes = uint64_t(block) * D, tok = uint64_t(p.first) + row / a.group, h = head * a.group + row % a.group;
+    const uint8_t* q = a.q + (tok * a.q_pitch + h * a.q_head_pitch) * 2;
+    const Sees see = sees(a, p, row);
+    float m = kNone, l = 0.0f, o[COLS];
+    int32_t e = -1;
+#pragma unroll
+    for (int c = 0; c < COLS; ++c) o[c] = 0.0f;
+    for (int32_t i = st.first; i < st.last; ++i) {
+        const int32_t t0 = i * kStep, t = t0 + lane;
+        const int32_t page = page_of(a.s, seq, int64_t(t) >> bl);
+        const uint64_t at = uint64_t(page < 0 ? 0 : page) * a.s.heads + head;
+        const bool seen = page >= 0 && t >= see.lo && t < see.hi;
+        float s = kNone;
+        if (seen) {
+            const uint8_t* k = a.k + at * page_bytes + uint64_t(t & (block - 1)) * D;
+            s = 0.0f;
+#pragma unroll 8
+            for (int c = 0; c < D; c += 4) {
+                const uint32_t code = *reinterpret_cast<const uint32_t*>(k + c);
+                const uint64_t x = *reinterpret_cast<const u64_any*>(q + 2 * c);
+                const f32x2 k0 = __builtin_amdgcn_cvt_pk_f32_fp8(code, false), k1 = __builtin_amdgcn_cvt_pk_f32_fp8(code, true);
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    const uint32_t u = uint32_t(x >> 16 * n) & 0xFFFF;
+                    const float f = F16 ? float(__builtin_bit_cast(f16x2, u).x) : as_f32(u << 16);
+                    s = __builtin_fmaf(n < 2 ? k0[n] : k1[n - 2], f, s);
+                }
+            }
+            s *= power_of(a.ks[at]) * a.f;
+        }
+        float top = s;
+#pragma unroll
+        for (int x = 1; x < 64; x *= 2) top = fmaxf(top, __shfl_xor(top, x));
+        const float now = fmaxf(m, top), keep = now == kNone ? 1.0f : __builtin_amdgcn_exp2f(m - now);
+        m = now, l *= keep;
+        const float n = seen ? __builtin_amdgcn_exp2f(s + (kOffset - (m == kNone ? 0.0f : m))) : 0.0f;
+        float sum = n;
+#pragma unroll
+        for (int x = 1; x < 64; x *= 2) sum += __shfl_xor(sum, x);
+        l += sum;
+#pragma unroll
+        for (int c = 0; c < COLS; ++c) o[c] *= keep;
+        const uint64_t mask = __ballot(seen);
+#pragma unroll 1
+        for (int g = 0; g < 64; g += 16) {
+            if (!(mask >> g & 0xFFFF)) continue;
+            const uint64_t of = uint64_t(__builtin_amdgcn_readlane(page, g)) * a.s.heads + head;
+            const uint8_t* v = a.v + of * page_bytes + uint64_t(lane) * COLS * block + ((t0 + g) & (block - 1));
+            const int32_t code = a.vs[of], unit = code == 255 ? 0 : code, to = unit > e ? unit : e;
+            const float by = code == 255 ? __builtin_nanf("") : 1.0f;
+            float x[COLS];
+#pragma unroll
+            for (int c = 0; c < COLS; ++c) x[c] = 0.0f;
+#pragma unroll 1
+            for (int b = g; b < g + 16; b += 4) {
+                // (what tokens that the row does not see hold may be NaN)
+                const uint32_t in = (uint32_t(mask >> b & 15) * 0x204081u & 0x01010101u) * 0xFFu;
+#pragma unroll
+                for (int c = 0; c < COLS; ++c) {
+                    const uint32_t w = *reinterpret_cast<const uint32_t*>(v + uint64_t(c) * block + (b - g)) & in;
+                    const f32x2 lo = __builtin_amdgcn_cvt_pk_f32_fp8(w, false), hi = __builtin_amdgcn_cvt_pk_f32_fp8(w, true);
+                    const float value[4] = {lo.x, lo.y, hi.x, hi.y};
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) x[c] = __builtin_fmaf(as_f32(__builtin_amdgcn_readlane(as_u32(n), b + t)), value[t], x[c]);
+                }
+            }
+#pragma unroll
+            for (int c = 0; c < COLS; ++c) o[c] = __builtin_amdgcn_ldexpf(o[c], e - to) + __builtin_amdgcn_ldexpf(x[c] * by, unit - to);
+            e = to;
+        }
+    }
+    if (l == 0.0f) e = -1;
+    const uint64_t out = tok * a.s.heads * a.group + h;
+    if (a.splits > 1 && lane == 0) a.stat[out * a.splits + split] = Part{m, l, e};
+#pragma unroll
+    for (int c = 0; c < COLS; ++c) {
+        const uint32_t d = lane * COLS + c;
+        if (a.splits > 1) {
+            a.part[(out * a.splits + split) * D + d] = o[c];
+        } else {
+            const float y = l == 0.0f ? 0.0f : __builtin_amdgcn_ldexpf(o[c] / l, e - 127);
+            *reinterpret_cast<uint16_t*>(a.out + (tok * a.out_pitch + h * a.out_head_pitch + d) * 2) = uint16_t(F16 ? cvt_f16x2(y, 0.0f) : cvt_bf16x2(y, 0.0f));
+        }
+    }
+}
+
 // Few rows: the wavefronts of a workgroup take the steps of one row tile in turn and join in LDS, in their order.  Bound by the codes' bytes: one
 // query of 2 sequences of 131071 tokens, 8 heads of 128 and five queries each (537 MB), 112 us, 4.8 TB/s; of 48 sequences of 100 to 8192 tokens
 // (408 MB) 100 to 107 us, 4 TB/s.  3 sequences' 4 drafts, 8 heads of 64, up to 1000 tokens: 9 us, of which the launch and four dependent
@@ -323,25 +497,14 @@ __global__ __launch_bounds__(kThreads, D * QT <= 128 ? 2 : 1) void attend(Args a
     constexpr int ROWS = 16 * QT, PITCH = D + 4;
     __shared__ __align__(16) float sum[ROWS][PITCH];
     __shared__ float top[kWaves][ROWS], den[kWaves][ROWS];
-    __shared__ int32_t unit[kWaves][ROWS];
+    __shared__ int32_t unit[kWaves][ROWS], apart[kWaves];
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    uint32_t b = blockIdx.x;
-    const uint32_t split = b % a.splits;
-    b /= a.splits;
-    const uint32_t tile = b % a.tiles;
-    b /= a.tiles;
-    const uint32_t head = b % a.s.heads, seq = b / a.s.heads;
-    const Span p = span_of(a.s, seq);
-    const uint32_t rows = uint32_t(p.count) * a.group, row0 = tile * ROWS;
-    if (row0 >= rows) return;
-    const uint32_t end = row0 + ROWS < rows ? row0 + ROWS : rows;
-    Steps st = steps_of(a, p, row0, end);
-    if (a.splits > 1) {
-        st.first += int32_t(split * a.chunk);
-        if (st.first >= st.last) return;
-        st.last = st.first + int32_t(a.chunk) < st.last ? st.first + int32_t(a.chunk) : st.last;
-    }
+    Tile t;
+    if (!tile_of(a, ROWS, blockIdx.x, t)) return;
+    const Span p = t.p;
+    const Steps st = t.st;
+    const uint32_t seq = t.seq, head = t.head, row0 = t.row0, end = t.end, rows = t.rows, split = t.split;
     W w;
     w.start(a, p, head, row0, rows);
 
@@ -389,7 +552,14 @@ __global__ __launch_bounds__(kThreads, D * QT <= 128 ? 2 : 1) void attend(Args a
     for (int j = 0; j < QT; ++j) {
         if (g == 0) top[wave][16 * j + r] = w.m[j], den[wave][16 * j + r] = w.l[j][0], unit[wave][16 * j + r] = w.units(j);
     }
+    if (lane == 0) apart[wave] = w.apart();
     __syncthreads();
+    if (apart[0] | apart[1] | apart[2] | apart[3]) {
+        const Args b = arguments_again();
+        if (!tile_of(b, ROWS, opaque_uniform(blockIdx.x), t)) return;
+        for (uint32_t row = t.row0 + wave; row < t.end; row += kWaves) attend_row<F16, D>(b, t, row);
+        return;
+    }
     float m[QT];
 #pragma unroll
     for (int j = 0; j < QT; ++j) {
@@ -419,18 +589,18 @@ __global__ __launch_bounds__(kThreads, D * QT <= 128 ? 2 : 1) void attend(Args a
     }
     for (uint32_t i4 = threadIdx.x; i4 < (end - row0) * (D / 4); i4 += kThreads) {
         const uint32_t rr = i4 / (D / 4), d = i4 % (D / 4) * 4, row = row0 + rr;
-        float t = kNone, l = 0.0f;
+        float m1 = kNone, l = 0.0f;
         int32_t e = -1;
 #pragma unroll
-        for (int o = 0; o < kWaves; ++o) t = fmaxf(t, top[o][rr]), e = unit[o][rr] > e ? unit[o][rr] : e;
+        for (int o = 0; o < kWaves; ++o) m1 = fmaxf(m1, top[o][rr]), e = unit[o][rr] > e ? unit[o][rr] : e;
 #pragma unroll
-        for (int o = 0; o < kWaves; ++o) l += top[o][rr] == kNone ? den[o][rr] : den[o][rr] * __builtin_amdgcn_exp2f(top[o][rr] - t);
+        for (int o = 0; o < kWaves; ++o) l += top[o][rr] == kNone ? den[o][rr] : den[o][rr] * __builtin_amdgcn_exp2f(top[o][rr] - m1);
         f32x4 x = *reinterpret_cast<const f32x4*>(&sum[rr][d]);
         const uint64_t tok = uint64_t(p.first) + row / a.group, h = head * a.group + row % a.group;
         if (a.splits > 1) {
             const uint64_t at = (tok * a.s.heads * a.group + h) * a.splits + split;
             *reinterpret_cast<f32x4*>(a.part + at * D + d) = x;
-            if (d == 0) a.stat[at] = Part{t, l, e};
+            if (d == 0) a.stat[at] = Part{m1, l, e};
         } else {
             float y[4];
 #pragma unroll
@@ -464,11 +634,12 @@ constexpr int wait_vmem(int n) { return (n & 15) | (n >> 4) << 14 | 7 << 4; }
 // work would come in patterns that leave part of an XCD idle (4 prompts of 682 to 2048 tokens: 511 us without gaps between the longest's tiles, 887 with).
 // All lanes of a wavefront take part, 64 sequences at a time.
 template <int ROWS>
-__device__ __forceinline__ bool place(const Args& a, uint32_t& seq, uint32_t& head, uint32_t& tile) {
-    const uint32_t H = a.s.heads, lane = threadIdx.x & 63, xcd = blockIdx.x % 8;
+__device__ __forceinline__ bool place(const Args& a, uint32_t block, Tile& to) {
+    const uint32_t H = a.s.heads, lane = threadIdx.x & 63, xcd = block % 8;
     const uint32_t ways = H % 8 == 0 ? 1 : 8 % H == 0 ? 8 / H : 8, groups = 8 / ways, per = H % 8 == 0 ? H / 8 : 8 % H == 0 ? 1 : H;
     const uint32_t way = xcd / groups;
-    uint32_t at = blockIdx.x / 8 / a.splits;
+    uint32_t at = block / 8 / a.splits;
+    to.split = block / 8 % a.splits;
     for (uint32_t base = 0; base < a.s.seqs; base += 64) {
         const uint32_t s = base + lane;
         uint32_t tiles = 0, len = 0;
@@ -489,10 +660,10 @@ __device__ __forceinline__ bool place(const Args& a, uint32_t& seq, uint32_t& he
             const uint64_t hit = __ballot(at >= before * per && at < (before + tiles) * per);
             const uint32_t o = uint32_t(__builtin_ctzll(hit)), t = __builtin_amdgcn_readlane(tiles, o);
             at -= __builtin_amdgcn_readlane(before, o) * per;
-            seq = base + o;
-            head = xcd % groups + (per > 1 ? at / t * groups : 0);
-            tile = way + (t - 1 - at % t) * ways;
-            return true;
+            to.seq = base + o;
+            to.head = xcd % groups + (per > 1 ? at / t * groups : 0);
+            to.row0 = (way + (t - 1 - at % t) * ways) * ROWS;
+            return complete(a, ROWS, to);
         }
         at -= total * per;
     }
@@ -510,19 +681,11 @@ __global__ __launch_bounds__(kThreads, D * QT <= 256 ? 2 : 1) void attend_many(A
     __shared__ __align__(128) uint8_t lds[LDS];
     const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    uint32_t seq, head, tile;
-    const uint32_t split = blockIdx.x / 8 % a.splits;
-    if (!place<ROWS>(a, seq, head, tile)) return;
-    const Span p = span_of(a.s, seq);
-    const uint32_t rows = uint32_t(p.count) * a.group, row0 = tile * ROWS;
-    if (row0 >= rows) return;
-    const uint32_t end = row0 + ROWS < rows ? row0 + ROWS : rows;
-    Steps st = steps_of(a, p, row0, end);
-    if (a.splits > 1) {
-        st.first += int32_t(split * a.chunk);
-        if (st.first >= st.last) return;
-        st.last = st.first + int32_t(a.chunk) < st.last ? st.first + int32_t(a.chunk) : st.last;
-    }
+    Tile t;
+    if (!place<ROWS>(a, blockIdx.x, t)) return;
+    const Span p = t.p;
+    const Steps st = t.st;
+    const uint32_t seq = t.seq, head = t.head, row0 = t.row0, end = t.end, rows = t.rows, split = t.split;
     const uint32_t mine = row0 + wave * 16 * QT;
     const bool work = mine < end;
     W w;
@@ -602,6 +765,13 @@ __global__ __launch_bounds__(kThreads, D * QT <= 256 ? 2 : 1) void attend_many(A
         buf = buf + 1 < kStages ? buf + 1 : 0;
     }
     __syncthreads();
+    if (work && w.apart()) {
+        const Args b = arguments_again();
+        if (!place<ROWS>(b, opaque_uniform(blockIdx.x), t)) return;
+        const uint32_t first = t.row0 + wave * 16 * QT;
+        for (uint32_t row = first; row < first + 16 * QT && row < t.end; ++row) attend_row<F16, D>(b, t, row);
+        return;
+    }
     float* mem = reinterpret_cast<float*>(lds) + wave * 16 * PITCH;
 #pragma unroll
     for (int j = 0; j < QT; ++j) {

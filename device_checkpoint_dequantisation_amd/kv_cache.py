@@ -144,8 +144,8 @@ def kv_attention(q, cache: QuantizedKvCache, table, lengths, starts=None, max_ne
     ``lengths[s]`` tokens, such as an encoder's, and a sequence may have more queries than tokens.  A query that sees no token, or only scores of minus infinity, gives 0.
     Tokens that a query does not see, and what pages hold behind a sequence's end, have no part in its result.
     Rows that belong to no sequence (before ``starts[0]``, from ``starts[-1]`` on, behind ``max_new``) stay as they are in ``out`` and are
-    0 without one.  Scores and sums are fp32; the softmax's numerators enter the second product with fp16's 11 bits, fp16 queries with values
-    as they are."""
+    0 without one.  Scores and sums are fp32; the softmax's numerators enter the second product with fp16's 11 bits, values
+    exactly unless their page's scale is 2**-7 times the largest that the query sees or less, then to 2**-17 of that scale."""
     who = "kv_attention"
     pages, heads, block, dim = _check_cache(cache, who)
     if dim not in HEAD_DIMS:

@@ -685,7 +685,8 @@ typedef struct st_kv_attention_args {
     uint32_t q_type;         /* ST_OUT_BF16 or ST_OUT_F16 */
 } st_kv_attention_args;
 /* out = softmax(scale * q k^T) v over the tokens a query sees; 0 where it sees none.  Scores, maxima, sums and results are kept in
- * fp32; the softmax's numerators are rounded to fp16 (11 bits) as they meet the values.  Tokens a query does not see have no part in its result,
+ * fp32; the softmax's numerators are rounded to fp16 (11 bits) as they meet the values, which are exact down to 2^-7 times the largest v_scale that the query
+ * sees in that head, and good to 2^-17 of it below.  Tokens a query does not see have no part in its result,
  * NaN codes among them.  Rows of `out` that belong to no sequence are left as they are.
  * head_dim: 64, 128 or 256; block: 16, 32, 64 or 128. */
 st_status st_kv_attention_workspace_bytes(const st_kv_attention_args* args, uint64_t* bytes);

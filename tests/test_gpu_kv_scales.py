@@ -78,7 +78,75 @@ def _far_apart(dim, heads, group, block, n, count, codes, seed, dt="bf16", **kw)
     table = [list(range(width))]
     got = _run(q, cache, table, [n], [0, count], **kw)
     want, tol = kv.attention(q, cache, table, [n], [0, count], **kw)
+    # Values meet the numerators as fp16 numbers relative to a power of two, at most 2^8 times the largest among the pages that a query sees: exact
+    # down to 2^-15 of it, below to half of fp16's smallest step, 2^-25 of it, which is 2^-17 of the query's own, and the weights add up to 1.
+    for t in range(count):
+        pos = n - count + t
+        see = [codes[b % len(codes)] for b in range(max(0, pos - (kw.get("window") or n) + 1) // block, pos // block + 1)]
+        if max(see) + 8 - min(see) > 15:
+            tol[t] += 2.0 ** (max(see) - 127 - 17)
     kv.check(got, want, tol)
+
+
+@pytest.mark.parametrize("dim,heads,group,count", FEW_MANY)
+@pytest.mark.parametrize("block", [16, 64])
+@pytest.mark.parametrize("codes", [(127, 107), (97, 127), (127, 100, 112, 90), (140, 20), (1, 125), (0, 127), (60, 128, 59)])
+def test_scales_that_only_some_queries_see(dim, heads, group, count, block, codes):
+    """Queries whose windows begin and end on different pages: what one sees and another does not leaves the other's result alone."""
+    print(f"attention windows over far scales {dim} {block} {group} x {count} {codes}", flush=True)
+    for window in (1, block, 2 * block + 5):
+        _far_apart(dim, heads, group, block, 5 * block + count // 2 + 1, count, codes, 7, window=window)
+    _far_apart(dim, heads, group, block, 5 * block + count // 2 + 1, count, codes, 7)
+
+
+@pytest.mark.parametrize("dim,heads,group,count", FEW_MANY)
+def test_scales_rise_and_fall(dim, heads, group, count):
+    """Pages whose scales rise, or fall, by 6 binades each: hundreds of tokens apart they differ by more than any 16-bit number's range."""
+    up = list(range(20, 128, 6))
+    print(f"attention rising scales {dim} {group} x {count}", flush=True)
+    for codes in (up, up[::-1]):
+        for window in (1, 30, 100):
+            _far_apart(dim, heads, group, 16, 16 * len(codes), count, codes, 9, window=window)
+        _far_apart(dim, heads, group, 16, 16 * len(codes), count, codes, 9, dt="f16", window=50)
+
+
+@pytest.mark.parametrize("dim,heads,group,count", FEW_MANY)
+@pytest.mark.parametrize("window", [None, 4500])
+def test_far_scales_in_parts(dim, heads, group, count, window):
+    """Scales that rise to the last page, which the first queries do not see, or fall from the first of their windows, over tokens that are
+    cut into parts."""
+    print(f"attention far scales in parts {dim} {group} x {count} {window}", flush=True)
+    for codes in (list(range(45, 124)), list(range(123, 44, -1))):
+        _far_apart(dim, heads, group, 64, 79 * 64 - 64 + count // 2 + 1, count, codes, 15, window=window)
+
+
+@pytest.mark.parametrize("dim,heads,group,count", FEW_MANY)
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+def test_far_scales_nan_and_missing_pages(dim, heads, group, count, dt):
+    """NaN codes where no query looks, one that only some see, a page of NaN scale that only some see, and a page that is not there."""
+    block, pages = 16, 12
+    n, window = pages * block - 5, 50
+    first = max(0, n - count - window + 1)
+    cache = kv.random_cache(st, pages, heads, dim, block, 17)
+    cache.v_scale = torch.tensor([[(127, 100, 80, 121)[b % 4]] * heads for b in range(pages)], dtype=torch.uint8).view(E8M0)
+    table = [list(range(pages))]
+    table[0][pages - 3] = -1
+    q = _queries(count, heads * group, dim, dt, 18)
+    k, v, vs = kv.raw(cache.k), kv.raw(cache.v), kv.raw(cache.v_scale)
+    for t in list(range(first)) + list(range(n, pages * block)):
+        k[t // block, :, t % block] = 0x7F
+        v[t // block, :, :, t % block] = 0xFF
+    t = n - count // 2 - 1                      # the last queries see it, the first ones do not
+    v[t // block, heads - 1, 5, t % block] = 0x7F
+    print(f"attention far scales with NaN {dim} {group} x {count} {dt}", flush=True)
+    for bad in (None, first // block):
+        if bad is not None:
+            vs[bad] = 255
+        got = _run(q, cache, table, [n], [0, count], window=window)
+        want, tol = kv.attention(q, cache, table, [n], [0, count], window=window)
+        assert (bad is not None or not want.isnan().all()) and (want.isnan() == got.cpu().isnan()).all()
+        tol += 2.0 ** (0 - 17)                  # as above: the largest seen is 2^0
+        kv.check(got, want, tol)
 
 
 @pytest.mark.parametrize("dim,heads,group,count", FEW_MANY)
