@@ -43,7 +43,7 @@ struct Args {
     Part* stat;                   // [tokens * query heads][splits]
     uint64_t q_pitch, q_head_pitch, out_pitch, out_head_pitch;
     uint32_t group, causal, window;
-    uint32_t tiles, splits, chunk;   // row tiles of a head, parts of the tokens, steps of a part
+    uint32_t tiles, splits;       // row tiles of a head, parts of a tile's tokens at most
     float f;                      // scale * log2(e)
 };
 
@@ -73,6 +73,15 @@ struct Steps {
 __device__ __forceinline__ Steps steps_of(const Args& a, const Span& p, uint32_t row0, uint32_t end) {
     const int32_t lo = sees(a, p, row0).lo, hi = sees(a, p, end - 1).hi;
     return hi > lo ? Steps{lo / kStep, (hi + kStep - 1) / kStep} : Steps{0, 0};
+}
+
+// Steps of each part of a tile: equal ones, four for each wavefront at least.  They follow from the tokens that a tile has, not from those that the
+// table has room for, which in a captured graph may be many more.
+constexpr uint32_t kLeastPart = 4 * kWaves;
+__device__ __forceinline__ uint32_t part_of(const Args& a, const Steps& st) {
+    uint32_t part = (uint32_t(st.last - st.first) + a.splits - 1) / a.splits;
+    part = (part + kWaves - 1) / kWaves * kWaves;
+    return part < kLeastPart ? kLeastPart : part;
 }
 
 // Over the four lane groups, by exchanging rows of 16 and halves of 32 lanes on the vector unit.
@@ -374,18 +383,23 @@ __device__ __forceinline__ bool complete(const Args& a, uint32_t tile_rows, Tile
     t.end = t.row0 + tile_rows < t.rows ? t.row0 + tile_rows : t.rows;
     t.st = steps_of(a, t.p, t.row0, t.end);
     if (a.splits > 1) {
-        t.st.first += int32_t(t.split * a.chunk);
+        const uint32_t part = part_of(a, t.st);
+        t.st.first += int32_t(t.split * part);
         if (t.st.first >= t.st.last) return false;
-        t.st.last = t.st.first + int32_t(a.chunk) < t.st.last ? t.st.first + int32_t(a.chunk) : t.st.last;
+        t.st.last = t.st.first + int32_t(part) < t.st.last ? t.st.first + int32_t(part) : t.st.last;
     }
     return true;
 }
 __device__ __forceinline__ bool tile_of(const Args& a, uint32_t tile_rows, uint32_t block, Tile& t) {
-    t.split = block % a.splits;
-    block /= a.splits;
+    // All first parts, then all second ones, and so on: those that sequences do not have leave no gaps between the others, which would come in patterns
+    // that idle part of the XCDs (16 sequences' 4 drafts, 64 queries on 8 heads of 128: 74 us, and with a table 16 times as wide as the
+    // longest; 92 and 168 with a tile's parts one after the other).  Tiles of a head, which read the same codes, close together, after
+    // the heads (32 sequences' 16 drafts, 32 queries on 8 heads of 64: 64 us; 67 with tiles ahead of heads, 74 behind sequences).
+    t.head = block % a.s.heads;
+    block /= a.s.heads;
     t.row0 = block % a.tiles * tile_rows;
     block /= a.tiles;
-    t.head = block % a.s.heads, t.seq = block / a.s.heads;
+    t.seq = block % a.s.seqs, t.split = block / a.s.seqs;
     return complete(a, tile_rows, t);
 }
 
@@ -828,7 +842,7 @@ __global__ __launch_bounds__(kThreads) void join(Args a, uint32_t tile_rows, uin
     if (have) {
         const uint32_t rows = uint32_t(p.count) * a.group, row = t * a.group + h % a.group, row0 = row / tile_rows * tile_rows;
         const Steps st = steps_of(a, p, row0, row0 + tile_rows < rows ? row0 + tile_rows : rows);
-        const uint32_t parts = (uint32_t(st.last - st.first) + a.chunk - 1) / a.chunk;
+        const uint32_t part = part_of(a, st), parts = (uint32_t(st.last - st.first) + part - 1) / part;
         const uint32_t n = parts > way ? (parts - way + ways - 1) / ways : 0;      // (a loop the compiler can unroll: it would wait for each load)
 #pragma unroll 4
         for (uint32_t i = 0; i < n; ++i) {
@@ -873,7 +887,7 @@ bool off(const void* p, uint64_t n) { return reinterpret_cast<uintptr_t>(p) % n 
 
 struct Plan {
     uint64_t rows;               // of a sequence's head, at most
-    uint32_t qt, tile_rows, tiles, splits, chunk;
+    uint32_t qt, tile_rows, tiles, splits;
     uint64_t count;              // new tokens of a sequence, at most
     bool many;
     uint32_t positions;          // workgroups of an XCD, at most
@@ -931,14 +945,12 @@ st_status plan_of(const st_kv_attention_args& g, Plan* p) {
     uint64_t tokens = g.table_blocks * g.block;
     if (g.window && g.window + p->tile_rows + 2 * kStep < tokens) tokens = g.window + p->tile_rows + 2 * kStep;
     const uint64_t steps = (tokens + kStep - 1) / kStep;
-    // Parts of equal length, about eight workgroups a CU (two of the larger ones), which evens out sequences of different length, each with four
-    // steps for each of its wavefronts at least
+    // Parts of a tile: as many as make about eight workgroups a CU (two of the larger ones), which evens out sequences of different length, and no more than
+    // its tokens can fill (part_of)
     const uint64_t want = p->many ? 512 : 2048;
-    uint64_t chunk = (groups * steps + want - 1) / want;
-    chunk = (chunk + kWaves - 1) / kWaves * kWaves;
-    if (chunk < 16) chunk = 16;
-    uint64_t splits = (steps + chunk - 1) / chunk;
-    if (groups >= want) splits = 1;
+    uint64_t splits = (want + groups - 1) / groups;
+    const uint64_t most = (steps + kLeastPart - 1) / kLeastPart;
+    splits = splits < most ? splits : most;
     if (p->many) {
         const uint64_t H = g.heads, ways = H % 8 == 0 ? 1 : 8 % H == 0 ? 8 / H : 8, per = H % 8 == 0 ? H / 8 : 8 % H == 0 ? 1 : H;
         const uint64_t positions = g.seqs * per * ((tiles + ways - 1) / ways);
@@ -948,7 +960,7 @@ st_status plan_of(const st_kv_attention_args& g, Plan* p) {
     }
     if ((groups + 8 * tiles) * splits >= uint64_t(1) << 24)
         return st_fail(ST_E_SHAPE, "%s: %llu workgroups are too many for one launch", kWho, (unsigned long long)(groups * splits));
-    p->tiles = uint32_t(tiles), p->splits = uint32_t(splits), p->chunk = uint32_t(chunk);
+    p->tiles = uint32_t(tiles), p->splits = uint32_t(splits);
     if (splits > 1) {
         const uint64_t n = g.tokens * g.heads * g.group * splits;
         p->part_bytes = n * g.head_dim * 4, p->stat_bytes = n * sizeof(Part);
@@ -1011,7 +1023,7 @@ extern "C" st_status st_kv_attention(const st_kv_attention_args* g, void* stream
     a.q_pitch = g->q_pitch; a.q_head_pitch = g->q_head_pitch; a.out_pitch = g->out_pitch; a.out_head_pitch = g->out_head_pitch;
     a.group = g->group; a.causal = g->causal;
     a.window = uint32_t(g->window < (uint64_t(1) << 31) - 1 ? g->window : 0);      // as long as any sequence: all
-    a.tiles = p.tiles; a.splits = p.splits; a.chunk = p.chunk;
+    a.tiles = p.tiles; a.splits = p.splits;
     a.f = float(g->scale * 1.4426950408889634);
     hipStream_t s = static_cast<hipStream_t>(stream);
     const bool h = g->q_type == ST_OUT_F16;
