@@ -199,9 +199,11 @@ struct Codes {
     }
 };
 
-// h as two terms, each to be rounded to bf16; infinities and NaN stay whole in the first.
+// h as two terms, each to be rounded to bf16; infinities and NaN stay whole in the first.  It is cut, not rounded, where rounding would make an infinity of a
+// number between bf16's largest and fp32's.
 __device__ __forceinline__ void terms_of(float h, float& hi, float& lo) {
-    hi = as_f32(cvt_bf16x2(h, 0.0f) << 16);
+    const uint32_t rounded = cvt_bf16x2(h, 0.0f) << 16, cut = as_u32(h) & 0xFFFF0000u;
+    hi = as_f32((rounded & 0x7FFFFFFFu) == 0x7F800000u ? cut : rounded);
     const float rest = h - hi;
     lo = rest == rest ? rest : 0.0f;
 }
