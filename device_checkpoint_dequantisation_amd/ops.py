@@ -166,14 +166,22 @@ def _overlaps(out, t) -> bool:
     (a, b), (c, d) = _span(out), _span(t)
     if not (a < d and c < b):
         return False
-    if out.dim() == t.dim() == 2 and out.shape[0] > 1 and t.shape[0] > 1:
-        # columns of one buffer: the same pitch p, and rows that start `by` bytes apart modulo p
+    if out.dim() in (2, 3) and t.dim() in (2, 3) and out.shape[0] > 1 and t.shape[0] > 1:
+        # columns of one buffer: the same pitch p, and rows (of a head's elements, or of all heads') that start `by` bytes apart modulo p
         p = out.stride(0) * out.element_size()
-        wide, other = out.shape[1] * out.element_size(), t.shape[1] * t.element_size()
-        if p == t.stride(0) * t.element_size() and out.stride(1) == t.stride(1) == 1:
+        wide, other = _row_bytes(out), _row_bytes(t)
+        if p == t.stride(0) * t.element_size() and 0 < wide <= p and 0 < other <= p:
             by = (c - a) % p
             return by < wide or by + other > p
     return True
+
+
+def _row_bytes(t) -> int:
+    """Bytes from the first to behind the last of t[i], a row or one row for each head; 0 for rows whose elements are not adjacent."""
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        return 0
+    heads = 0 if t.dim() == 2 else (t.shape[1] - 1) * t.stride(1)
+    return (heads + t.shape[-1]) * t.element_size()
 
 
 def linear(x, weight, bias=None, residual=None, activation: str | None = None, out_dtype: str | None = None, out=None,
