@@ -596,7 +596,8 @@ template <int WK, bool F16, Rows R, bool UP, int TK, Ends TAIL>
 __global__ __launch_bounds__(kTileThreads, R == TWO && TK == 128 ? 2 : 3) void tile(Args a) {
     constexpr bool FP4 = is_fp4(WK), MX = is_mx(WK), GROUPED = WK == ST_KIND_FP8_BLOCK128;
     constexpr int PLANES = R == PLAIN ? 1 : 2, MT = kTileRows / 16;
-    constexpr int WC = TK == 128 && !FP4 ? 2 : 1, WB = FP4 ? TK / 8 : 16;     // chunks of a weight row per lane and step, bytes of one
+    static_assert(TK == 128 || (TK == 64 && !FP4), "16 bytes of a weight row, or twice as many, per lane and step");
+    constexpr int WC = TK == 128 && !FP4 ? 2 : 1;                             // chunks of a weight row per lane and step
     constexpr int OPS = TK / 32;                                              // instructions of a step for 16 x 16 results
     constexpr int XC = TK / 8, PER = kTileRows * XC / kTileThreads;           // 16-byte chunks of a row of x per step; per thread and plane
     __shared__ __align__(16) uint8_t lds[2][PLANES][kTileRows * TK * 2];
@@ -645,15 +646,8 @@ __global__ __launch_bounds__(kTileThreads, R == TWO && TK == 128 ? 2 : 3) void t
                 for (int j = 0; j < WC; ++j) {
                     const uint32_t k = k0 + (FP4 ? TK / 4 * q : 64 * j + 16 * q), to = FP4 ? k / 2 : k;
                     const uint8_t* p = mat[i].w + uint64_t(n[i]) * w_row + to;
-                    if constexpr (WB == 8) {           // (rows of packed fp4 end on 8 bytes)
-                        const uint64_t v = k < K ? *reinterpret_cast<const u64_any*>(p) : 0;
-                        rw[i][j] = u32x4{uint32_t(v), uint32_t(v >> 32), 0, 0};
-                    } else {
-                        rw[i][j] = whole ? load_piece<WITHIN>(p, 16, w_row) : load_piece<TAIL>(p, bytes_left(int64_t(w_row) - to), w_row);
-                    }
-                    if constexpr (WK == ST_KIND_NVFP4 && TK == 64) {
-                        rs[i][j] = k < K ? mat[i].s[uint64_t(n[i]) * ws_row + k / 16] : 0;
-                    } else if constexpr (WK == ST_KIND_NVFP4) {
+                    rw[i][j] = whole ? load_piece<WITHIN>(p, 16, w_row) : load_piece<TAIL>(p, bytes_left(int64_t(w_row) - to), w_row);
+                    if constexpr (WK == ST_KIND_NVFP4) {
                         const uint8_t* ps = mat[i].s + uint64_t(n[i]) * ws_row + k / 16;
                         rs[i][j] = whole ? *reinterpret_cast<const u16_any*>(ps) : load_codes(ps, int64_t(ws_row) - k / 16, 2);
                     } else if constexpr (MX) {
