@@ -755,5 +755,26 @@ void by_end(uint32_t K, F go) {
     else return go(Ending<ODD>{});
 }
 
+// The gate and up products of rows of type X.
+template <int X, int WK>
+void launch_up(const Args& a, Cut cut, hipStream_t s) {
+    using D = Dense<X, WK>;
+    const uint32_t chunks = (a.k + One<WK>::E - 1) / One<WK>::E, turns = (a.k + Turn<WK>::SS - 1) / Turn<WK>::SS;
+    const dim3 few((a.i + 15) / 16, a.slots), block(64 * even(turns, kUpWaves));
+    by_end<WK>(a.k, [&](auto end) {
+        constexpr Ends END = decltype(end)::value;
+        switch (cut) {
+            case ONE:
+                hipLaunchKernelGGL((up_one<X, WK>), dim3((a.i + kUpColumns - 1) / kUpColumns, a.slots), dim3(64 * even((chunks + 63) / 64, kOneMaxWaves)), 0, s, a);
+                break;
+            case FEW:
+            case SOME: hipLaunchKernelGGL((up_few<X, WK, END>), few, block, 0, s, a); break;
+            case MANY:
+                hipLaunchKernelGGL((tile<WK, D::F16, D::SPLIT ? SPLIT : PLAIN, true, kUpK, END>), dim3((a.i + 63) / 64, a.slots), dim3(kTileThreads), 0, s, a);
+                break;
+        }
+    });
+}
+
 }  // namespace
 }  // namespace st_moe_impl
