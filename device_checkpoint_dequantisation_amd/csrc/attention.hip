@@ -645,7 +645,7 @@ constexpr int wait_vmem(int n) { return (n & 15) | (n >> 4) << 14 | 7 << 4; }
 // The sequence, head and row tile of this workgroup.  Workgroup b runs on XCD b mod 8.  An XCD takes an eighth of the heads, or with 8 / n
 // others every so-many-th tile of one of n heads, so that a head's codes meet in its L2; the longest sequences come first, and of each
 // the tiles with the most tokens.  There is no gap between the tiles of sequences of different size: workgroups without
-// work would come in patterns that leave part of an XCD idle (4 prompts of 682 to 2048 tokens: 511 us without gaps between the longest's tiles, 887 with).
+// work would come in patterns that leave part of an XCD idle (4 prompts' chunks, as above: 1.7 times as long with gaps between the longest's tiles).
 // All lanes of a wavefront take part, 64 sequences at a time.
 template <int ROWS>
 __device__ __forceinline__ bool place(const Args& a, uint32_t block, Tile& to) {

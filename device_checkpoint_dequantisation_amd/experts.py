@@ -76,7 +76,8 @@ class MoeExperts:
 
 
 def moe_route(x, router, top_k: int, score: str = "softmax", bias=None, renormalize: bool = True, scaling: float = 1.0, stream=None):
-    """The ``top_k`` experts of each row of ``x`` [..., K] and their weights: (weights fp32 [..., top_k], ids int32 [..., top_k]).
+    """The ``top_k`` experts of each row of ``x`` [..., K] and their weights: (weights fp32 [..., top_k], ids int32 [..., top_k]).  A call
+    takes fewer than 2**17 rows.
 
     Scores are softmax(x @ router.T) over the experts of ``router`` [experts, K], or its elements' logistic function ("sigmoid"); x and
     the router are bf16, fp16 or fp32, sums are 64-bit.  The experts with the largest scores are chosen, with a ``bias`` (fp32
@@ -119,7 +120,8 @@ def moe(x, experts: MoeExperts, ids, weights, activation: str | None = "silu", r
     adds nothing, one that a row has twice counts twice.  ``activation`` is one of :func:`linear`'s, ``residual`` [..., N] bf16,
     fp16 or fp32; the result has ``out_dtype`` (default x's type) or goes to ``out``, which may be ``residual`` itself.
 
-    Each chosen expert's weights are read once for up to 64 of its rows; from some hundred rows an expert on, :func:`linear` on each
+    Each chosen expert's weights are read once for up to 16 of its rows, or 64 where experts have many on average, and again, from cache or memory, for as
+    many more: a batch most of whose rows share one expert meets its weights many times.  From some hundred rows an expert on, :func:`linear` on each
     expert's rows is the faster way.  The weights' exact values enter, sums are fp32; act(gate) * up enters the down product with 16
     significant bits."""
     who = "moe"

@@ -105,7 +105,7 @@ def kv_append(cache: QuantizedKvCache, k, v, table, lengths, starts=None, max_ne
 
     A page and head has one power of two for its scale: the smallest >= amax / 448 over its finite values, but never less than
     that of tokens it holds already, whose codes are rounded to the new scale where it grows.  A value that is not finite becomes
-    the NaN code.  No two sequences may have their last page in common."""
+    the NaN code.  A page that new tokens go to belongs to one block of one sequence; pages of earlier tokens may be shared."""
     who = "kv_append"
     pages, heads, block, dim = _check_cache(cache, who)
     if dim % 32 or dim == 0 or dim > 256:
@@ -143,6 +143,7 @@ def kv_attention(q, cache: QuantizedKvCache, table, lengths, starts=None, max_ne
     their sequence and each sees the tokens up to its own, with a ``window`` the last ``window`` of them; not causal: each sees all
     ``lengths[s]`` tokens, such as an encoder's, and a sequence may have more queries than tokens.  A query that sees no token, or only scores of minus infinity, gives 0.
     Tokens that a query does not see, and what pages hold behind a sequence's end, have no part in its result.
+    A cache of no pages and a table of no blocks are refused.
     Rows that belong to no sequence (before ``starts[0]``, from ``starts[-1]`` on, behind ``max_new``) stay as they are in ``out`` and are
     0 without one.  Scores and sums are fp32; the softmax's numerators enter the second product with fp16's 11 bits, values
     exactly unless their page's scale is 2**-7 times the largest that the query sees or less, then to 2**-17 of that scale."""

@@ -660,7 +660,8 @@ typedef struct st_kv_append_args {
 /* Write the new tokens.  The scale of a block of tokens and a head is the smallest power of two >= amax / 448 over its finite
  * values (2^-127 where there is none); a block that already has tokens keeps its scale where that is larger, and where it is not
  * their codes are rounded to the new one (exact above e4m3's subnormals).  A value that is not finite becomes the NaN code and does
- * not enter amax.  Tokens of a block behind the sequence's last are left as they are.  No page may be the last one of two sequences.
+ * not enter amax.  Tokens of a block behind the sequence's last are left as they are.  A page that new
+ * tokens go to belongs to one block of one sequence (pages of earlier tokens may be shared).
  * head_dim: a multiple of 32 up to 256; block: 16, 32, 64 or 128. */
 st_status st_kv_append(const st_kv_append_args* args, void* stream);
 
@@ -688,7 +689,7 @@ typedef struct st_kv_attention_args {
  * fp32; the softmax's numerators are rounded to fp16 (11 bits) as they meet the values, which are exact down to 2^-7 times the largest v_scale that the query
  * sees in that head, and good to 2^-17 of it below.  Tokens a query does not see have no part in its result,
  * NaN codes among them.  Rows of `out` that belong to no sequence are left as they are.
- * head_dim: 64, 128 or 256; block: 16, 32, 64 or 128. */
+ * head_dim: 64, 128 or 256; block: 16, 32, 64 or 128; pages and table_blocks: 1 at least. */
 st_status st_kv_attention_workspace_bytes(const st_kv_attention_args* args, uint64_t* bytes);
 st_status st_kv_attention(const st_kv_attention_args* args, void* stream);
 /* Errors of these: ST_E_ARG (null or misaligned pointers, unknown types, scale, too little workspace), ST_E_SHAPE (head_dim, block,
@@ -711,7 +712,7 @@ typedef struct st_moe_route_args {
     int32_t* ids;
     void* workspace;         /* st_moe_route_workspace_bytes bytes, 16-byte aligned, this call's own until it is done */
     uint64_t workspace_bytes;
-    uint64_t t, k, x_pitch, router_pitch;
+    uint64_t t, k, x_pitch, router_pitch;   /* t below 2^17, k below 2^31 */
     double scaling;
     uint32_t experts, top;   /* 1 <= top <= experts <= 1024 */
     uint32_t score;          /* st_route_score */
