@@ -184,7 +184,7 @@ def kv_attention(q, cache: QuantizedKvCache, table, lengths, starts=None, max_ne
     args = KvAttentionArgs(q.data_ptr(), out.data_ptr(), cache.k.data_ptr(), cache.v.data_ptr(), cache.k_scale.data_ptr(),
                            cache.v_scale.data_ptr(), table.data_ptr(), lengths.data_ptr(),
                            None if starts is None else starts.data_ptr(), None, 0, pages, tokens, seqs, most, table.shape[1],
-                           table.stride(0), q.stride(0), q.stride(1), out.stride(0), out.stride(1), window or 0, scale, heads,
+                           table.stride(0), q.stride(0), q.stride(1), out.stride(0), out.stride(1), min(window or 0, 2 ** 31 - 1), scale, heads,
                            q.shape[1] // heads, dim, block, int(causal), _TYPE[q.dtype])
     need = C.c_uint64()
     check(lib().st_kv_attention_workspace_bytes(C.byref(args), C.byref(need)), who)
