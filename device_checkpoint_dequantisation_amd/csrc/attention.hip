@@ -502,9 +502,9 @@ __device__ __forceinline__ void attend_row(const Args& a, const Tile& tile, uint
 }
 
 // Few rows: the wavefronts of a workgroup take the steps of one row tile in turn and join in LDS, in their order.  Bound by the codes' bytes: one
-// query of 2 sequences of 131071 tokens, 8 heads of 128 and five queries each (537 MB), 112 us, 4.8 TB/s; of 48 sequences of 100 to 8192 tokens
-// (408 MB) 100 to 107 us, 4 TB/s.  3 sequences' 4 drafts, 8 heads of 64, up to 1000 tokens: 9 us, of which the launch and four dependent
-// loads (length, page, codes, scale) are most.
+// query of 2 sequences of 131071 tokens, 8 heads of 128 and five queries each (537 MB), 111 us, 4.8 TB/s; of 48 sequences of 100 to 8192 tokens
+// (408 MB) 94 to 97 us, 4.3 TB/s, whether the table holds the longest or 131072 tokens.  3 sequences' 4 drafts, 8 heads of 64, up to 1000
+// tokens: 9 us, of which the launch and four dependent loads (length, page, codes, scale) are most.
 template <bool F16, int D, int QT>
 __global__ __launch_bounds__(kThreads, D * QT <= 128 ? 2 : 1) void attend(Args a) {
     using W = Wave<F16, D, QT>;

@@ -158,3 +158,51 @@ def test_values_near_the_largest_number(dim, heads, group, count, n):
     for code in (246, 20, 3):
         _far_apart(dim, heads, group, 64, n, count, (code,), 11)
         _far_apart(dim, heads, group, 64, n, count, (code, code - 1, code - 3), 12)
+
+
+def test_far_scales_in_a_graph():
+    """Captured with pages alike, replayed with pages far apart and alike again, into part of a wide buffer; several sequences, some of
+    whose rows nobody has."""
+    dim, heads, group, block, window = 128, 2, 2, 16, 40
+    lengths, counts = [100, 0, 230, 64], [30, 2, 9, 50]
+    starts = [3]
+    for c in counts:
+        starts.append(starts[-1] + c)
+    width = -(-max(lengths) // block)
+    cache = kv.random_cache(st, 4 * width, heads, dim, block, 19)
+    table = [[s * width + b for b in range(width)] for s in range(4)]
+    tokens = starts[-1] + 4
+    q = _queries(tokens, heads * group, dim, "f16", 20)
+    wide = torch.zeros(tokens, 3 * heads * group * dim + 5, dtype=torch.float16, device=DEV)
+    part = lambda a: wide[:, a:a + heads * group * dim].unflatten(1, (heads * group, dim))   # noqa: E731
+    qd, out = part(1), part(1 + heads * group * dim + 3)
+    qd.copy_(q.to(DEV))
+    out.fill_(7.0)
+    d, tb, ln, sd = kv.to(cache, DEV), _i32(table), _i32(lengths), _i32(starts)
+
+    def step():
+        st.kv_attention(qd, d, tb, ln, starts=sd, max_new=50, window=window, out=out)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    near = kv.raw(cache.v_scale).clone()
+    far = torch.tensor([[(130, 90)[p % 2]] * heads for p in range(4 * width)], dtype=torch.uint8)
+    for codes in (near, far, near, far):
+        d.v_scale.view(torch.uint8).copy_(codes.to(DEV))
+        out.fill_(7.0)
+        g.replay()
+        torch.cuda.synchronize()
+        host = type(cache)(cache.k, cache.v, cache.k_scale, codes.view(E8M0))
+        want, tol = kv.attention(q, host, table, lengths, starts, window=window)
+        if codes is far:
+            # as in _far_apart, for queries that see a page of 2^3 (whose results are not tiny)
+            tol[starts[0]:starts[-1]] += 2.0 ** (130 - 127 - 17) * (want[starts[0]:starts[-1]].abs().amax(2, keepdim=True) > 2.0 ** -8)
+        kv.check(out[starts[0]:starts[-1]], want[starts[0]:starts[-1]], tol[starts[0]:starts[-1]])
+        assert (out[:starts[0]] == 7).all() and (out[starts[-1]:] == 7).all()
+        assert torch.equal(st.kv_attention(qd, d, tb, ln, starts=sd, max_new=50, window=window)[starts[0]:starts[-1]], out[starts[0]:starts[-1]])
+    assert (wide[:, 0] == 0).all() and (wide[:, -1] == 0).all()
