@@ -121,8 +121,8 @@ def moe(x, experts: MoeExperts, ids, weights, activation: str | None = "silu", r
     fp16 or fp32; the result has ``out_dtype`` (default x's type) or goes to ``out``, which may be ``residual`` itself.
 
     Each chosen expert's weights are read once for up to 16 of its rows, or 64 where experts have many on average, and again, from cache or memory, for as
-    many more: a batch most of whose rows share one expert meets its weights many times.  From some hundred rows an expert on, :func:`linear` on each
-    expert's rows is the faster way.  The weights' exact values enter, sums are fp32; act(gate) * up enters the down product with 16
+    many more: a batch most of whose rows share one expert meets its weights many times.  From some 300 to 500 rows an expert on,
+    :func:`linear` on each expert's rows is the faster way.  The weights' exact values enter, sums are fp32; act(gate) * up enters the down product with 16
     significant bits."""
     who = "moe"
     if not isinstance(experts, MoeExperts):
